@@ -13,17 +13,18 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
 from ._build import LIBRARY
 
 __all__ = ["QmmError", "packed_bytes", "pack", "pack_signed", "unpack", "gemv", "gemv_grouped", "gemv_lut", "gemm", "gemm_fp", "FP4_E2M1",
-           "FP8_E4M3", "FP6_E3M2", "FP6_E2M3", "FP3_E1M1", "FP5_E2M2", "FP7_E3M3", "gemm_w4a8", "gemm_wka8", "quantize",
-           "probe_read", "probe_mfma", "library_path", "SYMBOLS"]
+           "FP8_E4M3", "FP6_E3M2", "FP6_E2M3", "FP3_E1M1", "FP5_E2M2", "FP7_E3M3", "gemm_w4a8", "gemm_wka8", "quantize", "linear", "kv_append",
+           "paged_attention", "probe_read", "probe_mfma", "library_path", "SYMBOLS"]
 
 SYMBOLS = ("qmm_packed_bytes", "qmm_pack", "qmm_pack_signed", "qmm_unpack", "qmm_gemv", "qmm_gemv_grouped", "qmm_gemv_lut", "qmm_gemm", "qmm_gemm_fp", "qmm_gemm_w4a8", "qmm_gemm_wka8",
-           "qmm_quantize", "qmm_status_string", "qmm_last_error", "qmm_last_hip_error", "qmm_probe_read",
+           "qmm_quantize", "qmm_linear", "qmm_kv_append", "qmm_paged_attention", "qmm_paged_attention_workspace", "qmm_status_string", "qmm_last_error", "qmm_last_hip_error", "qmm_probe_read",
            "qmm_probe_mfma")
 
 
@@ -51,6 +52,10 @@ def _load():
         "qmm_gemm_w4a8": ([P, P, P, P, P, P, P, I64, I64, I64, I64, P], INT),
         "qmm_gemm_wka8": ([P, P, P, P, P, P, P, I64, I64, I64, INT, I64, P], INT),
         "qmm_quantize": ([P, P, P, P, I64, I64, INT, I64, P], INT),
+        "qmm_linear": ([P, P, P, P, P, I64, I64, I64, INT, I64, ctypes.c_char_p, P], INT),
+        "qmm_kv_append": ([ctypes.c_char_p, P], INT),
+        "qmm_paged_attention": ([ctypes.c_char_p, P], INT),
+        "qmm_paged_attention_workspace": ([ctypes.c_char_p], I64),
         "qmm_status_string": ([INT], ctypes.c_char_p),
         "qmm_last_error": ([], ctypes.c_char_p),
         "qmm_last_hip_error": ([], ctypes.c_char_p),
@@ -263,6 +268,205 @@ def quantize(W, bits: int, G: int, codes=None, s=None, z=None):
     _need(z, "z", torch.float16, (N, K // G), W.device)
     _check(_lib.qmm_quantize(_ptr(W), _ptr(codes), _ptr(s), _ptr(z), K, N, bits, G, _stream(W.device)))
     return codes, s, z
+
+
+# Argument structs of the calls below, laid out as include/qmm.h declares them (native alignment).
+_EPILOGUE = struct.Struct("@3Pi4x")                 # qmm_epilogue
+_APPEND = struct.Struct("@11P8q6q8q3i4x")           # qmm_kv_append_args
+_ATTENTION = struct.Struct("@11Pq4q6qq8q2qqd2i")    # qmm_attention_args
+_ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+_DTYPES = {torch.float16: 0, torch.bfloat16: 1}
+_E4M3 = torch.float8_e4m3fn
+
+
+def _at(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _raw_stream(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def linear(X, wq, s, z, bits: int, G: int, bias=None, act: str = "none", mul=None, residual=None, out=None) -> torch.Tensor:
+    """Y [M, N] fp16 = act(X [M, K] . dequant(wq) + bias) * mul + residual in one kernel, any M.
+
+    bias fp16 [N], mul and residual fp16 [M, N], each optional; act: "none", "relu", "silu", "gelu"
+    or "gelu_tanh".  The product's fp32 sums go through all of it in fp32 and are rounded once.
+    out may be mul or residual itself."""
+    if act not in _ACTS:
+        raise ValueError(f"unknown activation {act!r}: expected one of {sorted(_ACTS)}")
+    dev = X.device
+    if X.dim() != 2 or s.dim() != 2:
+        raise ValueError("X must be [M, K] and s [N, K / G]")
+    M, K = X.shape
+    N = s.shape[0]
+    if G < 1:
+        raise ValueError("G must be positive")
+    _need(X, "X", torch.float16)
+    _need(wq, "wq", torch.int32, (N, K * bits // 32), dev)
+    _need(s, "s", torch.float16, (N, K // G), dev)
+    if z is not None:
+        _need(z, "z", torch.float16, (N, K // G), dev)
+    if bias is not None:
+        _need(bias, "bias", torch.float16, (N,), dev)
+    if mul is not None:
+        _need(mul, "mul", torch.float16, (M, N), dev)
+    if residual is not None:
+        _need(residual, "residual", torch.float16, (M, N), dev)
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.float16, device=dev)
+    else:
+        _need(out, "out", torch.float16, (M, N), dev)
+    if M == 0:
+        return out
+    epi = _EPILOGUE.pack(_at(bias), _at(mul), _at(residual), _ACTS[act])
+    with torch.cuda.device(dev):
+        _check(_lib.qmm_linear(X.data_ptr(), wq.data_ptr(), s.data_ptr(), _at(z), out.data_ptr(), M, K, N, bits, G, epi,
+                               _raw_stream(dev)))
+    return out
+
+
+def _rows(t, name, dtype, device, shape=None):
+    """Strides of token and head of [tokens, heads, D] with the elements of a row side by side."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dim() != 3 or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape or '[tokens, heads, D]'}")
+    st = t.stride()
+    if st[2] != 1 and t.shape[2] > 1:
+        raise ValueError(f"{name}: the elements of a row must stand side by side")
+    return st[0], st[1]
+
+
+def _caches(k_cache, v_cache, dtype, device, k_scale, v_scale):
+    """(k strides, v strides, shape, cache type) of two caches [pages, Hkv, page, D]."""
+    got = []
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if t.dtype != dtype and t.dtype != _E4M3:
+            raise TypeError(f"{name} must be {dtype} or {_E4M3}, got {t.dtype}")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+        if t.dim() != 4:
+            raise ValueError(f"{name} must be [pages, heads, page, D]")
+        st = t.stride()
+        if st[3] != 1 and t.shape[3] > 1:
+            raise ValueError(f"{name}: the elements of a token must stand side by side")
+        got.append(st[:3])
+    if k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+        raise ValueError("k_cache and v_cache must have one shape and one type")
+    Hkv = k_cache.shape[1]
+    if k_cache.dtype == _E4M3:
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t is None:
+                raise ValueError(f"an e4m3 cache needs {name}")
+            _need(t, name, torch.float32, (Hkv,), device)
+        kind = 2
+    else:
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("k_scale and v_scale are for e4m3 caches")
+        kind = _DTYPES[dtype]
+    return got[0], got[1], k_cache.shape, kind
+
+
+def _gpu_type(q):
+    if q.dtype not in _DTYPES:
+        raise TypeError(f"q must be float16 or bfloat16, got {q.dtype}")
+    if not q.is_cuda:
+        raise ValueError("q must be a GPU tensor")
+    return q.dtype, q.device
+
+
+def kv_append(q, k, v, k_cache, v_cache, slots, positions=None, rope=None, pairs: bool = False, k_scale=None, v_scale=None, out=None):
+    """Rotary positions on q [T, Hq, D] and k [T, Hkv, D], and k and v [T, Hkv, D] into the caches
+    [pages, Hkv, page, D] (q's type, or float8_e4m3fn with fp32 scales [Hkv]).  Returns the turned q.
+
+    slots int64 [T]: page id * page + place, or -1 (padding: nothing is stored); positions int32
+    [T]: rows of rope, fp32 [rows, rot] with rot/2 cosines and then rot/2 sines (None: no rotation).
+    pairs: elements 2i and 2i + 1 turn together (False: i and i + rot/2).  q may be None (k and v
+    alone); q, k and v may be slices of one projection, out may be q."""
+    dtype, dev = _gpu_type(k if q is None else q)
+    if k.dim() != 3:
+        raise ValueError("k must be [tokens, heads, D]")
+    T, Hkv, D = k.shape
+    ks, vs = _rows(k, "k", dtype, dev), _rows(v, "v", dtype, dev, (T, Hkv, D))
+    Hq, qs, outs = 0, (0, 0), (0, 0)
+    if q is not None:
+        qs = _rows(q, "q", dtype, dev)
+        Hq = q.shape[1]
+        if q.shape[0] != T or q.shape[2] != D:
+            raise ValueError(f"q has shape {tuple(q.shape)}, expected {(T, Hq, D)}")
+        if out is None:
+            out = torch.empty((T, Hq, D), dtype=dtype, device=dev)
+        outs = _rows(out, "out", dtype, dev, (T, Hq, D))
+    elif out is not None:
+        raise ValueError("out without q")
+    kcs, vcs, shape, kind = _caches(k_cache, v_cache, dtype, dev, k_scale, v_scale)
+    if shape[1] != Hkv or shape[3] != D:
+        raise ValueError(f"k_cache has shape {tuple(shape)}, expected [pages, {Hkv}, page, {D}]")
+    _need(slots, "slots", torch.int64, (T,), dev)
+    rot = rows = 0
+    if rope is not None:
+        if positions is None:
+            raise ValueError("rope needs positions")
+        if rope.dim() != 2:
+            raise ValueError("rope must be [rows, rot]")
+        rows, rot = rope.shape
+        _need(rope, "rope", torch.float32, None, dev)
+        _need(positions, "positions", torch.int32, (T,), dev)
+    elif positions is not None:
+        raise ValueError("positions without rope")
+    args = _APPEND.pack(_at(q), k.data_ptr(), v.data_ptr(), _at(out), k_cache.data_ptr(), v_cache.data_ptr(), slots.data_ptr(),
+                        _at(positions), _at(rope), _at(k_scale), _at(v_scale), *qs, *ks, *vs, *outs, *kcs, *vcs, T, Hq, Hkv, D, rot,
+                        rows, shape[2], shape[0], _DTYPES[dtype], kind, bool(pairs))
+    with torch.cuda.device(dev):
+        _check(_lib.qmm_kv_append(args, _raw_stream(dev)))
+    return out
+
+
+def paged_attention(q, k_cache, v_cache, page_table, cu_q, kv_lens, max_q: int, max_kv: int, scale=None, window: int = 0,
+                    k_scale=None, v_scale=None, out=None, lse=None) -> torch.Tensor:
+    """Causal attention of new tokens q [T, Hq, D] over the paged caches [pages, Hkv, page, D].
+
+    page_table int32 [B, width]; cu_q int32 [B + 1]: sequence b's rows of q; kv_lens int32 [B]: its
+    keys, the new tokens' among them; max_q and max_kv: upper bounds of both (host integers: nothing
+    is read back).  scale: D ** -0.5 if None; window > 0: a row sees its last `window` keys alone;
+    lse fp32 [T, Hq] (written if given): the log of each row's sum.  A row that sees no key gives
+    zeros and -inf.  One call serves decode (one row each), chunks and whole prompts mixed."""
+    dtype, dev = _gpu_type(q)
+    qs = _rows(q, "q", dtype, dev)
+    T, Hq, D = q.shape
+    kcs, vcs, shape, kind = _caches(k_cache, v_cache, dtype, dev, k_scale, v_scale)
+    Hkv = shape[1]
+    if shape[3] != D:
+        raise ValueError(f"k_cache has shape {tuple(shape)}, expected [pages, heads, page, {D}]")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [sequences, width]")
+    B, width = page_table.shape
+    if page_table.stride(1) != 1 and width > 1:
+        raise ValueError("page_table: the ids of a sequence must stand side by side")
+    if page_table.dtype != torch.int32 or page_table.device != dev:
+        raise TypeError(f"page_table must be int32 on {dev}")
+    _need(cu_q, "cu_q", torch.int32, (B + 1,), dev)
+    _need(kv_lens, "kv_lens", torch.int32, (B,), dev)
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=dtype, device=dev)
+    outs = _rows(out, "out", dtype, dev, (T, Hq, D))
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (T, Hq), dev)
+    tail = (*qs, *outs, *kcs, *vcs, page_table.stride(0), T, B, Hq, Hkv, D, shape[2], shape[0], width, max_q, max_kv, window,
+            D ** -0.5 if scale is None else scale, _DTYPES[dtype], kind)
+    head = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), _at(lse), page_table.data_ptr(), cu_q.data_ptr(),
+            kv_lens.data_ptr(), _at(k_scale), _at(v_scale))
+    args = _ATTENTION.pack(*head, 0, 0, *tail)
+    with torch.cuda.device(dev):
+        need = _lib.qmm_paged_attention_workspace(args)
+        if need:
+            space = torch.empty(need, dtype=torch.uint8, device=dev)
+            args = _ATTENTION.pack(*head, space.data_ptr(), need, *tail)
+        _check(_lib.qmm_paged_attention(args, _raw_stream(dev)))
+    return out
 
 
 def probe_read(buf: torch.Tensor, grid: int, sink: torch.Tensor | None = None) -> None:

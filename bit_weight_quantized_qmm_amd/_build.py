@@ -16,16 +16,21 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIBRARY = os.path.join(PKG, "libqmm.so")
-SOURCES = ["abi.cpp", "pack.hip", "gemv.hip", "gemm.hip", "w4a8.hip", "quantize.hip", "probe.hip", "lut.hip"]
+# (source, object suffix, defines): the product kernels are compiled once without and once with an epilogue
+EPILOGUE = ["-DQMM_EPILOGUE"]
+SOURCES = [("gemv.hip", "", []), ("gemv.hip", ".linear", EPILOGUE), ("gemm.hip", "", []), ("gemm.hip", ".linear", EPILOGUE),
+           ("w4a8.hip", "", []), ("abi.cpp", "", []), ("pack.hip", "", []), ("quantize.hip", "", []), ("probe.hip", "", []),
+           ("lut.hip", "", []), ("append.hip", "", []), ("attend.hip", "", [])]
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 DEVICE_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-I", os.path.join(ROOT, "include")]
 
 
-def _compile(src: str) -> str:
-    obj = os.path.join(BUILD_DIR, src + ".o")
-    cmd = [HIPCC] + COMMON + DEVICE_FLAGS + ["-c", os.path.join(CSRC, src), "-o", obj]
+def _compile(item) -> str:
+    src, suffix, defines = item
+    obj = os.path.join(BUILD_DIR, src + suffix + ".o")
+    cmd = [HIPCC] + COMMON + DEVICE_FLAGS + defines + ["-c", os.path.join(CSRC, src), "-o", obj]
     if src.endswith(".hip"):
         cmd[1:1] = ["-x", "hip"]
     res = subprocess.run(cmd, capture_output=True, text=True)

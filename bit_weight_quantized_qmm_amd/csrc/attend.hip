@@ -1,0 +1,567 @@
+// attend.hip -- attention of new tokens over a paged KV cache.
+//
+//     o_i = sum_j p_ij v_j,   p_ij = exp(x_ij - max_j x_ij) / sum_j exp(..),   x_ij = scale q_i . k_j
+//
+// over the keys j that row i sees: j <= L - n + i (L keys in the sequence, n
+// of them new), and j > L - n + i - window where there is a window.  A row
+// that sees no key gives zeros and a log sum of -inf.
+//
+// One pass over the keys with a running maximum m and sum l (fp32), in base 2:
+// x is scaled by log2(e), so p is one v_exp_f32; O and l are scaled by
+// 2^(m_old - m_new) where a maximum rises.
+#include <algorithm>
+#include <math.h>
+
+#include "launch.hpp"
+#include "qmm_device.hpp"
+#include "elem.hpp"
+
+namespace qmm {
+
+typedef __bf16 bf8x_t __attribute__((ext_vector_type(8)));
+typedef __bf16 bf2x_t __attribute__((ext_vector_type(2)));
+typedef int int2v_t __attribute__((ext_vector_type(2)));
+
+constexpr uint32_t ATT_OOB = 0x80000000u;
+constexpr float ATT_LOG2E = 1.44269504088896340736f, ATT_LN2 = 0.69314718055994530942f;
+
+__device__ __forceinline__ float4_t mfma_16(int4_t a, int4_t b, float4_t c, _Float16)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, a), __builtin_bit_cast(half8_t, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ float4_t mfma_16(int4_t a, int4_t b, float4_t c, bf16_t)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8x_t, a), __builtin_bit_cast(bf8x_t, b), c, 0, 0, 0);
+}
+
+// two fp32 -> a dword of two elements, each rounded to nearest even
+__device__ __forceinline__ int pack2(float x, float y, _Float16) { return __builtin_bit_cast(int, half2_t{(_Float16)x, (_Float16)y}); }
+__device__ __forceinline__ int pack2(float x, float y, bf16_t) { return __builtin_bit_cast(int, bf2x_t{(bf16_t)x, (bf16_t)y}); }
+
+// two e4m3 (low or high half of a dword) -> two elements; exact in both types
+template <bool HI> __device__ __forceinline__ int widen(int w, _Float16)
+{
+    return __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((uint32_t)w, 1.0f, HI));
+}
+template <bool HI> __device__ __forceinline__ int widen(int w, bf16_t)
+{
+    return __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)w, 1.0f, HI));
+}
+
+// The keys of a block of rows: [lo, hi) is what any of its rows sees; start is
+// lo brought down to a multiple of 16.
+struct KeyRange {
+    int t0, n, L, lo, hi, start;
+};
+__device__ __forceinline__ KeyRange key_range(const AttendArgs &a, int b, int rb)
+{
+    KeyRange r;
+    int t0 = a.cu_q[b], n = a.cu_q[b + 1] - t0;
+    if (t0 < 0 || n < 0 || t0 + (int64_t)n > a.T) n = 0;
+    n = min(n, a.max_q);
+    r.t0 = t0;
+    r.n = n;
+    r.L = (int)min((int64_t)max(a.kv_lens[b], 0), min((int64_t)a.width * a.page, (int64_t)a.max_kv));
+    const int first = rb * a.rows / a.g, last = (min((rb + 1) * a.rows, n * a.g) - 1) / a.g;
+    r.hi = max(0, min(r.L, r.L - n + last + 1));
+    r.lo = a.window > 0 ? max(0, r.L - n + first - a.window + 1) : 0;
+    r.start = r.lo & ~15;
+    return r;
+}
+
+__device__ __forceinline__ int key_page(const AttendArgs &a, int key)
+{
+    return (int)(((uint64_t)(uint32_t)key * a.page_mul) >> a.page_sh);
+}
+
+// ---------------------------------------------------------------------------
+// Few query rows for each key head (decode, short chunks): every key is used by
+// at most 16 QT rows, so the cache's bytes bound it.  A workgroup takes one
+// (sequence, key head, block of 16 QT rows, split of the keys); its waves take
+// blocks of 32 keys in turn, each with its own running softmax, and are joined
+// in LDS at the end.  Nothing goes through LDS before: 
+//   S^T = K Q^T   the A operand of v_mfma_f32_16x16x32 is 8 consecutive elements
+//                 of one key: a 16-byte load.
+//   O^T = V^T P^T the contraction runs over keys in any order, so P leaves the
+//                 first product's accumulators (lane group g: keys 4g .. 4g+3 of
+//                 either half of the block) as the second one's B operand.  A
+//                 lane loads the same 8 keys' elements 8c .. 8c+7 (c = lane % 16)
+//                 and pairs them by v_perm_b32: tile x of the product holds rows
+//                 d = 8c + x.
+// Pages of a multiple of 16 tokens (P16): each half of a block lies in one page,
+// addressed by a buffer resource that ends at the last key of the range: what
+// lies behind it reads as zeros.  Other page sizes take a lane's key from its
+// own page; the rows' offsets are computed once for each key and handed round.
+// ---------------------------------------------------------------------------
+template <typename S, bool F8, int DP, bool P16, int QT, int NW>
+__global__ __launch_bounds__(64 * NW) void attend_rows_kernel(const AttendArgs a)
+{
+    constexpr int EB = F8 ? 1 : 2;                       // bytes of a cache element
+    constexpr int KJ = DP / 32;                          // steps of Q K^T
+    constexpr int KL = DP * EB / 64;                     // 16-byte loads of a key tile
+    constexpr int VW = DP >= 128 ? 8 : DP / 16;          // elements of a V row in one load
+    constexpr int VC = DP / (16 * VW);                   // loads of a V row
+    constexpr int VD = VW * EB / 4;                      // dwords of one
+    constexpr int XT = DP / 16;                          // O^T tiles
+    constexpr int LD = DP + 4;                           // row pitch of the join in LDS
+    extern __shared__ __attribute__((aligned(16))) float att_lds[];
+
+    int id = blockIdx.x;
+    const int split = id % a.splits;
+    id /= a.splits;
+    const int hk = id % a.Hkv;
+    id /= a.Hkv;
+    const int rb = id % a.rblocks, b = id / a.rblocks;
+
+    const KeyRange kr = key_range(a, b, rb);
+    const int nrow = min(16 * QT, kr.n * a.g - rb * a.rows);     // live rows
+    if (nrow <= 0) return;
+    const int begin = kr.start + split * a.chunk, end = min(kr.hi, begin + a.chunk);
+    if (begin >= end && split > 0) return;
+
+    const int lane = threadIdx.x & 63, wave = wave_id(), g = lane >> 4, c = lane & 15;
+    const S tag = (S)0.f;
+
+    // Q: row c of each tile, the elements of step j that the K operand has there
+    int4_t q[QT][KJ];
+    int vhi[QT], vlo[QT];      // the row's keys: [vlo, vhi)
+#pragma unroll
+    for (int qt = 0; qt < QT; ++qt) {
+        const int r = rb * a.rows + 16 * qt + c;
+        const int i = r / a.g, hq = hk * a.g + (r - i * a.g);
+        const bool live = 16 * qt + c < nrow;
+        vhi[qt] = live ? kr.L - kr.n + i + 1 : 0;
+        vlo[qt] = a.window > 0 ? vhi[qt] - a.window : 0;
+        const char *row = (const char *)a.q + (int64_t)(kr.t0 + (live ? i : 0)) * a.q_ts + (int64_t)(live ? hq : 0) * a.q_hs;
+#pragma unroll
+        for (int j = 0; j < KJ; ++j) {
+            const int d = F8 ? 64 * (j / 2) + 16 * g + 8 * (j & 1) : 32 * j + 8 * g;
+            q[qt][j] = int4_t{0, 0, 0, 0};
+            if (live && d < a.D) q[qt][j] = *reinterpret_cast<const int4_t *>(row + 2 * d);
+        }
+    }
+    // keys that every row of the block sees: [all_lo, all_hi)
+    const int all_hi = kr.L - kr.n + rb * a.rows / a.g + 1;
+    const int all_lo = a.window > 0 ? kr.hi - a.window : 0;
+
+    uint32_t koff[KL], voff[8][VC];
+#pragma unroll
+    for (int j = 0; j < KL; ++j) {
+        const uint32_t d = 64 * j + 16 * g;
+        koff[j] = d < (uint32_t)(a.D * EB) ? (P16 ? c * a.k_ts : 0u) + d : ATT_OOB;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+#pragma unroll
+        for (int x = 0; x < VC; ++x) {
+            const int d = 16 * VW * x + VW * c;
+            voff[e][x] = d < a.D ? (P16 ? (4 * g + (e & 3)) * a.v_ts : 0u) + (uint32_t)(d * EB) : ATT_OOB;
+        }
+
+    const float sl = a.scale * (F8 ? a.k_scale[hk] : 1.f) * ATT_LOG2E;
+    const char *kbase = (const char *)a.k + (int64_t)hk * a.k_hs, *vbase = (const char *)a.v + (int64_t)hk * a.v_hs;
+    const int32_t *table = a.table + (int64_t)b * a.table_s;
+
+    // page of (each half of) block blk: P16 two uniform ids, else the id of key lane % 32
+    struct Ids {
+        int p[2];
+    };
+    auto ids_of = [&](int blk) {
+        Ids r;
+        const int key = begin + 32 * blk;
+        if constexpr (P16) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int kk = __builtin_amdgcn_readfirstlane(max(0, min(key + 16 * h, end - 1)));
+                r.p[h] = end > begin ? table[key_page(a, kk)] : 0;
+            }
+        } else {
+            const int kk = max(0, min(key + (lane & 31), end - 1));
+            r.p[0] = end > begin ? table[key_page(a, kk)] : 0;
+            r.p[1] = 0;
+        }
+        return r;
+    };
+    // whether a lane's key (P16: the half) is there and its page is one
+    auto live_key = [&](int key, int pid) { return key < end && (uint32_t)pid < (uint32_t)a.pages; };
+
+    int4_t kd[2][KL];
+    int vd[8][VC][VD];
+    auto load_k = [&](int blk, const Ids &ids) {
+        const int key = begin + 32 * blk;
+        if constexpr (P16) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int kk = __builtin_amdgcn_readfirstlane(key + 16 * t), pid = __builtin_amdgcn_readfirstlane(ids.p[t]);
+                const bool ok = live_key(kk, pid);
+                const int at = ok ? kk - key_page(a, kk) * a.page : 0;
+                const int64_t off = ok ? (int64_t)pid * a.k_ps + (int64_t)at * a.k_ts : 0;
+                const uint32_t len = ok ? (uint32_t)(min(16, end - kk) - 1) * a.k_ts + (uint32_t)(a.D * EB) : 0u;
+                const __amdgpu_buffer_rsrc_t r = make_rsrc(kbase + off, len);
+#pragma unroll
+                for (int j = 0; j < KL; ++j)
+                    kd[t][j] = __builtin_bit_cast(int4_t, __builtin_amdgcn_raw_buffer_load_b128(r, koff[j], 0, 0));
+            }
+        } else {
+            const int kk = min(key + (lane & 31), end - 1), pid = live_key(kk, ids.p[0]) ? ids.p[0] : 0;
+            const int64_t off = (int64_t)pid * a.k_ps + (int64_t)(kk - key_page(a, kk) * a.page) * a.k_ts;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const uint32_t lo = (uint32_t)__shfl((int)(uint32_t)off, 16 * t + c), hi = (uint32_t)__shfl((int)(off >> 32), 16 * t + c);
+                const char *row = kbase + (int64_t)(((uint64_t)hi << 32) | lo);
+#pragma unroll
+                for (int j = 0; j < KL; ++j)
+                    kd[t][j] = *reinterpret_cast<const int4_t *>(row + (koff[j] == ATT_OOB ? 0u : koff[j]));
+            }
+        }
+    };
+    auto load_v = [&](int blk, const Ids &ids) {
+        const int key = begin + 32 * blk;
+        if constexpr (P16) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int kk = __builtin_amdgcn_readfirstlane(key + 16 * t), pid = __builtin_amdgcn_readfirstlane(ids.p[t]);
+                const bool ok = live_key(kk, pid);
+                const int at = ok ? kk - key_page(a, kk) * a.page : 0;
+                const int64_t off = ok ? (int64_t)pid * a.v_ps + (int64_t)at * a.v_ts : 0;
+                const uint32_t len = ok ? (uint32_t)(min(16, end - kk) - 1) * a.v_ts + (uint32_t)(a.D * EB) : 0u;
+                const __amdgpu_buffer_rsrc_t r = make_rsrc(vbase + off, len);
+#pragma unroll
+                for (int e = 4 * t; e < 4 * t + 4; ++e)
+#pragma unroll
+                    for (int x = 0; x < VC; ++x) {
+                        if constexpr (VD == 4) {
+                            const int4_t w = __builtin_bit_cast(int4_t, __builtin_amdgcn_raw_buffer_load_b128(r, voff[e][x], 0, 0));
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) vd[e][x][i] = w[i];
+                        } else if constexpr (VD == 2) {
+                            const int2v_t w = __builtin_bit_cast(int2v_t, __builtin_amdgcn_raw_buffer_load_b64(r, voff[e][x], 0, 0));
+                            vd[e][x][0] = w[0];
+                            vd[e][x][1] = w[1];
+                        } else {
+                            vd[e][x][0] = (int)__builtin_amdgcn_raw_buffer_load_b32(r, voff[e][x], 0, 0);
+                        }
+                    }
+            }
+        } else {
+            const int kk = min(key + (lane & 31), end - 1), pid = live_key(kk, ids.p[0]) ? ids.p[0] : 0;
+            const int64_t off = (int64_t)pid * a.v_ps + (int64_t)(kk - key_page(a, kk) * a.page) * a.v_ts;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int src = 16 * (e >> 2) + 4 * g + (e & 3);
+                const uint32_t lo = (uint32_t)__shfl((int)(uint32_t)off, src), hi = (uint32_t)__shfl((int)(off >> 32), src);
+                const char *row = vbase + (int64_t)(((uint64_t)hi << 32) | lo);
+#pragma unroll
+                for (int x = 0; x < VC; ++x) {
+                    const char *p = row + (voff[e][x] == ATT_OOB ? 0u : voff[e][x]);
+                    if constexpr (VD == 4) {
+                        const int4_t w = *reinterpret_cast<const int4_t *>(p);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) vd[e][x][i] = w[i];
+                    } else if constexpr (VD == 2) {
+                        const int2v_t w = *reinterpret_cast<const int2v_t *>(p);
+                        vd[e][x][0] = w[0];
+                        vd[e][x][1] = w[1];
+                    } else {
+                        vd[e][x][0] = *reinterpret_cast<const int *>(p);
+                    }
+                }
+            }
+        }
+    };
+
+    float m[QT], l[QT];
+    float4_t o[QT][XT];
+#pragma unroll
+    for (int qt = 0; qt < QT; ++qt) {
+        m[qt] = -INFINITY;
+        l[qt] = 0.f;
+#pragma unroll
+        for (int x = 0; x < XT; ++x) o[qt][x] = float4_t{0.f, 0.f, 0.f, 0.f};
+    }
+
+    const int blocks = (max(0, end - begin) + 31) >> 5;
+    if (wave < blocks) {
+        Ids cur = ids_of(wave), nxt = ids_of(wave + NW);
+        load_k(wave, cur);
+        load_v(wave, cur);
+        for (int blk = wave; blk < blocks; blk += NW) {
+            const int key0 = begin + 32 * blk;
+            float4_t s[QT][2];
+#pragma unroll
+            for (int qt = 0; qt < QT; ++qt)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) s[qt][t] = float4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int j = 0; j < KJ; ++j) {
+                    int4_t kf;
+                    if constexpr (F8) {
+                        const int w0 = kd[t][j / 2][2 * (j & 1)], w1 = kd[t][j / 2][2 * (j & 1) + 1];
+                        kf = int4_t{widen<false>(w0, tag), widen<true>(w0, tag), widen<false>(w1, tag), widen<true>(w1, tag)};
+                    } else {
+                        kf = kd[t][j];
+                    }
+#pragma unroll
+                    for (int qt = 0; qt < QT; ++qt) s[qt][t] = mfma_16(kf, q[qt][j], s[qt][t], tag);
+                }
+            // the next block's keys load under this block's softmax and second product
+            load_k(blk + NW, nxt);
+
+            bool bad[2];
+            if constexpr (P16) {
+#pragma unroll
+                for (int t = 0; t < 2; ++t) bad[t] = (uint32_t)cur.p[t] >= (uint32_t)a.pages;
+            } else {
+                // a bad page anywhere in the block: handled key by key below
+                bad[0] = bad[1] = __any((uint32_t)cur.p[0] >= (uint32_t)a.pages);
+            }
+            const bool masked = key0 + 32 > min(all_hi, end) || key0 < all_lo || bad[0] || bad[1];
+            if (masked) {
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int key = key0 + 16 * t + 4 * g + i;
+                        bool off = bad[t];
+                        if constexpr (!P16) off = (uint32_t)__shfl(cur.p[0], 16 * t + 4 * g + i) >= (uint32_t)a.pages;
+#pragma unroll
+                        for (int qt = 0; qt < QT; ++qt)
+                            if (off || key >= min(vhi[qt], end) || key < vlo[qt]) s[qt][t][i] = -INFINITY;
+                        // values that no row sees may hold anything: they meet p = 0 as zeros
+                        if (off || key >= end || key < kr.lo) {
+#pragma unroll
+                            for (int x = 0; x < VC; ++x)
+#pragma unroll
+                                for (int w = 0; w < VD; ++w) vd[4 * t + i][x][w] = 0;
+                        }
+                    }
+            }
+            int4_t p[QT];
+#pragma unroll
+            for (int qt = 0; qt < QT; ++qt) {
+                float x[8], mx = -INFINITY;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    x[e] = s[qt][e >> 2][e & 3] * sl;
+                    mx = fmaxf(mx, x[e]);
+                }
+                mx = fmaxf(mx, __shfl_xor(mx, 16));
+                mx = fmaxf(mx, __shfl_xor(mx, 32));
+                const float mn = fmaxf(m[qt], mx), ms = mn == -INFINITY ? 0.f : mn;
+                if (__any(mn > m[qt])) {
+                    const float al = __builtin_amdgcn_exp2f(m[qt] - ms);
+                    l[qt] *= al;
+#pragma unroll
+                    for (int xx = 0; xx < XT; ++xx) o[qt][xx] *= al;
+                    m[qt] = mn;
+                }
+                float sum = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    x[e] = __builtin_amdgcn_exp2f(x[e] - ms);
+                    sum += x[e];
+                }
+                l[qt] += sum;
+                p[qt] = int4_t{pack2(x[0], x[1], tag), pack2(x[2], x[3], tag), pack2(x[4], x[5], tag), pack2(x[6], x[7], tag)};
+            }
+#pragma unroll
+            for (int x = 0; x < VC; ++x)
+#pragma unroll
+                for (int w = 0; w < VW / 2; ++w) {
+                    // dword w of the 8 rows (elements 2w, 2w + 1): pair the rows
+                    int r[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        if constexpr (F8)
+                            r[e] = (w & 1) ? widen<true>(vd[e][x][w >> 1], tag) : widen<false>(vd[e][x][w >> 1], tag);
+                        else
+                            r[e] = vd[e][x][w];
+                    }
+                    int4_t lo, hi;
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        lo[y] = (int)__builtin_amdgcn_perm((uint32_t)r[2 * y + 1], (uint32_t)r[2 * y], 0x05040100u);
+                        hi[y] = (int)__builtin_amdgcn_perm((uint32_t)r[2 * y + 1], (uint32_t)r[2 * y], 0x07060302u);
+                    }
+#pragma unroll
+                    for (int qt = 0; qt < QT; ++qt) {
+                        o[qt][VW * x + 2 * w] = mfma_16(lo, p[qt], o[qt][VW * x + 2 * w], tag);
+                        o[qt][VW * x + 2 * w + 1] = mfma_16(hi, p[qt], o[qt][VW * x + 2 * w + 1], tag);
+                    }
+                }
+            load_v(blk + NW, nxt);
+            cur = nxt;
+            nxt = ids_of(blk + 2 * NW);
+        }
+    }
+
+    // join the waves
+    float *ml = att_lds + NW * nrow * LD;      // [wave][row][m, l]
+#pragma unroll
+    for (int qt = 0; qt < QT; ++qt) {
+        l[qt] += __shfl_xor(l[qt], 16);
+        l[qt] += __shfl_xor(l[qt], 32);
+        const int row = 16 * qt + c;
+        if (row < nrow) {
+            float *dst = att_lds + (wave * nrow + row) * LD;
+#pragma unroll
+            for (int x = 0; x < XT; x += 4)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<float4_t *>(dst + 16 * VW * (x / VW) + VW * (4 * g + i) + x % VW) =
+                        float4_t{o[qt][x][i], o[qt][x + 1][i], o[qt][x + 2][i], o[qt][x + 3][i]};
+            if (g == 0) {
+                ml[(wave * nrow + row) * 2] = m[qt];
+                ml[(wave * nrow + row) * 2 + 1] = l[qt];
+            }
+        }
+    }
+    __syncthreads();
+    const int d4 = a.D >> 2;
+    const float vs = F8 ? a.v_scale[hk] : 1.f;
+    for (int it = threadIdx.x; it < nrow * d4; it += 64 * NW) {
+        const int row = it / d4, d = 4 * (it - row * d4);
+        float mm = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) mm = fmaxf(mm, ml[(w * nrow + row) * 2]);
+        const float ms = mm == -INFINITY ? 0.f : mm;
+        float tot = 0.f;
+        float4_t sum = float4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            const float f = __builtin_amdgcn_exp2f(ml[(w * nrow + row) * 2] - ms);
+            tot += f * ml[(w * nrow + row) * 2 + 1];
+            sum += f * *reinterpret_cast<const float4_t *>(att_lds + (w * nrow + row) * LD + d);
+        }
+        const bool none = mm == -INFINITY;
+        const float inv = none ? 0.f : vs / tot;
+        const int r = rb * a.rows + row, i = r / a.g, hq = hk * a.g + (r - i * a.g);
+        const int64_t t = kr.t0 + i;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[e] = none ? 0.f : sum[e] * inv;
+        const float lse2 = none ? -INFINITY : mm + __builtin_amdgcn_logf(tot);
+        if (a.splits == 1) {
+            *reinterpret_cast<int2v_t *>((char *)a.out + t * a.o_ts + (int64_t)hq * a.o_hs + 2 * d) =
+                int2v_t{pack2(sum[0], sum[1], tag), pack2(sum[2], sum[3], tag)};
+            if (a.lse && d == 0) a.lse[t * a.Hq + hq] = lse2 * ATT_LN2;
+        } else {
+            const int64_t at = (t * a.Hq + hq) * a.splits + split;
+            *reinterpret_cast<float4_t *>(a.part + at * a.D + d) = sum;
+            if (d == 0) a.part[(int64_t)a.T * a.Hq * a.splits * a.D + at] = lse2;
+        }
+    }
+}
+
+// Joins the splits: one wave a row (token, query head).  Split s holds the
+// attention over its own keys, normalised, and the base-2 log of its sum.
+template <typename S>
+__global__ __launch_bounds__(256) void attend_join_kernel(const AttendArgs a)
+{
+    const int per = (int)(((int64_t)a.max_q * a.Hq + 3) / 4);
+    const int b = blockIdx.x / per, r = (blockIdx.x - b * per) * 4 + wave_id();
+    const int i = r / a.Hq, hq = r - i * a.Hq, lane = threadIdx.x & 63;
+    const int rb = (i * a.g + hq % a.g) / a.rows;
+    if (i >= a.max_q) return;
+    const KeyRange kr = key_range(a, b, rb);
+    if (i >= kr.n) return;
+    const int live = max(1, (max(0, kr.hi - kr.start) + a.chunk - 1) / a.chunk);
+    const int64_t row = ((int64_t)(kr.t0 + i) * a.Hq + hq);
+    const float *part = a.part + row * a.splits * a.D;
+    const float *lses = a.part + (int64_t)a.T * a.Hq * a.splits * a.D + row * a.splits;
+    float mm = -INFINITY;
+    for (int s = lane; s < live; s += 64) mm = fmaxf(mm, lses[s]);
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) mm = fmaxf(mm, __shfl_xor(mm, x));
+    const float ms = mm == -INFINITY ? 0.f : mm;
+    const int d = 4 * lane;
+    float4_t sum = float4_t{0.f, 0.f, 0.f, 0.f};
+    float tot = 0.f;
+    for (int s = 0; s < live; ++s) {
+        const float f = __builtin_amdgcn_exp2f(lses[s] - ms);
+        tot += f;
+        if (d < a.D) sum += f * *reinterpret_cast<const float4_t *>(part + (int64_t)s * a.D + d);
+    }
+    const float inv = mm == -INFINITY ? 0.f : 1.f / tot;
+    sum *= inv;
+    if (d < a.D)
+        *reinterpret_cast<int2v_t *>((char *)a.out + (int64_t)(kr.t0 + i) * a.o_ts + (int64_t)hq * a.o_hs + 2 * d) =
+            int2v_t{pack2(sum[0], sum[1], (S)0.f), pack2(sum[2], sum[3], (S)0.f)};
+    if (a.lse && lane == 0) a.lse[row] = mm == -INFINITY ? -INFINITY : (mm + __builtin_amdgcn_logf(tot)) * ATT_LN2;
+}
+
+constexpr int ROWS_NW = 4;
+
+int64_t plan_attend(AttendArgs &a, bool e4m3)
+{
+    (void)e4m3;
+    // key / page by one multiplication: with l = ceil(log2 page), mul = floor(2^(31+l) / page) + 1
+    // is exact for keys below 2^31 (mul page - 2^(31+l) <= page <= 2^l)
+    int lg = 0;
+    while ((int64_t(1) << lg) < a.page) ++lg;
+    a.page_mul = (uint32_t)((uint64_t(1) << (31 + lg)) / (uint64_t)a.page + 1);
+    a.page_sh = 31 + lg;
+
+    const int64_t rows = (int64_t)a.max_q * a.g;
+    a.rows = rows <= 16 || a.D > 128 ? 16 : 32;
+    a.rblocks = (int)((rows + a.rows - 1) / a.rows);
+    const int64_t span = a.window > 0 ? std::min<int64_t>(a.max_kv, (int64_t)a.window + (a.rows + a.g - 1) / a.g + 16) : a.max_kv;
+    const int64_t groups = (int64_t)a.B * a.Hkv * a.rblocks, unit = 32 * ROWS_NW;
+    int64_t splits = std::max<int64_t>(1, std::min((2048 + groups - 1) / groups, (span + 4 * unit - 1) / (4 * unit)));
+    a.chunk = (int)((((span + 15) + splits - 1) / splits + unit - 1) / unit * unit);
+    a.splits = (int)((span + 15 + a.chunk - 1) / a.chunk);
+    return a.splits > 1 ? (int64_t)a.T * a.Hq * a.splits * (a.D + 1) * 4 : 0;
+}
+
+template <typename S, bool F8, int DP, bool P16, int QT>
+static hipError_t rows_go(const AttendArgs &a, hipStream_t st)
+{
+    constexpr int NW = ROWS_NW;
+    static bool attr_set = false;
+    const int nrow = (int)std::min<int64_t>(16 * QT, (int64_t)a.max_q * a.g);
+    const size_t lds = (size_t)NW * nrow * (DP + 6) * 4;
+    if (!attr_set) {
+        hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&attend_rows_kernel<S, F8, DP, P16, QT, NW>),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+        if (e != hipSuccess) return e;
+        attr_set = true;
+    }
+    hipLaunchKernelGGL((attend_rows_kernel<S, F8, DP, P16, QT, NW>), dim3((unsigned)((int64_t)a.B * a.rblocks * a.Hkv * a.splits)),
+                       dim3(64 * NW), lds, st, a);
+    return hipGetLastError();
+}
+
+template <typename S, bool F8, int DP, bool P16>
+static hipError_t rows_pick(const AttendArgs &a, hipStream_t st)
+{
+    if constexpr (DP <= 128) {
+        if (a.rows == 32) return rows_go<S, F8, DP, P16, 2>(a, st);
+    }
+    return rows_go<S, F8, DP, P16, 1>(a, st);
+}
+
+template <typename S, bool F8>
+static hipError_t attend_type(const AttendArgs &a, hipStream_t st)
+{
+    hipError_t e;
+    const bool p16 = a.page % 16 == 0;
+    if (a.D <= 64)
+        e = p16 ? rows_pick<S, F8, 64, true>(a, st) : rows_pick<S, F8, 64, false>(a, st);
+    else if (a.D <= 128)
+        e = p16 ? rows_pick<S, F8, 128, true>(a, st) : rows_pick<S, F8, 128, false>(a, st);
+    else
+        e = p16 ? rows_pick<S, F8, 256, true>(a, st) : rows_pick<S, F8, 256, false>(a, st);
+    if (e != hipSuccess || a.splits == 1) return e;
+    const int64_t per = ((int64_t)a.max_q * a.Hq + 3) / 4;
+    hipLaunchKernelGGL((attend_join_kernel<S>), dim3((unsigned)(per * a.B)), dim3(256), 0, st, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_attend(const AttendArgs &a, bool bf16, bool e4m3, hipStream_t st)
+{
+    if (bf16) return e4m3 ? attend_type<bf16_t, true>(a, st) : attend_type<bf16_t, false>(a, st);
+    return e4m3 ? attend_type<_Float16, true>(a, st) : attend_type<_Float16, false>(a, st);
+}
+
+}  // namespace qmm

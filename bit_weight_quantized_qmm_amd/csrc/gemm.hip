@@ -21,8 +21,12 @@
 // run's 32; one multiply applies s (one rounding).
 #include "launch.hpp"
 #include "qmm_device.hpp"
+#include "epilogue.hpp"
 
 namespace qmm {
+#ifdef QMM_EPILOGUE
+namespace linear {
+#endif
 
 // 32 activations (natural order, two per dword) -> 16 half2 in the
 // half-slot order of RunPlan<BITS> (a permutation, no scaling).
@@ -67,7 +71,7 @@ template <int BITS, bool PGZ, int FMT, int WV, int NS, int BM, int KP>
 __global__ __launch_bounds__(64 * WV) void gemm_kernel(const uint16_t *__restrict__ X, const uint32_t *__restrict__ wq,
                                                    const uint16_t *__restrict__ s, const uint16_t *__restrict__ z,
                                                    uint16_t *__restrict__ Y, int M, int K, int N, int G, int mtiles,
-                                                   int ntiles)
+                                                   int ntiles QMM_EPI_PARAM)
 {
     using P = RunPlan<BITS>;
     constexpr int CW = WV / KP;                               // waves side by side in N per K part
@@ -288,6 +292,7 @@ __global__ __launch_bounds__(64 * WV) void gemm_kernel(const uint16_t *__restric
                 for (int ns = 0; ns < NS; ++ns) acc[ms][ns] += red[((((q - 1) * CW + cw) * MS + ms) * NS + ns) * 64 + lane];
     }
 
+#ifndef QMM_EPILOGUE
     // epilogue: lane (g, c) of MFMA tile (ms, ns) holds rows 4g..4g+3, column c.
 #pragma unroll
     for (int ms = 0; ms < MS; ++ms) {
@@ -301,6 +306,69 @@ __global__ __launch_bounds__(64 * WV) void gemm_kernel(const uint16_t *__restric
             }
         }
     }
+#else
+    // The wave's BM x 16 NS sums go through its own part of LDS, RP rows at a
+    // time, so that every lane holds 8 neighbouring columns: 16-byte loads and
+    // stores of mul, residual and Y.  (behind the K parts' sums, which other
+    // waves may still be reading)
+    constexpr int RED = (KP - 1) * CW * MS * NS * 64 * 16;
+    constexpr int ROOM = ((int)sizeof(lds) - RED) / CW / (64 * NS);       // rows that fit
+    constexpr int RP = ROOM >= BM ? BM : ROOM >= BM / 2 ? BM / 2 : BM / 4;
+    constexpr int VR = 2 * NS;                                            // vectors of 8 in a row
+    static_assert(RP >= 64 / VR && RP % (64 / VR) == 0, "whole rounds");
+    float *st = reinterpret_cast<float *>(&lds[0][0][0] + RED) + cw * RP * 16 * NS;
+    const int vr = lane / VR, vc = 8 * (lane % VR), col = wn0 + vc;
+    float bias[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) bias[e] = ep.bias && col + e < N ? (float)as_half(ep.bias[col + e]) : 0.f;
+    auto swz = [](int row) { return NS == 2 ? 8 * ((row >> 2) & 3) : 8 * ((row >> 2) & 1); };
+#pragma unroll
+    for (int r0 = 0; r0 < BM; r0 += RP) {
+#pragma unroll
+        for (int ms = 0; ms < RP / 16; ++ms)
+#pragma unroll
+            for (int ns = 0; ns < NS; ++ns)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = 16 * ms + 4 * g + i;
+                    st[row * 16 * NS + ((16 * ns + c) ^ swz(row))] = acc[r0 / 16 + ms][ns][i];
+                }
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+        for (int r = vr; r < RP; r += 64 / VR) {
+            const int row = m0 + r0 + r;
+            const float4_t *src = reinterpret_cast<const float4_t *>(st + r * 16 * NS + (vc ^ swz(r)));
+            const float4_t h0 = src[0], h1 = src[1];
+            if (row >= M || col >= N) continue;
+            const size_t at = (size_t)row * N + col;
+            if (ep.vec) {
+                half8_t mv, rv, y;
+                if (ep.mul) mv = *reinterpret_cast<const half8_t *>(ep.mul + at);
+                if (ep.residual) rv = *reinterpret_cast<const half8_t *>(ep.residual + at);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float h = activate((e < 4 ? h0[e & 3] : h1[e & 3]) + bias[e], ep.act);
+                    if (ep.mul) h *= (float)mv[e];
+                    if (ep.residual) h += (float)rv[e];
+                    y[e] = (_Float16)h;
+                }
+                *reinterpret_cast<half8_t *>(Y + at) = y;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if (col + e >= N) break;
+                    float h = activate((e < 4 ? h0[e & 3] : h1[e & 3]) + bias[e], ep.act);
+                    if (ep.mul) h *= (float)as_half(ep.mul[at + e]);
+                    if (ep.residual) h += (float)as_half(ep.residual[at + e]);
+                    Y[at + e] = f32_to_f16_bits(h);
+                }
+            }
+        }
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_wave_barrier();
+    }
+#endif
 }
 
 template <int BITS, int FMT, int WV, int NS, int BM, int KP = 1>
@@ -311,10 +379,10 @@ static hipError_t gemm_go(const GemvArgs &a, hipStream_t st)
     const dim3 block(64 * WV), grid((unsigned)(mtiles * ntiles));
     if (FMT == 0 && a.z)
         hipLaunchKernelGGL((gemm_kernel<BITS, true, FMT, WV, NS, BM, KP>), grid, block, 0, st, a.X, a.wq, a.s, a.z, a.Y, a.M,
-                           a.K, a.N, a.G, mtiles, ntiles);
+                           a.K, a.N, a.G, mtiles, ntiles QMM_EPI_ARG);
     else
         hipLaunchKernelGGL((gemm_kernel<BITS, false, FMT, WV, NS, BM, KP>), grid, block, 0, st, a.X, a.wq, a.s, a.z, a.Y, a.M,
-                           a.K, a.N, a.G, mtiles, ntiles);
+                           a.K, a.N, a.G, mtiles, ntiles QMM_EPI_ARG);
     return hipGetLastError();
 }
 
@@ -352,7 +420,14 @@ static hipError_t gemm_dispatch(const GemvArgs &a, hipStream_t st)
     return gemm_go<BITS, FMT, 8, 1, 32, 8>(a, st);
 }
 
+#ifdef QMM_EPILOGUE
+}  // namespace linear
+using namespace linear;
+
+hipError_t launch_gemm_linear(const GemvArgs &a, hipStream_t st)
+#else
 hipError_t launch_gemm(const GemvArgs &a, hipStream_t st)
+#endif
 {
     switch (a.bits) {
         case 1: return gemm_dispatch<1, 0>(a, st);
@@ -367,6 +442,7 @@ hipError_t launch_gemm(const GemvArgs &a, hipStream_t st)
     }
 }
 
+#ifndef QMM_EPILOGUE
 // Floating-point codes: fmt 0 = E2M1 (4-bit stream), 1 = E4M3 (8-bit), 2 = E3M2
 // and 3 = E2M3 (6-bit), 4 = E1M1 (3-bit), 5 = E2M2 (5-bit), 6 = E3M3 (7-bit);
 // a.bits must match, a.z is ignored.
@@ -381,5 +457,6 @@ hipError_t launch_gemm_fp(const GemvArgs &a, int fmt, hipStream_t st)
     if (fmt == 6 && a.bits == 7) return gemm_dispatch<7, 7>(a, st);
     return hipErrorInvalidValue;
 }
+#endif
 
 }  // namespace qmm

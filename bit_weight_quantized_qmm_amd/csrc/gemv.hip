@@ -9,8 +9,12 @@
 
 #include "launch.hpp"
 #include "qmm_device.hpp"
+#include "epilogue.hpp"
 
 namespace qmm {
+#ifdef QMM_EPILOGUE
+namespace linear {
+#endif
 
 // ---------------------------------------------------------------------------
 // The X side of one run: 32 activations (natural order, two per dword) ->
@@ -197,7 +201,7 @@ __device__ __forceinline__ float wave_sum_dpp(float v)
 template <int BITS, int RPL, int D, int IPT, bool PGZ, int FMT>
 __device__ __forceinline__ void m1_body(const uint16_t *__restrict__ X, const uint32_t *__restrict__ wq,
                                         const uint16_t *__restrict__ s, const uint16_t *__restrict__ z,
-                                        uint16_t *__restrict__ Y, int K, int N, int G, int wg, int nwg)
+                                        uint16_t *__restrict__ Y, int K, int N, int G, int wg, int nwg QMM_EPI_PARAM)
 {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
@@ -227,6 +231,15 @@ __device__ __forceinline__ void m1_body(const uint16_t *__restrict__ X, const ui
         const int it = tid + 256 * i;
         load_dwords<LOAD_DEFAULT>(xr, it < R ? (uint32_t)it * 64u : OOB, raw[i], 16);
     }
+#ifdef QMM_EPILOGUE
+    // the epilogue's operands of this lane's output, behind X: they arrive under
+    // the weight stream (an absent one has an empty resource and reads as zeros)
+    const uint32_t eoff = lane < ncw ? 2u * (uint32_t)(w + lane * W) : OOB;
+    const uint16_t ebias = __builtin_amdgcn_raw_buffer_load_b16(make_rsrc(ep.bias, ep.bias ? 2u * (uint32_t)N : 0u), eoff, 0, 0);
+    const uint16_t emul = __builtin_amdgcn_raw_buffer_load_b16(make_rsrc(ep.mul, ep.mul ? 2u * (uint32_t)N : 0u), eoff, 0, 0);
+    const uint16_t eres =
+        __builtin_amdgcn_raw_buffer_load_b16(make_rsrc(ep.residual, ep.residual ? 2u * (uint32_t)N : 0u), eoff, 0, 0);
+#endif
     __builtin_amdgcn_sched_barrier(0);
 
     // 2. prefetch the first D columns (weights and per-run scales)
@@ -417,15 +430,25 @@ __device__ __forceinline__ void m1_body(const uint16_t *__restrict__ X, const ui
             }
         }
     }
+#ifdef QMM_EPILOGUE
+    float h = activate(yout * __builtin_ldexpf(1.0f, -e) + (float)as_half(ebias), ep.act);
+    if (ep.mul) h *= (float)as_half(emul);
+    if (lane < ncw) Y[w + lane * W] = f32_to_f16_bits(h + (float)as_half(eres));
+#else
     if (lane < ncw) Y[w + lane * W] = f32_to_f16_bits(yout * __builtin_ldexpf(1.0f, -e));
+#endif
 }
 
 template <int BITS, int RPL, int D, int IPT, bool PGZ, int FMT = 0>
 __global__ __launch_bounds__(256) void gemv_m1_kernel(const uint16_t *__restrict__ X, const uint32_t *__restrict__ wq,
                                                       const uint16_t *__restrict__ s, const uint16_t *__restrict__ z,
-                                                      uint16_t *__restrict__ Y, int K, int N, int G)
+                                                      uint16_t *__restrict__ Y, int K, int N, int G QMM_EPI_PARAM)
 {
+#ifdef QMM_EPILOGUE
+    m1_body<BITS, RPL, D, IPT, PGZ, FMT>(X, wq, s, z, Y, K, N, G, (int)blockIdx.x, (int)gridDim.x, ep);
+#else
     m1_body<BITS, RPL, D, IPT, PGZ, FMT>(X, wq, s, z, Y, K, N, G, (int)blockIdx.x, (int)gridDim.x);
+#endif
 }
 
 // Columns in flight per wave for RPL runs per lane (the fastest measured:
@@ -434,6 +457,7 @@ __global__ __launch_bounds__(256) void gemv_m1_kernel(const uint16_t *__restrict
 __host__ __device__ constexpr int m1_depth(int bits, int rpl) { return rpl <= 1 ? 8 : rpl == 2 ? 4 : rpl == 4 ? (bits <= 2 ? 4 : 2) : 1; }
 __host__ __device__ constexpr int m1_ipt(int rpl) { return rpl == 16 ? 4 : rpl == 12 ? 3 : rpl == 8 ? 2 : 1; }
 
+#ifndef QMM_EPILOGUE
 // Several M = 1 products in one launch (qmm_gemv_grouped): workgroups
 // wg0[p] .. wg0[p + 1] - 1 serve problem p, each running the decode body above
 // for that problem's code width, so all problems stream at once over their
@@ -459,6 +483,7 @@ __global__ __launch_bounds__(256) void gemv_m1_grouped_kernel(const GroupArgs a)
     }
 #undef QMM_GB
 }
+#endif
 
 // ---------------------------------------------------------------------------
 // 2 <= M <= 16 (and M = 1 with very long K): f16 MFMA 16x16x32, M padded to 16.
@@ -475,7 +500,7 @@ template <int BITS, int T, bool PGZ>
 __global__ __launch_bounds__(512) void gemv_mfma_kernel(const uint16_t *__restrict__ X, const uint32_t *__restrict__ wq,
                                                         const uint16_t *__restrict__ s,
                                                         const uint16_t *__restrict__ z, uint16_t *__restrict__ Y,
-                                                        int M, int K, int N, int G, int passes)
+                                                        int M, int K, int N, int G, int passes QMM_EPI_PARAM)
 {
     __shared__ float red[8][256];
     const int lane = threadIdx.x & 63, wave = wave_id();
@@ -568,7 +593,12 @@ __global__ __launch_bounds__(512) void gemv_mfma_kernel(const uint16_t *__restri
             float v = 0.f;
 #pragma unroll
             for (int w = 0; w < 8; ++w) v += red[w][threadIdx.x];
+#ifdef QMM_EPILOGUE
+            if (row < M && col < nvalid)
+                Y[(size_t)row * N + tile * 16 + col] = f32_to_f16_bits(epilogue_at(ep, v, row, tile * 16 + col, N));
+#else
             if (row < M && col < nvalid) Y[(size_t)row * N + tile * 16 + col] = f32_to_f16_bits(v);
+#endif
         }
         __syncthreads();
         (void)n;
@@ -593,7 +623,7 @@ __global__ __launch_bounds__(512) void gemv_rows_kernel(const uint16_t *__restri
                                                          const uint32_t *__restrict__ wq,
                                                          const uint16_t *__restrict__ s,
                                                          const uint16_t *__restrict__ z, uint16_t *__restrict__ Y,
-                                                         int M, int K, int N, int G, int ks)
+                                                         int M, int K, int N, int G, int ks QMM_EPI_PARAM)
 {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     using P = RunPlan<BITS>;
@@ -791,7 +821,11 @@ __global__ __launch_bounds__(512) void gemv_rows_kernel(const uint16_t *__restri
         float v = 0.f;
         for (int w = 0; w < ks; ++w) v += red[(w * 4 + m) * 16 + cc];
         v *= __builtin_ldexpf(1.0f, -row_exponent(rmax[m]));
+#ifdef QMM_EPILOGUE
+        if (cc < nvalid) Y[(size_t)m * N + n0 + cc] = f32_to_f16_bits(epilogue_at(ep, v, m, n0 + cc, N));
+#else
         if (cc < nvalid) Y[(size_t)m * N + n0 + cc] = f32_to_f16_bits(v);
+#endif
     }
 }
 
@@ -830,7 +864,7 @@ constexpr int MMA_MAXNG = 64;  // groups per column and pass: 8192 rows, G >= 12
 template <int BITS, int S, int T, int D, bool PGZ, int FMT = 0, bool MP = false>
 __global__ __launch_bounds__(64 * MMA_WAVES) void gemv_mma_kernel(const uint16_t *__restrict__ X, const uint32_t *__restrict__ wq,
                                                        const uint16_t *__restrict__ s, const uint16_t *__restrict__ z,
-                                                       uint16_t *__restrict__ Y, int M, int K, int N, int G, int tpw)
+                                                       uint16_t *__restrict__ Y, int M, int K, int N, int G, int tpw QMM_EPI_PARAM)
 {
     static_assert(S % D == 0 || D % S == 0, "ring slots must stay compile-time indexes");
     __shared__ float red[MMA_WAVES][T][64][4];
@@ -1110,7 +1144,11 @@ __global__ __launch_bounds__(64 * MMA_WAVES) void gemv_mma_kernel(const uint16_t
             for (int w = 0; w < MMA_WAVES; ++w) mx = max(mx, rmx[w][m]);
             v *= __builtin_ldexpf(1.0f, -row_exponent(mx));
         }
+#ifdef QMM_EPILOGUE
+        if (m < M && n < N) Y[(size_t)m * N + n] = f32_to_f16_bits(epilogue_at(ep, v, m, n, N));
+#else
         if (m < M && n < N) Y[(size_t)m * N + n] = f32_to_f16_bits(v);
+#endif
     }
 }
 
@@ -1128,7 +1166,7 @@ static hipError_t gemv_mma_go(const GemvArgs &a, int grid, int tpw, hipStream_t 
     constexpr int D0 = MP && mma_ring(BITS) > 4 ? 4 : mma_ring(BITS);
     constexpr int D = D0 < S * T ? D0 : S * T;
     hipLaunchKernelGGL((gemv_mma_kernel<BITS, S, T, D, PGZ, FMT, MP>), dim3(grid), dim3(64 * MMA_WAVES), 0, st, a.X, a.wq, a.s, a.z, a.Y,
-                       a.M, a.K, a.N, a.G, tpw);
+                       a.M, a.K, a.N, a.G, tpw QMM_EPI_ARG);
     return hipGetLastError();
 }
 
@@ -1201,7 +1239,7 @@ static hipError_t gemv_m1_go(const GemvArgs &a, hipStream_t st)
     const size_t lds = m1_lds_bytes(RPL > 8 ? 32 * 64 * RPL : a.K, PGZ);   // RPL 16: runs staged up to 64 RPL
     const dim3 block(256), grid(m1_grid(a.N));
     hipLaunchKernelGGL((gemv_m1_kernel<BITS, RPL, D, IPT, PGZ, FMT>), grid, block, lds, st, a.X, a.wq, a.s, a.z, a.Y, a.K,
-                       a.N, a.G);
+                       a.N, a.G QMM_EPI_ARG);
     return hipGetLastError();
 }
 
@@ -1223,6 +1261,7 @@ static hipError_t gemv_m1_launch(const GemvArgs &a, hipStream_t st)
     return gemv_m1_go<BITS, 16, m1_depth(BITS, 16), m1_ipt(16), PGZ>(a, st);
 }
 
+#ifndef QMM_EPILOGUE
 // Grouped M = 1 products: the CUs are shared out in proportion to each
 // problem's estimated time, N (bits + 3): packed bytes plus a per-code share
 // for the unpack and dot products, which make the narrow codes relatively
@@ -1276,6 +1315,7 @@ hipError_t launch_gemv_grouped(const GroupArgs &in, hipStream_t st)
     if (rpl <= 4) return grouped_go<4>(ga, sum, st);
     return grouped_go<8>(ga, sum, st);
 }
+#endif
 
 template <int BITS, bool PGZ>
 static hipError_t gemv_mfma_launch(const GemvArgs &a, hipStream_t st)
@@ -1289,7 +1329,7 @@ static hipError_t gemv_mfma_launch(const GemvArgs &a, hipStream_t st)
     const dim3 block(512), grid((unsigned)min(tiles, 512));
 #define QMM_MF(TV)                                                                                              \
     hipLaunchKernelGGL((gemv_mfma_kernel<BITS, TV, PGZ>), grid, block, 0, st, a.X, a.wq, a.s, a.z, a.Y, a.M, a.K, \
-                       a.N, a.G, passes)
+                       a.N, a.G, passes QMM_EPI_ARG)
     switch (T) {
         case 1: QMM_MF(1); break;
         case 2: QMM_MF(2); break;
@@ -1324,7 +1364,7 @@ static hipError_t gemv_rows_go(const GemvArgs &a, int ks, size_t lds, hipStream_
     }
     const dim3 block(64 * ks), grid((a.N + 15) / 16);
     hipLaunchKernelGGL((gemv_rows_kernel<BITS, T, IPT, SPT, G128, PGZ>), grid, block, lds, st, a.X, a.wq, a.s, a.z,
-                       a.Y, a.M, a.K, a.N, a.G, ks);
+                       a.Y, a.M, a.K, a.N, a.G, ks QMM_EPI_ARG);
     return hipGetLastError();
 }
 
@@ -1376,6 +1416,7 @@ static hipError_t gemv_dispatch(const GemvArgs &a, hipStream_t st)
     return a.z ? gemv_mfma_launch<BITS, true>(a, st) : gemv_mfma_launch<BITS, false>(a, st);
 }
 
+#ifndef QMM_EPILOGUE
 // Floating-point codes (FMT 1: E2M1, 2: E4M3, 3: E3M2, 4: E2M3; no zero-point) at M = 1 on the
 // decode kernel and at 2 <= M <= 16 on the MFMA GEMV: hipErrorNotSupported
 // outside their shapes.
@@ -1406,8 +1447,16 @@ hipError_t launch_gemv_fp(const GemvArgs &a, int fmt, hipStream_t st)
     if (fmt == 6 && a.bits == 7) return gemv_small_fp<7, 7>(a, st);
     return hipErrorInvalidValue;
 }
+#endif
 
+#ifdef QMM_EPILOGUE
+}  // namespace linear
+using namespace linear;
+
+hipError_t launch_gemv_linear(const GemvArgs &a, hipStream_t st)
+#else
 hipError_t launch_gemv(const GemvArgs &a, hipStream_t st)
+#endif
 {
     switch (a.bits) {
         case 1: return gemv_dispatch<1>(a, st);

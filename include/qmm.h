@@ -270,6 +270,126 @@ qmm_status qmm_gemm_wka8(const int8_t *Xq, const qmm_half *sx, const uint32_t *w
 qmm_status qmm_quantize(const qmm_half *W, uint8_t *codes, qmm_half *s, qmm_half *z, int64_t K, int64_t N,
                         int bits, int64_t G, qmm_stream stream);
 
+/* ---------------------------------------------------------------------------
+ * A decoder layer around the products: a product with what follows it, the
+ * append of new keys and values to a paged cache with the rotary positions
+ * applied on the way, and attention over that cache.
+ *
+ * THE PAGED CACHE.  k_cache and v_cache hold pages x Hkv x page x D elements
+ * (page: tokens a page, any number from 1 on); the strides of page, head and
+ * token are given, the D elements of a token stand in a row.  A token's slot is
+ * page_id * page + its place in the page.  Elements are fp16 or bf16 like q, or
+ * e4m3 (OCP: largest 448, no infinity) with one fp32 scale a key head: an
+ * element stands for its e4m3 value times the scale.
+ * ------------------------------------------------------------------------- */
+
+/* element types */
+enum { QMM_F16 = 0, QMM_BF16 = 1, QMM_E4M3 = 2 };
+
+/* activations of qmm_linear: none, max(h, 0), h / (1 + exp(-h)), h Phi(h) with Phi the
+ * standard normal distribution, and h (1 + tanh(sqrt(2/pi) (h + 0.044715 h^3))) / 2 */
+enum { QMM_ACT_NONE = 0, QMM_ACT_RELU = 1, QMM_ACT_SILU = 2, QMM_ACT_GELU = 3, QMM_ACT_GELU_TANH = 4 };
+
+/* What follows the product in qmm_linear; null pointers: not there. */
+typedef struct qmm_epilogue {
+    const qmm_half *bias;       /* device, fp16 [N] */
+    const qmm_half *mul;        /* device, fp16 [M][N] */
+    const qmm_half *residual;   /* device, fp16 [M][N] */
+    int act;                    /* QMM_ACT_* */
+} qmm_epilogue;
+
+/* Y = act(X . dequant(Wq) + bias) * mul + residual for any M >= 1, in one
+ * kernel: the product of qmm_gemv (M <= 16) or qmm_gemm, with the rest computed
+ * in fp32 on its fp32 sums and rounded once to fp16.  relu takes NaN to 0.
+ *   epi    HOST struct, read during the call only; NULL: the plain product
+ * X, wq, s, z, Y, M, K, N, bits, G, stream, alignment and errors as for
+ * qmm_gemm; an unknown act gives QMM_ERR_INVALID_ARG.  Y may be mul or residual
+ * itself (every element is read before it is written), and must overlap
+ * nothing else. */
+qmm_status qmm_linear(const qmm_half *X, const uint32_t *wq, const qmm_half *s, const qmm_half *z,
+                      qmm_half *Y, int64_t M, int64_t K, int64_t N, int bits, int64_t G,
+                      const qmm_epilogue *epi, qmm_stream stream);
+
+/* Strides below are in elements. */
+typedef struct qmm_kv_append_args {
+    const void *q, *k, *v;             /* [T][Hq][D], [T][Hkv][D], [T][Hkv][D] (read); q NULL with Hq 0 */
+    void *out;                         /* [T][Hq][D]: q with its positions (written); may be q itself */
+    void *k_cache, *v_cache;           /* written at the tokens' slots alone */
+    const int64_t *slots;              /* [T]; one outside 0 .. pages * page - 1 (as -1, padding): nothing is
+                                          stored for the token.  Two tokens of a call must not share one. */
+    const int32_t *positions;          /* [T]: row of the table (brought into 0 .. table_rows - 1) */
+    const float *rope;                 /* [table_rows][rot]: rot/2 cosines, then rot/2 sines */
+    const float *k_scale, *v_scale;    /* [Hkv], e4m3 caches only */
+    int64_t q_stride[2], k_stride[2], v_stride[2], out_stride[2];   /* token, head */
+    int64_t k_cache_stride[3], v_cache_stride[3];                   /* page, head, token */
+    int64_t T, Hq, Hkv, D, rot, table_rows, page, pages;
+    int32_t dtype;                     /* QMM_F16 or QMM_BF16: q, k, v and out */
+    int32_t cache_dtype;               /* dtype's, or QMM_E4M3 */
+    int32_t pairs;                     /* 0: element i turns with i + rot/2; 1: 2i with 2i + 1 */
+} qmm_kv_append_args;
+
+/* Rotary positions and the append: for every token and head of q and k, each
+ * pair (a, b) of the first rot elements becomes (a cos - b sin, b cos + a sin),
+ * elements rot .. D-1 stay; q goes to out, k and v to the caches (e4m3: x /
+ * scale, saturated at +-448, to nearest even).  fp32 arithmetic, rounded once.
+ *   args   HOST struct, read during the call only
+ * rot may be 0 (no rotation: positions and rope NULL).  T = 0 does nothing.
+ * Errors: QMM_ERR_INVALID_ARG for null pointers, D odd or < 2, rot odd or
+ * outside 0..D, sizes < 1, unknown types; QMM_ERR_UNSUPPORTED for pages * page
+ * or T * D at 2^31 and beyond, or more than 65535 heads.  Rows whose starts and
+ * strides are multiples of 16 bytes, with rot and D - rot multiples of 16, move
+ * fastest. */
+qmm_status qmm_kv_append(const qmm_kv_append_args *args, qmm_stream stream);
+
+typedef struct qmm_attention_args {
+    const void *q;                     /* [T][Hq][D] */
+    const void *k_cache, *v_cache;
+    void *out;                         /* [T][Hq][D] (written) */
+    float *lse;                        /* [T][Hq] or NULL: natural log of sum_j exp(x_ij) (written) */
+    const int32_t *page_table;         /* [B][width]: page ids of each sequence, in order */
+    const int32_t *cu_q;               /* [B+1]: sequence b's new tokens are rows cu_q[b] .. cu_q[b+1] - 1 of q */
+    const int32_t *kv_lens;            /* [B]: keys of each sequence, the new tokens' among them */
+    const float *k_scale, *v_scale;    /* [Hkv], e4m3 caches only */
+    void *workspace;                   /* 16-byte aligned; may be NULL where none is needed */
+    int64_t workspace_bytes;
+    int64_t q_stride[2], out_stride[2];                             /* token, head */
+    int64_t k_cache_stride[3], v_cache_stride[3];                   /* page, head, token */
+    int64_t table_stride;              /* of a sequence's row */
+    int64_t T, B, Hq, Hkv, D, page, pages, width;
+    int64_t max_q, max_kv;             /* upper bounds of the sequences' new tokens and keys */
+    int64_t window;                    /* > 0: a row sees its last `window` keys alone; 0: no window */
+    double scale;                      /* finite, >= 0 */
+    int32_t dtype;                     /* QMM_F16 or QMM_BF16: q and out */
+    int32_t cache_dtype;               /* dtype's, or QMM_E4M3 */
+} qmm_attention_args;
+
+/* Causal attention of new tokens over the paged cache: row i of a sequence's n
+ * new tokens stands at position kv_len - n + i and sees the keys up to it
+ *     out_i = sum_j softmax_j(scale q_i . k_j) v_j,
+ * query head h reading key head h / (Hq / Hkv).  n = 1 is decode, n = kv_len a
+ * whole prompt.  A row that sees no key (kv_len 0, or below n) gives zeros and
+ * an lse of -inf.  What stands in the caches behind a sequence's last key, or
+ * before every row's window, takes no part whatever it holds; a page id outside
+ * 0 .. pages - 1 hides the keys of that page.  Keys and values that some row of
+ * the sequence sees must be finite.  Products on f16 / bf16 MFMA with fp32 sums,
+ * softmax in fp32, probabilities rounded once to q's type for the second
+ * product.  Rows of q that no sequence has are left alone in out and lse.
+ *   args   HOST struct, read during the call only
+ * The workspace (scratch during the call: one for each stream that has calls in
+ * flight) needs qmm_paged_attention_workspace() bytes; no call depends on what
+ * is in it.  The same inputs give the same bits.  T = 0 or B = 0 does nothing.
+ * Errors: QMM_ERR_INVALID_ARG for null pointers, Hq not a multiple of Hkv,
+ * negative or zero sizes, a bad scale or window, unknown types, a workspace too
+ * small, starts or strides that are no multiples of 16 bytes;
+ * QMM_ERR_UNSUPPORTED for D not a multiple of 16 in 16..256, or sizes beyond
+ * 32-bit indexes (T * max(1, splits), keys, grid). */
+qmm_status qmm_paged_attention(const qmm_attention_args *args, qmm_stream stream);
+
+/* Bytes of workspace that qmm_paged_attention takes for these arguments (from
+ * the sizes alone: no pointer is read but args), 0 if none or if they are not
+ * valid. */
+int64_t qmm_paged_attention_workspace(const qmm_attention_args *args);
+
 /* Static text for a status code. */
 const char *qmm_status_string(qmm_status status);
 
