@@ -74,6 +74,13 @@ __device__ __forceinline__ int key_page(const AttendArgs &a, int key)
     return (int)(((uint64_t)(uint32_t)key * a.page_mul) >> a.page_sh);
 }
 
+// What turns a product into a base-2 exponent.  Never zero: a hidden key's -inf
+// stays -inf under it (a scale of 0 still gives every key the same weight).
+__device__ __forceinline__ float score_scale(const AttendArgs &a, bool f8, int hk)
+{
+    return fmaxf(a.scale * (f8 ? a.k_scale[hk] : 1.f) * ATT_LOG2E, 1e-37f);
+}
+
 // ---------------------------------------------------------------------------
 // Few query rows for each key head (decode, short chunks): every key is used by
 // at most 16 QT rows, so the cache's bytes bound it.  A workgroup takes one
@@ -158,7 +165,7 @@ __global__ __launch_bounds__(64 * NW) void attend_rows_kernel(const AttendArgs a
             voff[e][x] = d < a.D ? (P16 ? (4 * g + (e & 3)) * a.v_ts : 0u) + (uint32_t)(d * EB) : ATT_OOB;
         }
 
-    const float sl = a.scale * (F8 ? a.k_scale[hk] : 1.f) * ATT_LOG2E;
+    const float sl = score_scale(a, F8, hk);
     const char *kbase = (const char *)a.k + (int64_t)hk * a.k_hs, *vbase = (const char *)a.v + (int64_t)hk * a.v_hs;
     const int32_t *table = a.table + (int64_t)b * a.table_s;
 
@@ -454,6 +461,285 @@ __global__ __launch_bounds__(64 * NW) void attend_rows_kernel(const AttendArgs a
     }
 }
 
+// ---------------------------------------------------------------------------
+// Many query rows for each key head (prompts, chunks): bound by the MFMA, with
+// the softmax's VALU work beside it.  A workgroup of NW waves takes 32 NW rows
+// of one (sequence, key head) and one split of the keys; the waves share tiles
+// of 64 keys and values in LDS (double-buffered, one barrier a tile), each with
+// its own 32 rows: Q^T as B operands, O^T and the statistics in registers.
+//   S^T = K Q^T (32x32x16): the A operand is 8 consecutive elements of a key.
+//   O^T = V^T P^T: as in the rows kernel the contraction takes the keys in the
+//   order in which the first product leaves them (slot (h, e) of step u is key
+//   16 u + 8 (e / 4) + 4 h + e % 4), so P goes from accumulators to B operand
+//   in registers; the A operand comes from ds_read_b64_tr_b16, which hands 16
+//   lanes the columns of a 4 x 16 block of V rows.
+// Rows in LDS are DP elements without padding; their 16-byte chunks are XOR-ed
+// with key % 8 (K: 8 lanes read one chunk of 8 keys) or 2 (key % 4) (V: 16 lanes
+// read two chunks of 4 keys), which spreads every such group over all banks.
+// The maximum is raised only when a tile's exceeds it by more than 2^8: p then
+// stays below 2^8, O and l are rarely scaled, and nothing else changes.
+// ---------------------------------------------------------------------------
+typedef float float16v_t __attribute__((ext_vector_type(16)));
+typedef short short4v_t __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ float16v_t mfma_32(int4_t a, int4_t b, float16v_t c, _Float16)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, a), __builtin_bit_cast(half8_t, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ float16v_t mfma_32(int4_t a, int4_t b, float16v_t c, bf16_t)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8x_t, a), __builtin_bit_cast(bf8x_t, b), c, 0, 0, 0);
+}
+
+constexpr int ATT_KB = 64;             // keys of a tile
+constexpr float ATT_LAZY = 8.f;        // a maximum may be exceeded by this much (base 2)
+
+template <typename S, bool F8, int DP, bool P16, int NW>
+__global__ __launch_bounds__(64 * NW) void attend_tiles_kernel(const AttendArgs a)
+{
+    constexpr int EB = F8 ? 1 : 2;
+    constexpr int CH = DP / 8;                           // 16-byte chunks of a row in LDS
+    constexpr int LN = ATT_KB * CH / (64 * NW);          // chunks of K (and of V) a thread stages
+    constexpr int RW = 64 / CH;                          // rows that a wave stages at once
+    constexpr int QJ = DP / 16, XT = DP / 32;
+    constexpr int TILE = ATT_KB * DP * 2;                // bytes
+    static_assert(RW <= 16 && 16 % RW == 0, "a wave's rows lie in one half of 16 keys");
+    extern __shared__ __attribute__((aligned(16))) uint8_t att_tiles[];   // K [2][TILE], V [2][TILE]
+    typedef __attribute__((address_space(3))) short4v_t lds4_t;
+
+    int id = blockIdx.x;
+    const int groups = a.B * a.Hkv;
+    const int bh = id % groups;                          // sequence and head fastest: one head's blocks share an L2
+    id /= groups;
+    const int split = id % a.splits, rb = a.rblocks - 1 - id / a.splits;   // the longest blocks first
+    const int b = bh / a.Hkv, hk = bh - b * a.Hkv;
+
+    const KeyRange kr = key_range(a, b, rb);
+    const int nrow = min(32 * NW, kr.n * a.g - rb * a.rows);
+    if (nrow <= 0) return;
+    const int begin = kr.start + split * a.chunk, end = min(kr.hi, begin + a.chunk);
+    if (begin >= end && split > 0) return;
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = wave_id(), c = lane & 31, h = lane >> 5;
+    const S tag = (S)0.f;
+
+    // this lane's row
+    const int r = rb * a.rows + 32 * wave + c, i = r / a.g, hq = hk * a.g + (r - i * a.g);
+    const bool live = 32 * wave + c < nrow;
+    const int vhi = live ? kr.L - kr.n + i + 1 : 0, vlo = a.window > 0 ? vhi - a.window : 0;
+    int4_t q[QJ];
+    {
+        const char *row = (const char *)a.q + (int64_t)(kr.t0 + (live ? i : 0)) * a.q_ts + (int64_t)(live ? hq : 0) * a.q_hs;
+#pragma unroll
+        for (int j = 0; j < QJ; ++j) {
+            const int d = 16 * j + 8 * h;
+            q[j] = int4_t{0, 0, 0, 0};
+            if (live && d < a.D) q[j] = *reinterpret_cast<const int4_t *>(row + 2 * d);
+        }
+    }
+    // keys that some row of the wave sees, and keys that all of them see
+    const int wr0 = rb * a.rows + 32 * wave, wr1 = min(wr0 + 31, rb * a.rows + nrow - 1);
+    const bool wlive = 32 * wave < nrow;
+    const int whi = wlive ? kr.L - kr.n + wr1 / a.g + 1 : 0, wall_hi = wlive ? kr.L - kr.n + wr0 / a.g + 1 : 0;
+    const int wlo = a.window > 0 ? wall_hi - a.window : 0, wall_lo = a.window > 0 ? whi - a.window : 0;
+
+    const float sl = score_scale(a, F8, hk);
+    const char *kbase = (const char *)a.k + (int64_t)hk * a.k_hs, *vbase = (const char *)a.v + (int64_t)hk * a.v_hs;
+    const int32_t *table = a.table + (int64_t)b * a.table_s;
+
+    // page id of the tile's key number `lane`
+    auto ids_of = [&](int tile) {
+        const int kk = max(0, min(begin + ATT_KB * tile + lane, end - 1));
+        return end > begin ? table[key_page(a, kk)] : 0;
+    };
+    // the pieces that this thread stages: row srow + (64 NW / CH) n, chunk sp
+    const int srow = tid / CH, sp = tid % CH;
+    constexpr int SSTEP = 64 * NW / CH;
+    constexpr int PD = EB * 2;                            // dwords of a piece
+    const bool in_d = 8 * sp < a.D;
+    int kst[LN][PD], vst[LN][PD];
+    auto load_piece = [&](const char *base, int64_t ps, uint32_t ts, int key0, int pid, int n, int first, int (&dst)[PD]) {
+        const int key = key0 + srow + SSTEP * n;
+        if constexpr (P16) {
+            const int row0 = (wave * 64) / CH + SSTEP * n;                 // uniform
+            const int kk = key0 + row0, pg = __builtin_amdgcn_readlane(pid, row0 & ~15);
+            const bool ok = kk < end && (uint32_t)pg < (uint32_t)a.pages;
+            const int at = ok ? kk - key_page(a, kk) * a.page : 0;
+            const int64_t off = ok ? (int64_t)pg * ps + (int64_t)at * ts : 0;
+            const uint32_t len = ok ? (uint32_t)(min(RW, end - kk) - 1) * ts + (uint32_t)(a.D * EB) : 0u;
+            const __amdgpu_buffer_rsrc_t rs = make_rsrc(base + off, len);
+            const uint32_t vo = in_d && key >= first ? (uint32_t)(key - kk) * ts + (uint32_t)(8 * EB * sp) : ATT_OOB;
+            if constexpr (PD == 4) {
+                const int4_t w = __builtin_bit_cast(int4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, vo, 0, 0));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dst[e] = w[e];
+            } else {
+                const int2v_t w = __builtin_bit_cast(int2v_t, __builtin_amdgcn_raw_buffer_load_b64(rs, vo, 0, 0));
+                dst[0] = w[0];
+                dst[1] = w[1];
+            }
+        } else {
+            const int pg = __shfl(pid, srow + SSTEP * n);
+            const bool ok = key < end && key >= first && (uint32_t)pg < (uint32_t)a.pages && in_d;
+            const int64_t off = ok ? (int64_t)pg * ps + (int64_t)(key - key_page(a, key) * a.page) * ts + 8 * EB * sp : 0;
+            if constexpr (PD == 4) {
+                int4_t w = int4_t{0, 0, 0, 0};
+                if (ok) w = *reinterpret_cast<const int4_t *>(base + off);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dst[e] = w[e];
+            } else {
+                int2v_t w = int2v_t{0, 0};
+                if (ok) w = *reinterpret_cast<const int2v_t *>(base + off);
+                dst[0] = w[0];
+                dst[1] = w[1];
+            }
+        }
+    };
+    auto load_tile = [&](int tile, int pid) {
+        const int key0 = begin + ATT_KB * tile;
+#pragma unroll
+        for (int n = 0; n < LN; ++n) load_piece(kbase, a.k_ps, a.k_ts, key0, pid, n, 0, kst[n]);
+#pragma unroll
+        for (int n = 0; n < LN; ++n) load_piece(vbase, a.v_ps, a.v_ts, key0, pid, n, kr.lo, vst[n]);
+    };
+    auto store_tile = [&](int buf) {
+        auto put = [&](const int (&w)[PD], uint8_t *dst) {
+            if constexpr (F8)
+                *reinterpret_cast<int4_t *>(dst) = int4_t{widen<false>(w[0], tag), widen<true>(w[0], tag), widen<false>(w[1], tag), widen<true>(w[1], tag)};
+            else
+                *reinterpret_cast<int4_t *>(dst) = int4_t{w[0], w[1], w[2], w[3]};
+        };
+#pragma unroll
+        for (int n = 0; n < LN; ++n) {
+            const int row = srow + SSTEP * n;
+            put(kst[n], att_tiles + buf * TILE + row * DP * 2 + 16 * (sp ^ (row & 7)));
+            put(vst[n], att_tiles + (2 + buf) * TILE + row * DP * 2 + 16 * (sp ^ (2 * (row & 3))));
+        }
+    };
+
+    // LDS addresses of this lane's operands: K row c, chunk (2 j + h) ^ (c % 8), j % 4 apart;
+    // V block: rows lane % 16 / 4 and 4 h, columns 16 (lane / 16 % 2) + 4 (lane % 4), steps of x by 2 apart
+    uint32_t ka[4], va[2];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) ka[j] = (uint32_t)(c * DP * 2 + 16 * ((2 * j + h) ^ (c & 7)));
+    {
+        const int l16 = lane & 15, row = 4 * h + (l16 >> 2), sw = 2 * (row & 3);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int chunk = (4 * x + 2 * ((lane >> 4) & 1) + ((l16 & 3) >> 1)) ^ sw;
+            va[x] = (uint32_t)(2 * TILE + row * DP * 2 + 16 * chunk + 8 * (l16 & 1));
+        }
+    }
+
+    float m = -INFINITY, l = 0.f;
+    float16v_t o[XT];
+#pragma unroll
+    for (int x = 0; x < XT; ++x)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[x][e] = 0.f;
+
+    const int tiles = (max(0, end - begin) + ATT_KB - 1) / ATT_KB;
+    int pid = ids_of(0), pid1 = ids_of(1);
+    load_tile(0, pid);
+    store_tile(0);
+    __syncthreads();
+    for (int tile = 0; tile < tiles; ++tile) {
+        const int buf = tile & 1, key0 = begin + ATT_KB * tile;
+        const uint64_t bad = __ballot((uint32_t)pid >= (uint32_t)a.pages);
+        pid = pid1;
+        load_tile(tile + 1, pid);
+        pid1 = ids_of(tile + 2);
+        if (key0 < whi && key0 + ATT_KB > wlo) {
+            const uint8_t *kl = att_tiles + buf * TILE;
+            float16v_t s[2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) s[t][e] = 0.f;
+#pragma unroll
+                for (int j = 0; j < QJ; ++j) {
+                    const int4_t kf = *reinterpret_cast<const int4_t *>(kl + ka[j & 3] + 128 * (j >> 2) + t * 32 * DP * 2);
+                    s[t] = mfma_32(kf, q[j], s[t], tag);
+                }
+            }
+            if (key0 + ATT_KB > min(wall_hi, end) || key0 < wall_lo || bad) {
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int kt = 32 * t + (e & 3) + 8 * (e >> 2) + 4 * h, key = key0 + kt;
+                        if (key >= min(vhi, end) || key < vlo || ((bad >> kt) & 1)) s[t][e] = -INFINITY;
+                    }
+            }
+            float mx = s[0][0];
+#pragma unroll
+            for (int e = 1; e < 32; ++e) mx = fmaxf(mx, s[e >> 4][e & 15]);
+            mx = fmaxf(mx, __shfl_xor(mx, 32));
+            mx *= sl;
+            if (__any(mx > m + ATT_LAZY)) {              // also the first finite maximum: m is -inf
+                const float mn = fmaxf(m, mx), al = __builtin_amdgcn_exp2f(m - (mn == -INFINITY ? 0.f : mn));
+                l *= al;
+#pragma unroll
+                for (int x = 0; x < XT; ++x) o[x] *= al;
+                m = mn;
+            }
+            const float ms = m == -INFINITY ? 0.f : m;
+            float sum = 0.f;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+                const float p = __builtin_amdgcn_exp2f(fmaf(s[e >> 4][e & 15], sl, -ms));
+                sum += p;
+                s[e >> 4][e & 15] = p;
+            }
+            l += sum;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                int4_t p;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) p[e] = pack2(s[u >> 1][8 * (u & 1) + 2 * e], s[u >> 1][8 * (u & 1) + 2 * e + 1], tag);
+#pragma unroll
+                for (int x = 0; x < XT; ++x) {
+                    const uint32_t at = va[x & 1] + buf * TILE + 128 * (x >> 1) + u * 16 * DP * 2;
+                    const short4v_t v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4_t *)(att_tiles + at));
+                    const short4v_t v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4_t *)(att_tiles + at + 8 * DP * 2));
+                    const int2v_t w0 = __builtin_bit_cast(int2v_t, v0), w1 = __builtin_bit_cast(int2v_t, v1);
+                    o[x] = mfma_32(int4_t{w0[0], w0[1], w1[0], w1[1]}, p, o[x], tag);
+                }
+            }
+        }
+        store_tile(buf ^ 1);
+        __syncthreads();
+    }
+
+    l += __shfl_xor(l, 32);
+    if (!live) return;
+    const bool none = m == -INFINITY;
+    const float inv = none ? 0.f : (F8 ? a.v_scale[hk] : 1.f) / l;
+    const float lse2 = none ? -INFINITY : m + __builtin_amdgcn_logf(l);
+    const int64_t t = kr.t0 + i, at = (t * a.Hq + hq) * a.splits + split;
+    char *out = (char *)a.out + t * a.o_ts + (int64_t)hq * a.o_hs;
+#pragma unroll
+    for (int x = 0; x < XT; ++x)
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+            const int d = 32 * x + 2 * e + 4 * h;
+            if (d >= a.D) continue;
+            float4_t y;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] = none ? 0.f : o[x][e + k] * inv;
+            if (a.splits == 1)
+                *reinterpret_cast<int2v_t *>(out + 2 * d) = int2v_t{pack2(y[0], y[1], tag), pack2(y[2], y[3], tag)};
+            else
+                *reinterpret_cast<float4_t *>(a.part + at * a.D + d) = y;
+        }
+    if (h == 0) {
+        if (a.splits > 1)
+            a.part[(int64_t)a.T * a.Hq * a.splits * a.D + at] = lse2;
+        else if (a.lse)
+            a.lse[t * a.Hq + hq] = lse2 * ATT_LN2;
+    }
+}
+
 // Joins the splits: one wave a row (token, query head).  Split s holds the
 // attention over its own keys, normalised, and the base-2 log of its sum.
 template <typename S>
@@ -492,6 +778,9 @@ __global__ __launch_bounds__(256) void attend_join_kernel(const AttendArgs a)
 }
 
 constexpr int ROWS_NW = 4;
+// waves of a tiles workgroup: two a SIMD up to D = 128 (256 registers each), one
+// beyond (O^T and Q^T alone take 192)
+__host__ __device__ constexpr int tiles_waves(int D) { return D <= 128 ? 8 : 4; }
 
 int64_t plan_attend(AttendArgs &a, bool e4m3)
 {
@@ -504,14 +793,33 @@ int64_t plan_attend(AttendArgs &a, bool e4m3)
     a.page_sh = 31 + lg;
 
     const int64_t rows = (int64_t)a.max_q * a.g;
-    a.rows = rows <= 16 || a.D > 128 ? 16 : 32;
+    const bool tiles = rows > 32;
+    a.rows = tiles ? 32 * tiles_waves(a.D) : rows <= 16 || a.D > 128 ? 16 : 32;
     a.rblocks = (int)((rows + a.rows - 1) / a.rows);
     const int64_t span = a.window > 0 ? std::min<int64_t>(a.max_kv, (int64_t)a.window + (a.rows + a.g - 1) / a.g + 16) : a.max_kv;
-    const int64_t groups = (int64_t)a.B * a.Hkv * a.rblocks, unit = 32 * ROWS_NW;
-    int64_t splits = std::max<int64_t>(1, std::min((2048 + groups - 1) / groups, (span + 4 * unit - 1) / (4 * unit)));
+    const int64_t groups = (int64_t)a.B * a.Hkv * a.rblocks, unit = tiles ? 512 : 32 * ROWS_NW;
+    const int64_t want = tiles ? 1024 : 2048;
+    int64_t splits = std::max<int64_t>(1, std::min((want + groups - 1) / groups, (span + 4 * unit - 1) / (4 * unit)));
     a.chunk = (int)((((span + 15) + splits - 1) / splits + unit - 1) / unit * unit);
     a.splits = (int)((span + 15 + a.chunk - 1) / a.chunk);
     return a.splits > 1 ? (int64_t)a.T * a.Hq * a.splits * (a.D + 1) * 4 : 0;
+}
+
+template <typename S, bool F8, int DP, bool P16>
+static hipError_t tiles_go(const AttendArgs &a, hipStream_t st)
+{
+    constexpr int NW = tiles_waves(DP);
+    static bool attr_set = false;
+    const size_t lds = (size_t)4 * ATT_KB * DP * 2;
+    if (!attr_set) {
+        hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&attend_tiles_kernel<S, F8, DP, P16, NW>),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+        if (e != hipSuccess) return e;
+        attr_set = true;
+    }
+    hipLaunchKernelGGL((attend_tiles_kernel<S, F8, DP, P16, NW>), dim3((unsigned)((int64_t)a.B * a.rblocks * a.Hkv * a.splits)),
+                       dim3(64 * NW), lds, st, a);
+    return hipGetLastError();
 }
 
 template <typename S, bool F8, int DP, bool P16, int QT>
@@ -535,6 +843,7 @@ static hipError_t rows_go(const AttendArgs &a, hipStream_t st)
 template <typename S, bool F8, int DP, bool P16>
 static hipError_t rows_pick(const AttendArgs &a, hipStream_t st)
 {
+    if (a.rows > 32) return tiles_go<S, F8, DP, P16>(a, st);
     if constexpr (DP <= 128) {
         if (a.rows == 32) return rows_go<S, F8, DP, P16, 2>(a, st);
     }
