@@ -52,7 +52,7 @@ def _load():
         "qmm_gemm_w4a8": ([P, P, P, P, P, P, P, I64, I64, I64, I64, P], INT),
         "qmm_gemm_wka8": ([P, P, P, P, P, P, P, I64, I64, I64, INT, I64, P], INT),
         "qmm_quantize": ([P, P, P, P, I64, I64, INT, I64, P], INT),
-        "qmm_linear": ([P, P, P, P, P, I64, I64, I64, INT, I64, ctypes.c_char_p, P], INT),
+        "qmm_linear": ([ctypes.c_char_p, P], INT),
         "qmm_kv_append": ([ctypes.c_char_p, P], INT),
         "qmm_paged_attention": ([ctypes.c_char_p, P], INT),
         "qmm_paged_attention_workspace": ([ctypes.c_char_p], I64),
@@ -271,7 +271,7 @@ def quantize(W, bits: int, G: int, codes=None, s=None, z=None):
 
 
 # Argument structs of the calls below, laid out as include/qmm.h declares them (native alignment).
-_EPILOGUE = struct.Struct("@3Pi4x")                 # qmm_epilogue
+_LINEAR = struct.Struct("@8P4q2i")                   # qmm_linear_args
 _APPEND = struct.Struct("@11P8q6q8q3i4x")           # qmm_kv_append_args
 _ATTENTION = struct.Struct("@11Pq4q6qq8q2qqd2i")    # qmm_attention_args
 _ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
@@ -283,8 +283,22 @@ def _at(t):
     return 0 if t is None else t.data_ptr()
 
 
-def _raw_stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
+def _call(fn, args, index):
+    """fn(args, the device's current stream) with that device current."""
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if index == torch._C._cuda_getDevice():
+        status = fn(args, stream)
+    else:
+        with torch.cuda.device(index):
+            status = fn(args, stream)
+    if status:
+        _check(status)
+
+
+def _expect(t, name, dtype, shape, index):
+    """_need for a shape and a device index; the usual case costs four attribute reads."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        _need(t, name, dtype, shape, torch.device("cuda", index))
 
 
 def linear(X, wq, s, z, bits: int, G: int, bias=None, act: str = "none", mul=None, residual=None, out=None) -> torch.Tensor:
@@ -293,89 +307,88 @@ def linear(X, wq, s, z, bits: int, G: int, bias=None, act: str = "none", mul=Non
     bias fp16 [N], mul and residual fp16 [M, N], each optional; act: "none", "relu", "silu", "gelu"
     or "gelu_tanh".  The product's fp32 sums go through all of it in fp32 and are rounded once.
     out may be mul or residual itself."""
-    if act not in _ACTS:
+    code = _ACTS.get(act)
+    if code is None:
         raise ValueError(f"unknown activation {act!r}: expected one of {sorted(_ACTS)}")
-    dev = X.device
     if X.dim() != 2 or s.dim() != 2:
         raise ValueError("X must be [M, K] and s [N, K / G]")
-    M, K = X.shape
-    N = s.shape[0]
     if G < 1:
         raise ValueError("G must be positive")
-    _need(X, "X", torch.float16)
-    _need(wq, "wq", torch.int32, (N, K * bits // 32), dev)
-    _need(s, "s", torch.float16, (N, K // G), dev)
+    M, K = X.shape
+    N = s.shape[0]
+    index = X.get_device()
+    if X.dtype is not torch.float16 or index < 0 or not X.is_contiguous():
+        _need(X, "X", torch.float16)
+    _expect(wq, "wq", torch.int32, (N, K * bits // 32), index)
+    _expect(s, "s", torch.float16, (N, K // G), index)
     if z is not None:
-        _need(z, "z", torch.float16, (N, K // G), dev)
+        _expect(z, "z", torch.float16, (N, K // G), index)
     if bias is not None:
-        _need(bias, "bias", torch.float16, (N,), dev)
+        _expect(bias, "bias", torch.float16, (N,), index)
     if mul is not None:
-        _need(mul, "mul", torch.float16, (M, N), dev)
+        _expect(mul, "mul", torch.float16, (M, N), index)
     if residual is not None:
-        _need(residual, "residual", torch.float16, (M, N), dev)
+        _expect(residual, "residual", torch.float16, (M, N), index)
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float16, device=dev)
+        out = X.new_empty(M, N)
     else:
-        _need(out, "out", torch.float16, (M, N), dev)
-    if M == 0:
-        return out
-    epi = _EPILOGUE.pack(_at(bias), _at(mul), _at(residual), _ACTS[act])
-    with torch.cuda.device(dev):
-        _check(_lib.qmm_linear(X.data_ptr(), wq.data_ptr(), s.data_ptr(), _at(z), out.data_ptr(), M, K, N, bits, G, epi,
-                               _raw_stream(dev)))
+        _expect(out, "out", torch.float16, (M, N), index)
+    if M > 0:
+        _call(_lib.qmm_linear, _LINEAR.pack(X.data_ptr(), wq.data_ptr(), s.data_ptr(), _at(z), out.data_ptr(), _at(bias), _at(mul),
+                                            _at(residual), M, K, N, G, bits, code), index)
     return out
 
 
-def _rows(t, name, dtype, device, shape=None):
-    """Strides of token and head of [tokens, heads, D] with the elements of a row side by side."""
-    if t.dtype != dtype:
+def _rows(t, name, dtype, index, shape):
+    """Strides of token and head of [tokens, heads, D] whose rows' elements stand side by side."""
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dim() != 3 or (shape is not None and tuple(t.shape) != shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape or '[tokens, heads, D]'}")
-    st = t.stride()
-    if st[2] != 1 and t.shape[2] > 1:
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    a, b, c = t.stride()
+    if c != 1 and shape[2] > 1:
         raise ValueError(f"{name}: the elements of a row must stand side by side")
-    return st[0], st[1]
+    return a, b
 
 
-def _caches(k_cache, v_cache, dtype, device, k_scale, v_scale):
-    """(k strides, v strides, shape, cache type) of two caches [pages, Hkv, page, D]."""
-    got = []
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if t.dtype != dtype and t.dtype != _E4M3:
-            raise TypeError(f"{name} must be {dtype} or {_E4M3}, got {t.dtype}")
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
-        if t.dim() != 4:
-            raise ValueError(f"{name} must be [pages, heads, page, D]")
-        st = t.stride()
-        if st[3] != 1 and t.shape[3] > 1:
-            raise ValueError(f"{name}: the elements of a token must stand side by side")
-        got.append(st[:3])
-    if k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+def _caches(k_cache, v_cache, dtype, index, k_scale, v_scale):
+    """(strides of both, shape, type code) of two caches [pages, heads, page, D]."""
+    shape, kind = k_cache.shape, k_cache.dtype
+    if len(shape) != 4:
+        raise ValueError("k_cache must be [pages, heads, page, D]")
+    if v_cache.shape != shape or v_cache.dtype is not kind:
         raise ValueError("k_cache and v_cache must have one shape and one type")
-    Hkv = k_cache.shape[1]
-    if k_cache.dtype == _E4M3:
-        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-            if t is None:
-                raise ValueError(f"an e4m3 cache needs {name}")
-            _need(t, name, torch.float32, (Hkv,), device)
-        kind = 2
-    else:
-        if k_scale is not None or v_scale is not None:
-            raise ValueError("k_scale and v_scale are for e4m3 caches")
-        kind = _DTYPES[dtype]
-    return got[0], got[1], k_cache.shape, kind
+    if kind is not dtype and kind is not _E4M3:
+        raise TypeError(f"the caches must be {dtype} or {_E4M3}, got {kind}")
+    if k_cache.get_device() != index or v_cache.get_device() != index:
+        raise ValueError(f"the caches are on {k_cache.device} and {v_cache.device}, expected cuda:{index}")
+    ka, kb, kc, kd = k_cache.stride()
+    va, vb, vc, vd = v_cache.stride()
+    if (kd != 1 or vd != 1) and shape[3] > 1:
+        raise ValueError("the elements of a cache's token must stand side by side")
+    if kind is _E4M3:
+        if k_scale is None or v_scale is None:
+            raise ValueError("e4m3 caches need k_scale and v_scale")
+        _expect(k_scale, "k_scale", torch.float32, (shape[1],), index)
+        _expect(v_scale, "v_scale", torch.float32, (shape[1],), index)
+    elif k_scale is not None or v_scale is not None:
+        raise ValueError("k_scale and v_scale are for e4m3 caches")
+    return (ka, kb, kc, va, vb, vc), shape, 2 if kind is _E4M3 else _DTYPES[dtype]
 
 
-def _gpu_type(q):
-    if q.dtype not in _DTYPES:
-        raise TypeError(f"q must be float16 or bfloat16, got {q.dtype}")
-    if not q.is_cuda:
-        raise ValueError("q must be a GPU tensor")
-    return q.dtype, q.device
+def _gpu_rows(t, name):
+    """(type, type code, device index, shape) of the tensor [tokens, heads, D] that leads a call."""
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float16 or bfloat16, got {t.dtype}")
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, D]")
+    return t.dtype, code, index, t.shape
 
 
 def kv_append(q, k, v, k_cache, v_cache, slots, positions=None, rope=None, pairs: bool = False, k_scale=None, v_scale=None, out=None):
@@ -386,26 +399,24 @@ def kv_append(q, k, v, k_cache, v_cache, slots, positions=None, rope=None, pairs
     [T]: rows of rope, fp32 [rows, rot] with rot/2 cosines and then rot/2 sines (None: no rotation).
     pairs: elements 2i and 2i + 1 turn together (False: i and i + rot/2).  q may be None (k and v
     alone); q, k and v may be slices of one projection, out may be q."""
-    dtype, dev = _gpu_type(k if q is None else q)
-    if k.dim() != 3:
-        raise ValueError("k must be [tokens, heads, D]")
-    T, Hkv, D = k.shape
-    ks, vs = _rows(k, "k", dtype, dev), _rows(v, "v", dtype, dev, (T, Hkv, D))
+    dtype, code, index, shape = _gpu_rows(k, "k")
+    T, Hkv, D = shape
+    ks, vs = _rows(k, "k", dtype, index, shape), _rows(v, "v", dtype, index, shape)
     Hq, qs, outs = 0, (0, 0), (0, 0)
     if q is not None:
-        qs = _rows(q, "q", dtype, dev)
+        if q.dim() != 3:
+            raise ValueError("q must be [tokens, heads, D]")
         Hq = q.shape[1]
-        if q.shape[0] != T or q.shape[2] != D:
-            raise ValueError(f"q has shape {tuple(q.shape)}, expected {(T, Hq, D)}")
+        qs = _rows(q, "q", dtype, index, (T, Hq, D))
         if out is None:
-            out = torch.empty((T, Hq, D), dtype=dtype, device=dev)
-        outs = _rows(out, "out", dtype, dev, (T, Hq, D))
+            out = q.new_empty(T, Hq, D)
+        outs = _rows(out, "out", dtype, index, (T, Hq, D))
     elif out is not None:
         raise ValueError("out without q")
-    kcs, vcs, shape, kind = _caches(k_cache, v_cache, dtype, dev, k_scale, v_scale)
-    if shape[1] != Hkv or shape[3] != D:
-        raise ValueError(f"k_cache has shape {tuple(shape)}, expected [pages, {Hkv}, page, {D}]")
-    _need(slots, "slots", torch.int64, (T,), dev)
+    cs, (pages, heads, page, width), kind = _caches(k_cache, v_cache, dtype, index, k_scale, v_scale)
+    if heads != Hkv or width != D:
+        raise ValueError(f"k_cache has shape {tuple(k_cache.shape)}, expected [pages, {Hkv}, page, {D}]")
+    _expect(slots, "slots", torch.int64, (T,), index)
     rot = rows = 0
     if rope is not None:
         if positions is None:
@@ -413,15 +424,13 @@ def kv_append(q, k, v, k_cache, v_cache, slots, positions=None, rope=None, pairs
         if rope.dim() != 2:
             raise ValueError("rope must be [rows, rot]")
         rows, rot = rope.shape
-        _need(rope, "rope", torch.float32, None, dev)
-        _need(positions, "positions", torch.int32, (T,), dev)
+        _expect(rope, "rope", torch.float32, (rows, rot), index)
+        _expect(positions, "positions", torch.int32, (T,), index)
     elif positions is not None:
         raise ValueError("positions without rope")
-    args = _APPEND.pack(_at(q), k.data_ptr(), v.data_ptr(), _at(out), k_cache.data_ptr(), v_cache.data_ptr(), slots.data_ptr(),
-                        _at(positions), _at(rope), _at(k_scale), _at(v_scale), *qs, *ks, *vs, *outs, *kcs, *vcs, T, Hq, Hkv, D, rot,
-                        rows, shape[2], shape[0], _DTYPES[dtype], kind, bool(pairs))
-    with torch.cuda.device(dev):
-        _check(_lib.qmm_kv_append(args, _raw_stream(dev)))
+    _call(_lib.qmm_kv_append, _APPEND.pack(_at(q), k.data_ptr(), v.data_ptr(), _at(out), k_cache.data_ptr(), v_cache.data_ptr(),
+                                           slots.data_ptr(), _at(positions), _at(rope), _at(k_scale), _at(v_scale), *qs, *ks, *vs, *outs,
+                                           *cs, T, Hq, Hkv, D, rot, rows, page, pages, code, kind, bool(pairs)), index)
     return out
 
 
@@ -434,38 +443,36 @@ def paged_attention(q, k_cache, v_cache, page_table, cu_q, kv_lens, max_q: int, 
     is read back).  scale: D ** -0.5 if None; window > 0: a row sees its last `window` keys alone;
     lse fp32 [T, Hq] (written if given): the log of each row's sum.  A row that sees no key gives
     zeros and -inf.  One call serves decode (one row each), chunks and whole prompts mixed."""
-    dtype, dev = _gpu_type(q)
-    qs = _rows(q, "q", dtype, dev)
-    T, Hq, D = q.shape
-    kcs, vcs, shape, kind = _caches(k_cache, v_cache, dtype, dev, k_scale, v_scale)
-    Hkv = shape[1]
-    if shape[3] != D:
-        raise ValueError(f"k_cache has shape {tuple(shape)}, expected [pages, heads, page, {D}]")
+    dtype, code, index, shape = _gpu_rows(q, "q")
+    T, Hq, D = shape
+    qs = _rows(q, "q", dtype, index, shape)
+    cs, (pages, Hkv, page, width), kind = _caches(k_cache, v_cache, dtype, index, k_scale, v_scale)
+    if width != D:
+        raise ValueError(f"k_cache has shape {tuple(k_cache.shape)}, expected [pages, heads, page, {D}]")
     if page_table.dim() != 2:
         raise ValueError("page_table must be [sequences, width]")
     B, width = page_table.shape
-    if page_table.stride(1) != 1 and width > 1:
+    row, step = page_table.stride()
+    if page_table.dtype is not torch.int32 or page_table.get_device() != index:
+        raise TypeError(f"page_table must be int32 on cuda:{index}")
+    if step != 1 and width > 1:
         raise ValueError("page_table: the ids of a sequence must stand side by side")
-    if page_table.dtype != torch.int32 or page_table.device != dev:
-        raise TypeError(f"page_table must be int32 on {dev}")
-    _need(cu_q, "cu_q", torch.int32, (B + 1,), dev)
-    _need(kv_lens, "kv_lens", torch.int32, (B,), dev)
+    _expect(cu_q, "cu_q", torch.int32, (B + 1,), index)
+    _expect(kv_lens, "kv_lens", torch.int32, (B,), index)
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=dtype, device=dev)
-    outs = _rows(out, "out", dtype, dev, (T, Hq, D))
+        out = q.new_empty(T, Hq, D)
+    outs = _rows(out, "out", dtype, index, shape)
     if lse is not None:
-        _need(lse, "lse", torch.float32, (T, Hq), dev)
-    tail = (*qs, *outs, *kcs, *vcs, page_table.stride(0), T, B, Hq, Hkv, D, shape[2], shape[0], width, max_q, max_kv, window,
-            D ** -0.5 if scale is None else scale, _DTYPES[dtype], kind)
+        _expect(lse, "lse", torch.float32, (T, Hq), index)
     head = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), _at(lse), page_table.data_ptr(), cu_q.data_ptr(),
             kv_lens.data_ptr(), _at(k_scale), _at(v_scale))
+    tail = (*qs, *outs, *cs, row, T, B, Hq, Hkv, D, page, pages, width, max_q, max_kv, window, D ** -0.5 if scale is None else scale, code, kind)
     args = _ATTENTION.pack(*head, 0, 0, *tail)
-    with torch.cuda.device(dev):
-        need = _lib.qmm_paged_attention_workspace(args)
-        if need:
-            space = torch.empty(need, dtype=torch.uint8, device=dev)
-            args = _ATTENTION.pack(*head, space.data_ptr(), need, *tail)
-        _check(_lib.qmm_paged_attention(args, _raw_stream(dev)))
+    need = _lib.qmm_paged_attention_workspace(args)
+    if need:
+        space = torch.empty(need, dtype=torch.uint8, device=q.device)
+        args = _ATTENTION.pack(*head, space.data_ptr(), need, *tail)
+    _call(_lib.qmm_paged_attention, args, index)
     return out
 
 

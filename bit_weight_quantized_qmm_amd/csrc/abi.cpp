@@ -212,21 +212,18 @@ qmm_status qmm_quantize(const qmm_half *W, uint8_t *codes, qmm_half *s, qmm_half
     return hip_status(qmm::launch_quantize(W, codes, s, z, (int)K, (int)N, bits, (int)G, (hipStream_t)stream), fn);
 }
 
-qmm_status qmm_linear(const qmm_half *X, const uint32_t *wq, const qmm_half *s, const qmm_half *z, qmm_half *Y,
-                      int64_t M, int64_t K, int64_t N, int bits, int64_t G, const qmm_epilogue *epi, qmm_stream stream)
+qmm_status qmm_linear(const qmm_linear_args *p, qmm_stream stream)
 {
     const char *fn = "qmm_linear";
-    qmm_status st = check_shape(fn, M, K, N, bits, G, true);
+    if (!p) return fail(QMM_ERR_INVALID_ARG, "%s: null arguments", fn);
+    qmm_status st = check_shape(fn, p->M, p->K, p->N, p->bits, p->G, true);
     if (st != QMM_OK) return st;
-    if (!X || !wq || !s || !Y) return fail(QMM_ERR_INVALID_ARG, "%s: null pointer", fn);
-    qmm::GemvArgs a{X, wq, s, z, Y, (int)M, (int)K, (int)N, bits, (int)G};
-    if (epi) {
-        if (epi->act < QMM_ACT_NONE || epi->act > QMM_ACT_GELU_TANH)
-            return fail(QMM_ERR_INVALID_ARG, "%s: unknown activation", fn);
-        a.ep = qmm::Epilogue{epi->bias, epi->mul, epi->residual, epi->act, 0};
-    }
-    a.ep.vec = N % 8 == 0 && aligned(Y, 16) && aligned(a.ep.mul, 16) && aligned(a.ep.residual, 16);
-    const hipError_t e = M <= 16 ? qmm::launch_gemv_linear(a, (hipStream_t)stream) : qmm::launch_gemm_linear(a, (hipStream_t)stream);
+    if (!p->X || !p->wq || !p->s || !p->Y) return fail(QMM_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if (p->act < QMM_ACT_NONE || p->act > QMM_ACT_GELU_TANH) return fail(QMM_ERR_INVALID_ARG, "%s: unknown activation", fn);
+    qmm::GemvArgs a{p->X, p->wq, p->s, p->z, p->Y, (int)p->M, (int)p->K, (int)p->N, p->bits, (int)p->G};
+    const bool vec = p->N % 8 == 0 && aligned(p->Y, 16) && aligned(p->mul, 16) && aligned(p->residual, 16);
+    a.ep = qmm::Epilogue{p->bias, p->mul, p->residual, p->act, vec};
+    const hipError_t e = p->M <= 16 ? qmm::launch_gemv_linear(a, (hipStream_t)stream) : qmm::launch_gemm_linear(a, (hipStream_t)stream);
     return hip_status(e, fn);
 }
 
@@ -346,7 +343,7 @@ qmm_status qmm_paged_attention(const qmm_attention_args *p, qmm_stream stream)
         return fail(QMM_ERR_INVALID_ARG, "%s: workspace missing, too small or not 16-byte aligned", fn);
     a.part = (float *)p->workspace;
     const int64_t most = (int64_t(1) << 31) - 1;
-    if ((int64_t)a.B * a.rblocks > most / a.Hkv / a.splits || (int64_t)a.B > most / (((int64_t)a.max_q * a.Hq + 3) / 4))
+    if ((int64_t)a.B * a.rblocks > most / a.Hkv / a.splits || (int64_t)a.B > most / a.max_q / a.Hq)
         return fail(QMM_ERR_UNSUPPORTED, "%s: grid beyond the supported range", fn);
     return hip_status(qmm::launch_attend(a, p->dtype == QMM_BF16, e4m3, (hipStream_t)stream), fn);
 }

@@ -740,38 +740,64 @@ __global__ __launch_bounds__(64 * NW) void attend_tiles_kernel(const AttendArgs 
     }
 }
 
-// Joins the splits: one wave a row (token, query head).  Split s holds the
-// attention over its own keys, normalised, and the base-2 log of its sum.
-template <typename S>
+// Joins the splits.  Split s of a row (token, query head) holds the attention
+// over its own keys, normalised, and the base-2 log of its sum.  JW waves take
+// a row; a wave reads 64 / (DP / 4) splits at once, each lane 4 elements of its
+// split, so a row's loads do not wait for each other.
+template <typename S, int DP, int JW>
 __global__ __launch_bounds__(256) void attend_join_kernel(const AttendArgs a)
 {
-    const int per = (int)(((int64_t)a.max_q * a.Hq + 3) / 4);
-    const int b = blockIdx.x / per, r = (blockIdx.x - b * per) * 4 + wave_id();
-    const int i = r / a.Hq, hq = r - i * a.Hq, lane = threadIdx.x & 63;
-    const int rb = (i * a.g + hq % a.g) / a.rows;
-    if (i >= a.max_q) return;
+    constexpr int LN = DP / 4, SW = 64 / LN;        // lanes of a split, splits of a wave
+    constexpr int RG = 4 / JW;                      // rows of the workgroup
+    __shared__ __attribute__((aligned(16))) float sums[4][DP];
+    __shared__ float tots[4];
+    const int per = (int)(((int64_t)a.max_q * a.Hq + RG - 1) / RG);
+    const int b = blockIdx.x / per, wave = wave_id(), part_wave = wave % JW, lane = threadIdx.x & 63;
+    const int r = (blockIdx.x - b * per) * RG + wave / JW, i = r / a.Hq, hq = r - i * a.Hq;
+    const int rb = (min(i, a.max_q - 1) * a.g + hq % a.g) / a.rows;
     const KeyRange kr = key_range(a, b, rb);
-    if (i >= kr.n) return;
-    const int live = max(1, (max(0, kr.hi - kr.start) + a.chunk - 1) / a.chunk);
-    const int64_t row = ((int64_t)(kr.t0 + i) * a.Hq + hq);
-    const float *part = a.part + row * a.splits * a.D;
+    const bool live = i < a.max_q && i < kr.n;
+    if (JW == 4 && !live) return;                    // the whole workgroup
+    const int splits = live ? max(1, (max(0, kr.hi - kr.start) + a.chunk - 1) / a.chunk) : 0;
+    const int64_t row = live ? (int64_t)(kr.t0 + i) * a.Hq + hq : 0;
     const float *lses = a.part + (int64_t)a.T * a.Hq * a.splits * a.D + row * a.splits;
     float mm = -INFINITY;
-    for (int s = lane; s < live; s += 64) mm = fmaxf(mm, lses[s]);
+    for (int s = lane; s < splits; s += 64) mm = fmaxf(mm, lses[s]);
 #pragma unroll
     for (int x = 1; x < 64; x <<= 1) mm = fmaxf(mm, __shfl_xor(mm, x));
     const float ms = mm == -INFINITY ? 0.f : mm;
-    const int d = 4 * lane;
+    const int d = 4 * (lane % LN);
+    const float *part = a.part + row * a.splits * a.D + (d < a.D ? d : 0);
     float4_t sum = float4_t{0.f, 0.f, 0.f, 0.f};
     float tot = 0.f;
-    for (int s = 0; s < live; ++s) {
+#pragma unroll 4
+    for (int s = part_wave * SW + lane / LN; s < splits; s += JW * SW) {
         const float f = __builtin_amdgcn_exp2f(lses[s] - ms);
         tot += f;
-        if (d < a.D) sum += f * *reinterpret_cast<const float4_t *>(part + (int64_t)s * a.D + d);
+        sum += f * *reinterpret_cast<const float4_t *>(part + (int64_t)s * a.D);
     }
-    const float inv = mm == -INFINITY ? 0.f : 1.f / tot;
-    sum *= inv;
-    if (d < a.D)
+#pragma unroll
+    for (int x = LN; x < 64; x <<= 1) {
+        tot += __shfl_xor(tot, x);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[e] += __shfl_xor(sum[e], x);
+    }
+    if constexpr (JW > 1) {
+        if (lane < LN) *reinterpret_cast<float4_t *>(&sums[wave][d]) = sum;
+        if (lane == 0) tots[wave] = tot;
+        __syncthreads();
+        if (part_wave != 0) return;
+        tot = 0.f;
+        sum = float4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < JW; ++w) {
+            tot += tots[wave + w];
+            sum += *reinterpret_cast<const float4_t *>(&sums[wave + w][d]);
+        }
+    }
+    if (!live) return;
+    sum *= mm == -INFINITY ? 0.f : 1.f / tot;
+    if (lane < LN && d < a.D)
         *reinterpret_cast<int2v_t *>((char *)a.out + (int64_t)(kr.t0 + i) * a.o_ts + (int64_t)hq * a.o_hs + 2 * d) =
             int2v_t{pack2(sum[0], sum[1], (S)0.f), pack2(sum[2], sum[3], (S)0.f)};
     if (a.lse && lane == 0) a.lse[row] = mm == -INFINITY ? -INFINITY : (mm + __builtin_amdgcn_logf(tot)) * ATT_LN2;
@@ -850,6 +876,19 @@ static hipError_t rows_pick(const AttendArgs &a, hipStream_t st)
     return rows_go<S, F8, DP, P16, 1>(a, st);
 }
 
+// A wave a row where the splits are few, the workgroup's four where a single
+// wave would read them in more than four rounds.
+template <typename S, int DP>
+static hipError_t join_go(const AttendArgs &a, hipStream_t st)
+{
+    const int64_t rows = (int64_t)a.max_q * a.Hq;
+    if (a.splits <= 4 * (256 / DP))
+        hipLaunchKernelGGL((attend_join_kernel<S, DP, 1>), dim3((unsigned)((rows + 3) / 4 * a.B)), dim3(256), 0, st, a);
+    else
+        hipLaunchKernelGGL((attend_join_kernel<S, DP, 4>), dim3((unsigned)(rows * a.B)), dim3(256), 0, st, a);
+    return hipGetLastError();
+}
+
 template <typename S, bool F8>
 static hipError_t attend_type(const AttendArgs &a, hipStream_t st)
 {
@@ -862,9 +901,9 @@ static hipError_t attend_type(const AttendArgs &a, hipStream_t st)
     else
         e = p16 ? rows_pick<S, F8, 256, true>(a, st) : rows_pick<S, F8, 256, false>(a, st);
     if (e != hipSuccess || a.splits == 1) return e;
-    const int64_t per = ((int64_t)a.max_q * a.Hq + 3) / 4;
-    hipLaunchKernelGGL((attend_join_kernel<S>), dim3((unsigned)(per * a.B)), dim3(256), 0, st, a);
-    return hipGetLastError();
+    if (a.D <= 64) return join_go<S, 64>(a, st);
+    if (a.D <= 128) return join_go<S, 128>(a, st);
+    return join_go<S, 256>(a, st);
 }
 
 hipError_t launch_attend(const AttendArgs &a, bool bf16, bool e4m3, hipStream_t st)

@@ -290,25 +290,28 @@ enum { QMM_F16 = 0, QMM_BF16 = 1, QMM_E4M3 = 2 };
  * standard normal distribution, and h (1 + tanh(sqrt(2/pi) (h + 0.044715 h^3))) / 2 */
 enum { QMM_ACT_NONE = 0, QMM_ACT_RELU = 1, QMM_ACT_SILU = 2, QMM_ACT_GELU = 3, QMM_ACT_GELU_TANH = 4 };
 
-/* What follows the product in qmm_linear; null pointers: not there. */
-typedef struct qmm_epilogue {
-    const qmm_half *bias;       /* device, fp16 [N] */
-    const qmm_half *mul;        /* device, fp16 [M][N] */
-    const qmm_half *residual;   /* device, fp16 [M][N] */
-    int act;                    /* QMM_ACT_* */
-} qmm_epilogue;
+typedef struct qmm_linear_args {
+    const qmm_half *X;          /* device, fp16 [M][K] */
+    const uint32_t *wq;         /* device, as for qmm_gemm, and s and z */
+    const qmm_half *s;
+    const qmm_half *z;
+    qmm_half *Y;                /* device, fp16 [M][N] (written) */
+    const qmm_half *bias;       /* device, fp16 [N], or NULL */
+    const qmm_half *mul;        /* device, fp16 [M][N], or NULL */
+    const qmm_half *residual;   /* device, fp16 [M][N], or NULL */
+    int64_t M, K, N, G;
+    int32_t bits;
+    int32_t act;                /* QMM_ACT_* */
+} qmm_linear_args;
 
 /* Y = act(X . dequant(Wq) + bias) * mul + residual for any M >= 1, in one
  * kernel: the product of qmm_gemv (M <= 16) or qmm_gemm, with the rest computed
  * in fp32 on its fp32 sums and rounded once to fp16.  relu takes NaN to 0.
- *   epi    HOST struct, read during the call only; NULL: the plain product
- * X, wq, s, z, Y, M, K, N, bits, G, stream, alignment and errors as for
- * qmm_gemm; an unknown act gives QMM_ERR_INVALID_ARG.  Y may be mul or residual
- * itself (every element is read before it is written), and must overlap
- * nothing else. */
-qmm_status qmm_linear(const qmm_half *X, const uint32_t *wq, const qmm_half *s, const qmm_half *z,
-                      qmm_half *Y, int64_t M, int64_t K, int64_t N, int bits, int64_t G,
-                      const qmm_epilogue *epi, qmm_stream stream);
+ *   args   HOST struct, read during the call only
+ * Shapes, alignment and errors as for qmm_gemm; a NULL args or an unknown act
+ * gives QMM_ERR_INVALID_ARG.  Y may be mul or residual itself (every element is
+ * read before it is written), and must overlap nothing else. */
+qmm_status qmm_linear(const qmm_linear_args *args, qmm_stream stream);
 
 /* Strides below are in elements. */
 typedef struct qmm_kv_append_args {
