@@ -113,12 +113,13 @@ __global__ __launch_bounds__(64 * NW) void attend_rows_kernel(const AttendArgs a
     constexpr int LD = DP + 4;                           // row pitch of the join in LDS
     extern __shared__ __attribute__((aligned(16))) float att_lds[];
 
+    // sequence and head fastest, splits slowest: the blocks of one XCD (every 8th)
+    // then hold early and late splits alike, and the last ones to start, most of
+    // them past their sequence's end, are over at once
     int id = blockIdx.x;
-    const int split = id % a.splits;
-    id /= a.splits;
-    const int hk = id % a.Hkv;
-    id /= a.Hkv;
-    const int rb = id % a.rblocks, b = id / a.rblocks;
+    const int groups = a.B * a.Hkv, bh = id % groups;
+    id /= groups;
+    const int rb = id % a.rblocks, split = id / a.rblocks, b = bh / a.Hkv, hk = bh - b * a.Hkv;
 
     const KeyRange kr = key_range(a, b, rb);
     const int nrow = min(16 * QT, kr.n * a.g - rb * a.rows);     // live rows
@@ -474,8 +475,10 @@ __global__ __launch_bounds__(64 * NW) void attend_rows_kernel(const AttendArgs a
 //   in registers; the A operand comes from ds_read_b64_tr_b16, which hands 16
 //   lanes the columns of a 4 x 16 block of V rows.
 // Rows in LDS are DP elements without padding; their 16-byte chunks are XOR-ed
-// with key % 8 (K: 8 lanes read one chunk of 8 keys) or 2 (key % 4) (V: 16 lanes
-// read two chunks of 4 keys), which spreads every such group over all banks.
+// with a function of the key, so that the 64 banks (256 bytes) are all used: by
+// 16 lanes that read one chunk of 16 keys of K, and by 32 lanes that read four
+// chunks of 4 keys of V (with XORs that reach 8 chunks only, every read took
+// twice its time).
 // The maximum is raised only when a tile's exceeds it by more than 2^8: p then
 // stays below 2^8, O and l are rarely scaled, and nothing else changes.
 // ---------------------------------------------------------------------------
@@ -503,6 +506,8 @@ __global__ __launch_bounds__(64 * NW) void attend_tiles_kernel(const AttendArgs 
     constexpr int RW = 64 / CH;                          // rows that a wave stages at once
     constexpr int QJ = DP / 16, XT = DP / 32;
     constexpr int TILE = ATT_KB * DP * 2;                // bytes
+    auto swizzle_k = [](int row) { return CH == 8 ? (row >> 1) & 7 : row & 15; };
+    auto swizzle_v = [](int row) { return CH == 8 ? 4 * ((row >> 1) & 1) : 4 * (row & 3); };
     static_assert(RW <= 16 && 16 % RW == 0, "a wave's rows lie in one half of 16 keys");
     extern __shared__ __attribute__((aligned(16))) uint8_t att_tiles[];   // K [2][TILE], V [2][TILE]
     typedef __attribute__((address_space(3))) short4v_t lds4_t;
@@ -612,21 +617,23 @@ __global__ __launch_bounds__(64 * NW) void attend_tiles_kernel(const AttendArgs 
 #pragma unroll
         for (int n = 0; n < LN; ++n) {
             const int row = srow + SSTEP * n;
-            put(kst[n], att_tiles + buf * TILE + row * DP * 2 + 16 * (sp ^ (row & 7)));
-            put(vst[n], att_tiles + (2 + buf) * TILE + row * DP * 2 + 16 * (sp ^ (2 * (row & 3))));
+            put(kst[n], att_tiles + buf * TILE + row * DP * 2 + 16 * (sp ^ swizzle_k(row)));
+            put(vst[n], att_tiles + (2 + buf) * TILE + row * DP * 2 + 16 * (sp ^ swizzle_v(row)));
         }
     };
 
-    // LDS addresses of this lane's operands: K row c, chunk (2 j + h) ^ (c % 8), j % 4 apart;
-    // V block: rows lane % 16 / 4 and 4 h, columns 16 (lane / 16 % 2) + 4 (lane % 4), steps of x by 2 apart
-    uint32_t ka[4], va[2];
+    // LDS addresses of this lane's operands: K row c, chunk 2 j + h; V block: rows 4 h + lane % 16 / 4,
+    // columns 16 (lane / 16 % 2) + 4 (lane % 4) of the 32 of step x.  (The swizzles change 4 bits of the
+    // chunk at most: the other steps lie 256 bytes apart.)
+    constexpr int KA = QJ < 8 ? QJ : 8, VA = XT < 4 ? XT : 4;
+    uint32_t ka[KA], va[VA];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) ka[j] = (uint32_t)(c * DP * 2 + 16 * ((2 * j + h) ^ (c & 7)));
+    for (int j = 0; j < KA; ++j) ka[j] = (uint32_t)(c * DP * 2 + 16 * ((2 * j + h) ^ swizzle_k(c)));
     {
-        const int l16 = lane & 15, row = 4 * h + (l16 >> 2), sw = 2 * (row & 3);
+        const int l16 = lane & 15, row = 4 * h + (l16 >> 2);
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int chunk = (4 * x + 2 * ((lane >> 4) & 1) + ((l16 & 3) >> 1)) ^ sw;
+        for (int x = 0; x < VA; ++x) {
+            const int chunk = (4 * x + 2 * ((lane >> 4) & 1) + ((l16 & 3) >> 1)) ^ swizzle_v(row);
             va[x] = (uint32_t)(2 * TILE + row * DP * 2 + 16 * chunk + 8 * (l16 & 1));
         }
     }
@@ -658,7 +665,7 @@ __global__ __launch_bounds__(64 * NW) void attend_tiles_kernel(const AttendArgs 
                 for (int e = 0; e < 16; ++e) s[t][e] = 0.f;
 #pragma unroll
                 for (int j = 0; j < QJ; ++j) {
-                    const int4_t kf = *reinterpret_cast<const int4_t *>(kl + ka[j & 3] + 128 * (j >> 2) + t * 32 * DP * 2);
+                    const int4_t kf = *reinterpret_cast<const int4_t *>(kl + ka[j % KA] + 256 * (j / KA) + t * 32 * DP * 2);
                     s[t] = mfma_32(kf, q[j], s[t], tag);
                 }
             }
@@ -699,7 +706,7 @@ __global__ __launch_bounds__(64 * NW) void attend_tiles_kernel(const AttendArgs 
                 for (int e = 0; e < 4; ++e) p[e] = pack2(s[u >> 1][8 * (u & 1) + 2 * e], s[u >> 1][8 * (u & 1) + 2 * e + 1], tag);
 #pragma unroll
                 for (int x = 0; x < XT; ++x) {
-                    const uint32_t at = va[x & 1] + buf * TILE + 128 * (x >> 1) + u * 16 * DP * 2;
+                    const uint32_t at = va[x % VA] + buf * TILE + 256 * (x / VA) + u * 16 * DP * 2;
                     const short4v_t v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4_t *)(att_tiles + at));
                     const short4v_t v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4_t *)(att_tiles + at + 8 * DP * 2));
                     const int2v_t w0 = __builtin_bit_cast(int2v_t, v0), w1 = __builtin_bit_cast(int2v_t, v1);
@@ -803,6 +810,8 @@ __global__ __launch_bounds__(256) void attend_join_kernel(const AttendArgs a)
     if (a.lse && lane == 0) a.lse[row] = mm == -INFINITY ? -INFINITY : (mm + __builtin_amdgcn_logf(tot)) * ATT_LN2;
 }
 
+#include <stdlib.h>
+static int envi(const char*n,int d){const char*e=getenv(n);return e?atoi(e):d;}
 constexpr int ROWS_NW = 4;
 // waves of a tiles workgroup: two a SIMD up to D = 128 (256 registers each), one
 // beyond (O^T and Q^T alone take 192)
@@ -823,9 +832,9 @@ int64_t plan_attend(AttendArgs &a, bool e4m3)
     a.rows = tiles ? 32 * tiles_waves(a.D) : rows <= 16 || a.D > 128 ? 16 : 32;
     a.rblocks = (int)((rows + a.rows - 1) / a.rows);
     const int64_t span = a.window > 0 ? std::min<int64_t>(a.max_kv, (int64_t)a.window + (a.rows + a.g - 1) / a.g + 16) : a.max_kv;
-    const int64_t groups = (int64_t)a.B * a.Hkv * a.rblocks, unit = tiles ? 512 : 32 * ROWS_NW;
-    const int64_t want = tiles ? 1024 : 2048;
-    int64_t splits = std::max<int64_t>(1, std::min((want + groups - 1) / groups, (span + 4 * unit - 1) / (4 * unit)));
+    const int64_t groups = (int64_t)a.B * a.Hkv * a.rblocks, unit = tiles ? envi("TU",512) : envi("RU",32 * ROWS_NW);
+    const int64_t want = tiles ? envi("TW",1024) : envi("RW",2048);
+    int64_t splits = std::max<int64_t>(1, std::min((want + groups - 1) / groups, (span + envi("MU",4) * unit - 1) / (envi("MU",4) * unit)));
     a.chunk = (int)((((span + 15) + splits - 1) / splits + unit - 1) / unit * unit);
     a.splits = (int)((span + 15 + a.chunk - 1) / a.chunk);
     return a.splits > 1 ? (int64_t)a.T * a.Hq * a.splits * (a.D + 1) * 4 : 0;
