@@ -498,7 +498,7 @@ constexpr int ATT_KB = 64;             // keys of a tile
 constexpr float ATT_LAZY = 8.f;        // a maximum may be exceeded by this much (base 2)
 
 template <typename S, bool F8, int DP, bool P16, int NW>
-__global__ __launch_bounds__(64 * NW) void attend_tiles_kernel(const AttendArgs a)
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4, NW / 4))) void attend_tiles_kernel(const AttendArgs a)
 {
     constexpr int EB = F8 ? 1 : 2;
     constexpr int CH = DP / 8;                           // 16-byte chunks of a row in LDS
@@ -658,24 +658,56 @@ __global__ __launch_bounds__(64 * NW) void attend_tiles_kernel(const AttendArgs 
         pid1 = ids_of(tile + 2);
         if (key0 < whi && key0 + ATT_KB > wlo) {
             const uint8_t *kl = att_tiles + buf * TILE;
+            // operands are read from LDS KA steps ahead of the products that take them
+            auto read_k = [&](int n) {     // step n of 2 QJ: tile n / QJ, step n % QJ
+                const int t = n / QJ, j = n % QJ;
+                return *reinterpret_cast<const int4_t *>(kl + ka[j % KA] + 256 * (j / KA) + t * 32 * DP * 2);
+            };
+            auto read_v = [&](int n) {     // step n of 4 XT: keys 16 (n / XT), columns 32 (n % XT)
+                const int u = n / XT, x = n % XT;
+                const uint32_t at = va[x % VA] + buf * TILE + 256 * (x / VA) + u * 16 * DP * 2;
+                const int2v_t w0 = __builtin_bit_cast(int2v_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4_t *)(att_tiles + at)));
+                const int2v_t w1 = __builtin_bit_cast(int2v_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4_t *)(att_tiles + at + 8 * DP * 2)));
+                return int4_t{w0[0], w0[1], w1[0], w1[1]};
+            };
             float16v_t s[2];
+            int4_t kf[KA], vf[VA];
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
+            for (int n = 0; n < KA; ++n) kf[n] = read_k(n);
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) s[t][e] = 0.f;
 #pragma unroll
-                for (int j = 0; j < QJ; ++j) {
-                    const int4_t kf = *reinterpret_cast<const int4_t *>(kl + ka[j % KA] + 256 * (j / KA) + t * 32 * DP * 2);
-                    s[t] = mfma_32(kf, q[j], s[t], tag);
-                }
+            for (int n = 0; n < 2 * QJ; ++n) {
+                s[n / QJ] = mfma_32(kf[n % KA], q[n % QJ], s[n / QJ], tag);
+                if (n + KA < 2 * QJ)
+                    kf[n % KA] = read_k(n + KA);
+                else if (n + KA - 2 * QJ < VA)
+                    vf[n + KA - 2 * QJ] = read_v(n + KA - 2 * QJ);
             }
+            __builtin_amdgcn_sched_group_barrier(0x100, KA, 0);
+#pragma unroll
+            for (int n = 0; n < 2 * QJ; ++n) {
+                __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+                if (n + KA < 2 * QJ)
+                    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                else if (n + KA - 2 * QJ < VA)
+                    __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
             if (key0 + ATT_KB > min(wall_hi, end) || key0 < wall_lo || bad) {
+                // element e of tile t is key key0 + 4 h + kt, kt a constant
+                const int to = min(vhi, end) - key0 - 4 * h, from = vlo - key0 - 4 * h;
+                const uint64_t hide = bad >> (4 * h);
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const int kt = 32 * t + (e & 3) + 8 * (e >> 2) + 4 * h, key = key0 + kt;
-                        if (key >= min(vhi, end) || key < vlo || ((bad >> kt) & 1)) s[t][e] = -INFINITY;
+                        const int kt = 32 * t + (e & 3) + 8 * (e >> 2);
+                        const bool off = kt >= to || kt < from || ((uint32_t)(hide >> (32 * t)) & (1u << (kt & 31)));
+                        s[t][e] = off ? -INFINITY : s[t][e];
                     }
             }
             float mx = s[0][0];
@@ -706,11 +738,9 @@ __global__ __launch_bounds__(64 * NW) void attend_tiles_kernel(const AttendArgs 
                 for (int e = 0; e < 4; ++e) p[e] = pack2(s[u >> 1][8 * (u & 1) + 2 * e], s[u >> 1][8 * (u & 1) + 2 * e + 1], tag);
 #pragma unroll
                 for (int x = 0; x < XT; ++x) {
-                    const uint32_t at = va[x % VA] + buf * TILE + 256 * (x / VA) + u * 16 * DP * 2;
-                    const short4v_t v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4_t *)(att_tiles + at));
-                    const short4v_t v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4_t *)(att_tiles + at + 8 * DP * 2));
-                    const int2v_t w0 = __builtin_bit_cast(int2v_t, v0), w1 = __builtin_bit_cast(int2v_t, v1);
-                    o[x] = mfma_32(int4_t{w0[0], w0[1], w1[0], w1[1]}, p, o[x], tag);
+                    const int n = u * XT + x;
+                    o[x] = mfma_32(vf[n % VA], p, o[x], tag);
+                    if (n + VA < 4 * XT) vf[n % VA] = read_v(n + VA);
                 }
             }
         }
