@@ -100,8 +100,10 @@ __device__ __forceinline__ float score_scale(const AttendArgs &a, bool f8, int h
 // lies behind it reads as zeros.  Other page sizes take a lane's key from its
 // own page; the rows' offsets are computed once for each key and handed round.
 // ---------------------------------------------------------------------------
+__host__ __device__ constexpr int rows_occupancy(int DP, int QT) { return DP <= 128 && QT == 1 ? 3 : 2; }
+
 template <typename S, bool F8, int DP, bool P16, int QT, int NW>
-__global__ __launch_bounds__(64 * NW) void attend_rows_kernel(const AttendArgs a)
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(rows_occupancy(DP, QT), rows_occupancy(DP, QT)))) void attend_rows_kernel(const AttendArgs a)
 {
     constexpr int EB = F8 ? 1 : 2;                       // bytes of a cache element
     constexpr int KJ = DP / 32;                          // steps of Q K^T
@@ -144,8 +146,8 @@ __global__ __launch_bounds__(64 * NW) void attend_rows_kernel(const AttendArgs a
 #pragma unroll
         for (int j = 0; j < KJ; ++j) {
             const int d = F8 ? 64 * (j / 2) + 16 * g + 8 * (j & 1) : 32 * j + 8 * g;
-            q[qt][j] = int4_t{0, 0, 0, 0};
-            if (live && d < a.D) q[qt][j] = *reinterpret_cast<const int4_t *>(row + 2 * d);
+            q[qt][j] = *reinterpret_cast<const int4_t *>(row + (d < a.D ? 2 * d : 0));
+            if (!live || d >= a.D) q[qt][j] = int4_t{0, 0, 0, 0};
         }
     }
     // keys that every row of the block sees: [all_lo, all_hi)
@@ -181,11 +183,11 @@ __global__ __launch_bounds__(64 * NW) void attend_rows_kernel(const AttendArgs a
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int kk = __builtin_amdgcn_readfirstlane(max(0, min(key + 16 * h, end - 1)));
-                r.p[h] = end > begin ? table[key_page(a, kk)] : 0;
+                r.p[h] = table[key_page(a, kk)];
             }
         } else {
             const int kk = max(0, min(key + (lane & 31), end - 1));
-            r.p[0] = end > begin ? table[key_page(a, kk)] : 0;
+            r.p[0] = table[key_page(a, kk)];
             r.p[1] = 0;
         }
         return r;
@@ -538,8 +540,8 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
 #pragma unroll
         for (int j = 0; j < QJ; ++j) {
             const int d = 16 * j + 8 * h;
-            q[j] = int4_t{0, 0, 0, 0};
-            if (live && d < a.D) q[j] = *reinterpret_cast<const int4_t *>(row + 2 * d);
+            q[j] = *reinterpret_cast<const int4_t *>(row + (d < a.D ? 2 * d : 0));
+            if (!live || d >= a.D) q[j] = int4_t{0, 0, 0, 0};
         }
     }
     // keys that some row of the wave sees, and keys that all of them see
@@ -555,7 +557,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
     // page id of the tile's key number `lane`
     auto ids_of = [&](int tile) {
         const int kk = max(0, min(begin + ATT_KB * tile + lane, end - 1));
-        return end > begin ? table[key_page(a, kk)] : 0;
+        return table[key_page(a, kk)];
     };
     // the pieces that this thread stages: row srow + (64 NW / CH) n, chunk sp
     const int srow = tid / CH, sp = tid % CH;
@@ -840,16 +842,12 @@ __global__ __launch_bounds__(256) void attend_join_kernel(const AttendArgs a)
     if (a.lse && lane == 0) a.lse[row] = mm == -INFINITY ? -INFINITY : (mm + __builtin_amdgcn_logf(tot)) * ATT_LN2;
 }
 
-#include <stdlib.h>
-static int envi(const char*n,int d){const char*e=getenv(n);return e?atoi(e):d;}
-constexpr int ROWS_NW = 4;
 // waves of a tiles workgroup: two a SIMD up to D = 128 (256 registers each), one
 // beyond (O^T and Q^T alone take 192)
 __host__ __device__ constexpr int tiles_waves(int D) { return D <= 128 ? 8 : 4; }
 
 int64_t plan_attend(AttendArgs &a, bool e4m3)
 {
-    (void)e4m3;
     // key / page by one multiplication: with l = ceil(log2 page), mul = floor(2^(31+l) / page) + 1
     // is exact for keys below 2^31 (mul page - 2^(31+l) <= page <= 2^l)
     int lg = 0;
@@ -861,12 +859,30 @@ int64_t plan_attend(AttendArgs &a, bool e4m3)
     const bool tiles = rows > 32;
     a.rows = tiles ? 32 * tiles_waves(a.D) : rows <= 16 || a.D > 128 ? 16 : 32;
     a.rblocks = (int)((rows + a.rows - 1) / a.rows);
-    const int64_t span = a.window > 0 ? std::min<int64_t>(a.max_kv, (int64_t)a.window + (a.rows + a.g - 1) / a.g + 16) : a.max_kv;
-    const int64_t groups = (int64_t)a.B * a.Hkv * a.rblocks, unit = tiles ? envi("TU",512) : envi("RU",32 * ROWS_NW);
-    const int64_t want = tiles ? envi("TW",1024) : envi("RW",2048);
-    int64_t splits = std::max<int64_t>(1, std::min((want + groups - 1) / groups, (span + envi("MU",4) * unit - 1) / (envi("MU",4) * unit)));
-    a.chunk = (int)((((span + 15) + splits - 1) / splits + unit - 1) / unit * unit);
-    a.splits = (int)((span + 15 + a.chunk - 1) / a.chunk);
+    const int64_t span = 15 + (a.window > 0 ? std::min<int64_t>(a.max_kv, (int64_t)a.window + (a.rows + a.g - 1) / a.g) : a.max_kv);
+    const int64_t groups = (int64_t)a.B * a.Hkv * a.rblocks;
+    int64_t splits, unit;
+    if (tiles) {
+        // two workgroups a CU where rows alone do not give them, at least 2048 keys each:
+        // every split costs 8 bytes of fp32 sums for each output
+        unit = 512;
+        splits = std::min((512 + groups - 1) / groups, span / (4 * unit));
+    } else {
+        // One launch without a join where it costs no more: up to 768 keys (one
+        // sequence of 513 with 8 key heads: 9.0 us, 11.7 in splits; of 1000: 12.7 and
+        // 11.7), more where the groups fill the GPU (32 sequences of up to 2048: 35 and
+        // 39 us).  Beyond, two workgroups a CU, at least 256 and at most 4 MB of keys
+        // each: larger shares measured best (4 sequences of up to 131071 keys, e4m3: 167
+        // us, with shares of 1 MB 177; 8 of up to 32768: 157 and 162).
+        unit = 128;
+        const int64_t key_bytes = 2 * a.D * (e4m3 ? 1 : 2), most = int64_t(4) << 20;
+        splits = std::max((512 + groups - 1) / groups, (span * key_bytes + most - 1) / most);
+        splits = std::min(splits, (span + 255) / 256);
+        if (span <= std::max<int64_t>(768, std::min<int64_t>(2048, 8 * groups)) + 15) splits = 1;
+    }
+    splits = std::max<int64_t>(1, splits);
+    a.chunk = (int)(((span + splits - 1) / splits + unit - 1) / unit * unit);
+    a.splits = (int)((span + a.chunk - 1) / a.chunk);
     return a.splits > 1 ? (int64_t)a.T * a.Hq * a.splits * (a.D + 1) * 4 : 0;
 }
 
@@ -890,7 +906,7 @@ static hipError_t tiles_go(const AttendArgs &a, hipStream_t st)
 template <typename S, bool F8, int DP, bool P16, int QT>
 static hipError_t rows_go(const AttendArgs &a, hipStream_t st)
 {
-    constexpr int NW = ROWS_NW;
+    constexpr int NW = 4;
     static bool attr_set = false;
     const int nrow = (int)std::min<int64_t>(16 * QT, (int64_t)a.max_q * a.g);
     const size_t lds = (size_t)NW * nrow * (DP + 6) * 4;
