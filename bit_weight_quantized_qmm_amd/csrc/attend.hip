@@ -499,18 +499,16 @@ __device__ __forceinline__ float16v_t mfma_32(int4_t a, int4_t b, float16v_t c, 
 constexpr int ATT_KB = 64;             // keys of a tile
 constexpr float ATT_LAZY = 8.f;        // a maximum may be exceeded by this much (base 2)
 
-template <typename S, bool F8, int DP, bool P16, int NW>
+template <typename S, bool F8, int DP, int NW>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4, NW / 4))) void attend_tiles_kernel(const AttendArgs a)
 {
     constexpr int EB = F8 ? 1 : 2;
     constexpr int CH = DP / 8;                           // 16-byte chunks of a row in LDS
     constexpr int LN = ATT_KB * CH / (64 * NW);          // chunks of K (and of V) a thread stages
-    constexpr int RW = 64 / CH;                          // rows that a wave stages at once
     constexpr int QJ = DP / 16, XT = DP / 32;
     constexpr int TILE = ATT_KB * DP * 2;                // bytes
     auto swizzle_k = [](int row) { return CH == 8 ? (row >> 1) & 7 : row & 15; };
     auto swizzle_v = [](int row) { return CH == 8 ? 4 * ((row >> 1) & 1) : 4 * (row & 3); };
-    static_assert(RW <= 16 && 16 % RW == 0, "a wave's rows lie in one half of 16 keys");
     extern __shared__ __attribute__((aligned(16))) uint8_t att_tiles[];   // K [2][TILE], V [2][TILE]
     typedef __attribute__((address_space(3))) short4v_t lds4_t;
 
@@ -554,60 +552,43 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
     const char *kbase = (const char *)a.k + (int64_t)hk * a.k_hs, *vbase = (const char *)a.v + (int64_t)hk * a.v_hs;
     const int32_t *table = a.table + (int64_t)b * a.table_s;
 
-    // page id of the tile's key number `lane`
-    auto ids_of = [&](int tile) {
-        const int kk = max(0, min(begin + ATT_KB * tile + lane, end - 1));
-        return table[key_page(a, kk)];
-    };
-    // the pieces that this thread stages: row srow + (64 NW / CH) n, chunk sp
-    const int srow = tid / CH, sp = tid % CH;
+    // Lane l looks up the tile's key number l: its page id, then its row's place in
+    // both caches, which the lanes that stage the row take from it.  A key past the
+    // end reads the last one's row and a bad page id page 0's: in bounds, and hidden.
+    auto key_of = [&](int tile) { return max(0, min(begin + ATT_KB * tile + lane, end - 1)); };
+    auto ids_of = [&](int tile) { return table[key_page(a, key_of(tile))]; };
+    const int srow = tid / CH, sp = tid % CH;             // this thread stages rows srow + SSTEP n, chunk sp
     constexpr int SSTEP = 64 * NW / CH;
     constexpr int PD = EB * 2;                            // dwords of a piece
-    const bool in_d = 8 * sp < a.D;
+    const int in_row = 8 * sp < a.D ? 8 * EB * sp : 0;
     int kst[LN][PD], vst[LN][PD];
-    auto load_piece = [&](const char *base, int64_t ps, uint32_t ts, int key0, int pid, int n, int first, int (&dst)[PD]) {
-        const int key = key0 + srow + SSTEP * n;
-        if constexpr (P16) {
-            const int row0 = (wave * 64) / CH + SSTEP * n;                 // uniform
-            const int kk = key0 + row0, pg = __builtin_amdgcn_readlane(pid, row0 & ~15);
-            const bool ok = kk < end && (uint32_t)pg < (uint32_t)a.pages;
-            const int at = ok ? kk - key_page(a, kk) * a.page : 0;
-            const int64_t off = ok ? (int64_t)pg * ps + (int64_t)at * ts : 0;
-            const uint32_t len = ok ? (uint32_t)(min(RW, end - kk) - 1) * ts + (uint32_t)(a.D * EB) : 0u;
-            const __amdgpu_buffer_rsrc_t rs = make_rsrc(base + off, len);
-            const uint32_t vo = in_d && key >= first ? (uint32_t)(key - kk) * ts + (uint32_t)(8 * EB * sp) : ATT_OOB;
-            if constexpr (PD == 4) {
-                const int4_t w = __builtin_bit_cast(int4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, vo, 0, 0));
-#pragma unroll
-                for (int e = 0; e < 4; ++e) dst[e] = w[e];
-            } else {
-                const int2v_t w = __builtin_bit_cast(int2v_t, __builtin_amdgcn_raw_buffer_load_b64(rs, vo, 0, 0));
-                dst[0] = w[0];
-                dst[1] = w[1];
-            }
-        } else {
-            const int pg = __shfl(pid, srow + SSTEP * n);
-            const bool ok = key < end && key >= first && (uint32_t)pg < (uint32_t)a.pages && in_d;
-            const int64_t off = ok ? (int64_t)pg * ps + (int64_t)(key - key_page(a, key) * a.page) * ts + 8 * EB * sp : 0;
-            if constexpr (PD == 4) {
-                int4_t w = int4_t{0, 0, 0, 0};
-                if (ok) w = *reinterpret_cast<const int4_t *>(base + off);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) dst[e] = w[e];
-            } else {
-                int2v_t w = int2v_t{0, 0};
-                if (ok) w = *reinterpret_cast<const int2v_t *>(base + off);
-                dst[0] = w[0];
-                dst[1] = w[1];
-            }
-        }
-    };
+    uint64_t vlive = 0;                                   // staged keys that a row may see
     auto load_tile = [&](int tile, int pid) {
-        const int key0 = begin + ATT_KB * tile;
+        const int key = begin + ATT_KB * tile + lane, at = key_of(tile) - key_page(a, key_of(tile)) * a.page;
+        const bool ok = (uint32_t)pid < (uint32_t)a.pages;
+        vlive = __ballot(ok && key >= kr.lo && key < end);
+        const int pg = ok ? pid : 0;
+        const int64_t ko = (int64_t)pg * a.k_ps + (int64_t)at * a.k_ts, vo = (int64_t)pg * a.v_ps + (int64_t)at * a.v_ts;
 #pragma unroll
-        for (int n = 0; n < LN; ++n) load_piece(kbase, a.k_ps, a.k_ts, key0, pid, n, 0, kst[n]);
+        for (int n = 0; n < LN; ++n) {
+            auto row_at = [&](const char *base, int64_t off) {
+                const uint32_t lo = (uint32_t)__shfl((int)(uint32_t)off, srow + SSTEP * n), hi = (uint32_t)__shfl((int)(off >> 32), srow + SSTEP * n);
+                return base + (int64_t)(((uint64_t)hi << 32) | lo) + in_row;
+            };
+            auto load = [&](const char *src, int (&dst)[PD]) {
+                if constexpr (PD == 4) {
+                    const int4_t w = *reinterpret_cast<const int4_t *>(src);
 #pragma unroll
-        for (int n = 0; n < LN; ++n) load_piece(vbase, a.v_ps, a.v_ts, key0, pid, n, kr.lo, vst[n]);
+                    for (int e = 0; e < 4; ++e) dst[e] = w[e];
+                } else {
+                    const int2v_t w = *reinterpret_cast<const int2v_t *>(src);
+                    dst[0] = w[0];
+                    dst[1] = w[1];
+                }
+            };
+            load(row_at(kbase, ko), kst[n]);
+            load(row_at(vbase, vo), vst[n]);
+        }
     };
     auto store_tile = [&](int buf) {
         auto put = [&](const int (&w)[PD], uint8_t *dst) {
@@ -616,6 +597,12 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
             else
                 *reinterpret_cast<int4_t *>(dst) = int4_t{w[0], w[1], w[2], w[3]};
         };
+        if (~vlive) {     // what a row must not see may hold anything: it meets p = 0 as zeros
+#pragma unroll
+            for (int n = 0; n < LN; ++n)
+#pragma unroll
+                for (int e = 0; e < PD; ++e) vst[n][e] = (vlive >> (srow + SSTEP * n)) & 1 ? vst[n][e] : 0;
+        }
 #pragma unroll
         for (int n = 0; n < LN; ++n) {
             const int row = srow + SSTEP * n;
@@ -886,19 +873,19 @@ int64_t plan_attend(AttendArgs &a, bool e4m3)
     return a.splits > 1 ? (int64_t)a.T * a.Hq * a.splits * (a.D + 1) * 4 : 0;
 }
 
-template <typename S, bool F8, int DP, bool P16>
+template <typename S, bool F8, int DP>
 static hipError_t tiles_go(const AttendArgs &a, hipStream_t st)
 {
     constexpr int NW = tiles_waves(DP);
     static bool attr_set = false;
     const size_t lds = (size_t)4 * ATT_KB * DP * 2;
     if (!attr_set) {
-        hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&attend_tiles_kernel<S, F8, DP, P16, NW>),
+        hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&attend_tiles_kernel<S, F8, DP, NW>),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
         if (e != hipSuccess) return e;
         attr_set = true;
     }
-    hipLaunchKernelGGL((attend_tiles_kernel<S, F8, DP, P16, NW>), dim3((unsigned)((int64_t)a.B * a.rblocks * a.Hkv * a.splits)),
+    hipLaunchKernelGGL((attend_tiles_kernel<S, F8, DP, NW>), dim3((unsigned)((int64_t)a.B * a.rblocks * a.Hkv * a.splits)),
                        dim3(64 * NW), lds, st, a);
     return hipGetLastError();
 }
@@ -924,7 +911,7 @@ static hipError_t rows_go(const AttendArgs &a, hipStream_t st)
 template <typename S, bool F8, int DP, bool P16>
 static hipError_t rows_pick(const AttendArgs &a, hipStream_t st)
 {
-    if (a.rows > 32) return tiles_go<S, F8, DP, P16>(a, st);
+    if (a.rows > 32) return tiles_go<S, F8, DP>(a, st);
     if constexpr (DP <= 128) {
         if (a.rows == 32) return rows_go<S, F8, DP, P16, 2>(a, st);
     }
