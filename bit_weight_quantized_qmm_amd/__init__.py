@@ -24,7 +24,7 @@ __all__ = ["QmmError", "packed_bytes", "pack", "pack_signed", "unpack", "gemv", 
            "paged_attention", "probe_read", "probe_mfma", "library_path", "SYMBOLS"]
 
 SYMBOLS = ("qmm_packed_bytes", "qmm_pack", "qmm_pack_signed", "qmm_unpack", "qmm_gemv", "qmm_gemv_grouped", "qmm_gemv_lut", "qmm_gemm", "qmm_gemm_fp", "qmm_gemm_w4a8", "qmm_gemm_wka8",
-           "qmm_quantize", "qmm_linear", "qmm_kv_append", "qmm_paged_attention", "qmm_paged_attention_workspace", "qmm_status_string", "qmm_last_error", "qmm_last_hip_error", "qmm_probe_read",
+           "qmm_quantize", "qmm_linear", "qmm_linear_workspace", "qmm_kv_append", "qmm_paged_attention", "qmm_paged_attention_workspace", "qmm_status_string", "qmm_last_error", "qmm_last_hip_error", "qmm_probe_read",
            "qmm_probe_mfma")
 
 
@@ -53,6 +53,7 @@ def _load():
         "qmm_gemm_wka8": ([P, P, P, P, P, P, P, I64, I64, I64, INT, I64, P], INT),
         "qmm_quantize": ([P, P, P, P, I64, I64, INT, I64, P], INT),
         "qmm_linear": ([ctypes.c_char_p, P], INT),
+        "qmm_linear_workspace": ([ctypes.c_char_p], I64),
         "qmm_kv_append": ([ctypes.c_char_p, P], INT),
         "qmm_paged_attention": ([ctypes.c_char_p, P], INT),
         "qmm_paged_attention_workspace": ([ctypes.c_char_p], I64),
@@ -271,7 +272,7 @@ def quantize(W, bits: int, G: int, codes=None, s=None, z=None):
 
 
 # Argument structs of the calls below, laid out as include/qmm.h declares them (native alignment).
-_LINEAR = struct.Struct("@8P4q2i")                   # qmm_linear_args
+_LINEAR = struct.Struct("@9P5q2i")                   # qmm_linear_args
 _APPEND = struct.Struct("@11P8q6q8q3i4x")           # qmm_kv_append_args
 _ATTENTION = struct.Struct("@11Pq4q6qq8q2qqd2i")    # qmm_attention_args
 _ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
@@ -302,7 +303,7 @@ def _expect(t, name, dtype, shape, index):
 
 
 def linear(X, wq, s, z, bits: int, G: int, bias=None, act: str = "none", mul=None, residual=None, out=None) -> torch.Tensor:
-    """Y [M, N] fp16 = act(X [M, K] . dequant(wq) + bias) * mul + residual in one kernel, any M.
+    """Y [M, N] fp16 = act(X [M, K] . dequant(wq) + bias) * mul + residual, any M.
 
     bias fp16 [N], mul and residual fp16 [M, N], each optional; act: "none", "relu", "silu", "gelu"
     or "gelu_tanh".  The product's fp32 sums go through all of it in fp32 and are rounded once.
@@ -334,8 +335,13 @@ def linear(X, wq, s, z, bits: int, G: int, bias=None, act: str = "none", mul=Non
     else:
         _expect(out, "out", torch.float16, (M, N), index)
     if M > 0:
-        _call(_lib.qmm_linear, _LINEAR.pack(X.data_ptr(), wq.data_ptr(), s.data_ptr(), _at(z), out.data_ptr(), _at(bias), _at(mul),
-                                            _at(residual), M, K, N, G, bits, code), index)
+        head = (X.data_ptr(), wq.data_ptr(), s.data_ptr(), _at(z), out.data_ptr(), _at(bias), _at(mul), _at(residual))
+        args = _LINEAR.pack(*head, 0, 0, M, K, N, G, bits, code)
+        need = _lib.qmm_linear_workspace(args) if 1 < M <= 64 else 0
+        if need:
+            space = torch.empty(need, dtype=torch.uint8, device=X.device)
+            args = _LINEAR.pack(*head, space.data_ptr(), need, M, K, N, G, bits, code)
+        _call(_lib.qmm_linear, args, index)
     return out
 
 

@@ -19,7 +19,7 @@ LIBRARY = os.path.join(PKG, "libqmm.so")
 # (source, object suffix, defines): the product kernels are compiled once without and once with an epilogue
 EPILOGUE = ["-DQMM_EPILOGUE"]
 SOURCES = [("gemv.hip", "", []), ("gemv.hip", ".linear", EPILOGUE), ("gemm.hip", "", []), ("gemm.hip", ".linear", EPILOGUE),
-           ("w4a8.hip", "", []), ("abi.cpp", "", []), ("pack.hip", "", []), ("quantize.hip", "", []), ("probe.hip", "", []),
+           ("w4a8.hip", "", []), ("stream.hip", "", []), ("abi.cpp", "", []), ("pack.hip", "", []), ("quantize.hip", "", []), ("probe.hip", "", []),
            ("lut.hip", "", []), ("append.hip", "", []), ("attend.hip", "", [])]
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -223,8 +223,20 @@ qmm_status qmm_linear(const qmm_linear_args *p, qmm_stream stream)
     qmm::GemvArgs a{p->X, p->wq, p->s, p->z, p->Y, (int)p->M, (int)p->K, (int)p->N, p->bits, (int)p->G};
     const bool vec = p->N % 8 == 0 && aligned(p->Y, 16) && aligned(p->mul, 16) && aligned(p->residual, 16);
     a.ep = qmm::Epilogue{p->bias, p->mul, p->residual, p->act, vec};
+    if (qmm::stream_takes(a.M, a.K, a.N)) {
+        const int64_t need = qmm::stream_workspace(a.M, a.K, a.N);
+        if (need > 0 && (!p->workspace || p->workspace_bytes < need || !aligned(p->workspace, 16)))
+            return fail(QMM_ERR_INVALID_ARG, "%s: workspace missing, too small or not 16-byte aligned", fn);
+        return hip_status(qmm::launch_stream(a, (float *)p->workspace, (hipStream_t)stream), fn);
+    }
     const hipError_t e = p->M <= 16 ? qmm::launch_gemv_linear(a, (hipStream_t)stream) : qmm::launch_gemm_linear(a, (hipStream_t)stream);
     return hip_status(e, fn);
+}
+
+int64_t qmm_linear_workspace(const qmm_linear_args *p)
+{
+    if (!p || check_shape("qmm_linear_workspace", p->M, p->K, p->N, p->bits, p->G, true) != QMM_OK) return 0;
+    return qmm::stream_takes((int)p->M, (int)p->K, (int)p->N) ? qmm::stream_workspace((int)p->M, (int)p->K, (int)p->N) : 0;
 }
 
 qmm_status qmm_kv_append(const qmm_kv_append_args *p, qmm_stream stream)

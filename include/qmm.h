@@ -299,19 +299,30 @@ typedef struct qmm_linear_args {
     const qmm_half *bias;       /* device, fp16 [N], or NULL */
     const qmm_half *mul;        /* device, fp16 [M][N], or NULL */
     const qmm_half *residual;   /* device, fp16 [M][N], or NULL */
+    void *workspace;            /* device, 16-byte aligned; may be NULL where none is needed */
+    int64_t workspace_bytes;
     int64_t M, K, N, G;
     int32_t bits;
     int32_t act;                /* QMM_ACT_* */
 } qmm_linear_args;
 
-/* Y = act(X . dequant(Wq) + bias) * mul + residual for any M >= 1, in one
- * kernel: the product of qmm_gemv (M <= 16) or qmm_gemm, with the rest computed
- * in fp32 on its fp32 sums and rounded once to fp16.  relu takes NaN to 0.
+/* Y = act(X . dequant(Wq) + bias) * mul + residual for any M >= 1: f16 products
+ * with fp32 sums, everything after them in fp32 on those sums, rounded once to
+ * fp16.  At M = 1 the product is qmm_gemv's, beyond 64 rows qmm_gemm's; between,
+ * the weights are streamed once, every one rounded once to fp16 as in qmm_gemm.
+ * relu takes NaN to 0.
  *   args   HOST struct, read during the call only
- * Shapes, alignment and errors as for qmm_gemm; a NULL args or an unknown act
- * gives QMM_ERR_INVALID_ARG.  Y may be mul or residual itself (every element is
- * read before it is written), and must overlap nothing else. */
+ * The workspace (scratch during the call: one for each stream that has calls in
+ * flight) needs qmm_linear_workspace() bytes, where K is long and M is 2 to 64.
+ * Shapes, alignment and errors as for qmm_gemm; a NULL args, an unknown act or a
+ * workspace too small gives QMM_ERR_INVALID_ARG.  Y may be mul or residual
+ * itself (every element is read before it is written), and must overlap
+ * nothing else. */
 qmm_status qmm_linear(const qmm_linear_args *args, qmm_stream stream);
+
+/* Bytes of workspace that qmm_linear takes for these arguments (from the sizes
+ * alone), 0 if none or if they are not valid. */
+int64_t qmm_linear_workspace(const qmm_linear_args *args);
 
 /* Strides below are in elements. */
 typedef struct qmm_kv_append_args {
