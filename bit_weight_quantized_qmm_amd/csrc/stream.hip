@@ -39,6 +39,9 @@ __global__ __launch_bounds__(64 * stream_waves(RB)) void stream_kernel(const uin
 {
     using P = RunPlan<BITS>;
     constexpr int D = STREAM_D, ROWS = 16 * RB;
+    // Where a step is one group its sum can be scaled in fp32 instead of its weights in
+    // fp16: 4 RB operations for 16.
+    constexpr bool AFTER = G128 && RB <= 2;
     extern __shared__ __attribute__((aligned(16))) uint8_t xs[];   // [4 steps][ROWS] of 64 bytes
     const int tid = threadIdx.x, lane = tid & 63, wave = wave_id(), g = lane >> 4, c = lane & 15;
     const int R = K >> 5, ng = K / G, tiles = (N + 15) >> 4;
@@ -56,30 +59,29 @@ __global__ __launch_bounds__(64 * stream_waves(RB)) void stream_kernel(const uin
         load_dwords<LOAD_DEFAULT>(wr, run < run1 ? (uint32_t)c * col_bytes + (uint32_t)run * run_bytes : STREAM_OOB, d[i], BITS);
     };
     // s and z of the D steps from st on: 16 runs, so at most 16 groups from that of the
-    // first run on.  G128 (G a multiple of 128): a step is one group, and every lane
-    // loads its column's four; else lane group g loads groups 4g .. 4g + 3 and the lanes
+    // first run on.  G128 (G = 128): step and group are one, and every lane loads its
+    // column's four; else lane group g loads groups 4g .. 4g + 3 and the lanes
     // take theirs from each other (a 2-byte load for each step and lane costs more
     // requests than the weights: 46 -> 63 us for K 28672, N 8192, 16 rows with the
     // zero-points loaded so).  Loads are dwords: the three that hold four halves.
     uint32_t sw[3], zw[3];
+    auto first_group = [&](int st) { return G128 ? (run0 >> 2) + st : run_group(min(run0 + 4 * st, R - 1), ginv); };
     auto issue_sz = [&](int tile, int st) {
         const int t = min(tile, tiles - 1), cols = tile < tiles ? min(16, N - 16 * t) : 0;
         const uint32_t bytes = ((uint32_t)(cols * ng) * 2u + 3u) & ~3u;
-        const int at = c * ng + run_group(min(run0 + 4 * st, R - 1), ginv) + (G128 ? 0 : 4 * g);
+        const int at = c * ng + first_group(st) + (G128 ? 0 : 4 * g);
         load_dwords<LOAD_DEFAULT>(make_rsrc(s + (size_t)t * 16 * ng, bytes), (uint32_t)(at >> 1) * 4u, sw, 3);
         if constexpr (PGZ) load_dwords<LOAD_DEFAULT>(make_rsrc(z + (size_t)t * 16 * ng, bytes), (uint32_t)(at >> 1) * 4u, zw, 3);
     };
     auto four = [&](const uint32_t (&w)[3], int st, uint16_t (&v)[D]) {
-        const int first = run_group(min(run0 + 4 * st, R - 1), ginv);
+        const int first = first_group(st);
         const bool odd = (c * ng + first + (G128 ? 0 : 4 * g)) & 1;
         const uint32_t lo = odd ? __builtin_amdgcn_alignbit(w[1], w[0], 16) : w[0];
         const uint32_t hi = odd ? __builtin_amdgcn_alignbit(w[2], w[1], 16) : w[1];
 #pragma unroll
         for (int i = 0; i < D; ++i) {
             if constexpr (G128) {
-                // steps of one group where G > 128
-                const int k = run_group(min(run0 + 4 * (st + i), R - 1), ginv) - first;
-                v[i] = (uint16_t)((k & 2 ? hi : lo) >> (16 * (k & 1)));
+                v[i] = (uint16_t)((i & 2 ? hi : lo) >> (16 * (i & 1)));
             } else {
                 const int k = run_group(min(run0 + 4 * (st + i) + g, R - 1), ginv) - first, src = 16 * (k >> 2) + c;
                 const uint32_t x = (uint32_t)__shfl((int)lo, src), y = (uint32_t)__shfl((int)hi, src);
@@ -151,7 +153,8 @@ __global__ __launch_bounds__(64 * stream_waves(RB)) void stream_kernel(const uin
                         base[0] = (_Float16)(1024.0f * pow2neg(P::pos[2 * j]) + (PGZ ? 0.0f : zdef));
                         base[1] = (_Float16)(1024.0f * pow2neg(P::pos[2 * j + 1]) + (PGZ ? 0.0f : zdef));
                         if (PGZ) base = base + z2;
-                        const half2_t w = (as_half2(h[j]) * pinv - base) * s2;
+                        half2_t w = as_half2(h[j]) * pinv - base;
+                        if constexpr (!AFTER) w = w * s2;
                         w8[u][2 * e] = w[0];
                         w8[u][2 * e + 1] = w[1];
                     }
@@ -160,13 +163,20 @@ __global__ __launch_bounds__(64 * stream_waves(RB)) void stream_kernel(const uin
                     issue(tile, s0 + D + i, i);
                 else
                     issue(tile + stride, i, i);
+                float4_t y[RB];
+#pragma unroll
+                for (int rb = 0; rb < RB; ++rb) y[rb] = AFTER ? float4_t{0.f, 0.f, 0.f, 0.f} : acc[rb];
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
 #pragma unroll
                     for (int rb = 0; rb < RB; ++rb) {
                         const half8_t x8 = *reinterpret_cast<const half8_t *>(xa[u] + (4 * (s0 + i) * ROWS + 16 * rb) * 64);
-                        acc[rb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x8, w8[u], acc[rb], 0, 0, 0);
+                        y[rb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x8, w8[u], y[rb], 0, 0, 0);
                     }
+#pragma unroll
+                for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) acc[rb][k] = AFTER ? fmaf((float)s2[0], y[rb][k], acc[rb][k]) : y[rb][k];
             }
         }
         // lane (g, c) holds rows 4g .. 4g + 3 of column c
@@ -266,7 +276,7 @@ static hipError_t stream_launch(const GemvArgs &a, const StreamPlan &p, float *s
 template <int BITS, bool PGZ, int RB>
 static hipError_t stream_groups(const GemvArgs &a, const StreamPlan &p, float *sums, hipStream_t st)
 {
-    return a.G % 128 == 0 ? stream_launch<BITS, PGZ, RB, true>(a, p, sums, st) : stream_launch<BITS, PGZ, RB, false>(a, p, sums, st);
+    return a.G == 128 ? stream_launch<BITS, PGZ, RB, true>(a, p, sums, st) : stream_launch<BITS, PGZ, RB, false>(a, p, sums, st);
 }
 
 template <int BITS, bool PGZ>

@@ -309,7 +309,7 @@ typedef struct qmm_linear_args {
 /* Y = act(X . dequant(Wq) + bias) * mul + residual for any M >= 1: f16 products
  * with fp32 sums, everything after them in fp32 on those sums, rounded once to
  * fp16.  At M = 1 the product is qmm_gemv's, beyond 64 rows qmm_gemm's; between,
- * the weights are streamed once, every one rounded once to fp16 as in qmm_gemm.
+ * the weights are streamed once, each rounded to fp16 at most once as in qmm_gemm.
  * relu takes NaN to 0.
  *   args   HOST struct, read during the call only
  * The workspace (scratch during the call: one for each stream that has calls in
