@@ -24,8 +24,8 @@ constexpr uint32_t STREAM_OOB = 0x80000000u;
 constexpr int STREAM_D = 4;        // steps of weights in flight
 constexpr int STREAM_LDS = 128 * 1024;
 
-// most waves of a workgroup: 16 leave 128 registers a wave, which 4 row blocks overrun
-__host__ __device__ constexpr int stream_waves(int RB) { return RB == 4 ? 8 : 16; }
+// most waves of a workgroup: 16 leave 128 registers a wave, which more row blocks overrun
+__host__ __device__ constexpr int stream_waves(int RB) { return RB > 1 ? 8 : 16; }
 
 // X in LDS: [run][row] of 64 bytes, the 16-byte chunks XOR-ed with the run and the
 // row as in the GEMM's tiles: no bank conflicts in the fragment reads
@@ -207,7 +207,7 @@ __global__ __launch_bounds__(256) void stream_join_kernel(const float *__restric
     float h[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) h[e] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
     for (int p = 0; p < slices; ++p) {
         if constexpr (V == 4) {
             const float4_t x = *reinterpret_cast<const float4_t *>(part + p * MN + at);
