@@ -12,12 +12,12 @@ PyTorch is used for device memory and streams only.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
-import struct
 
 import torch
 
-from ._build import LIBRARY
+from ._build import BINDING, LIBRARY
 
 __all__ = ["QmmError", "packed_bytes", "pack", "pack_signed", "unpack", "gemv", "gemv_grouped", "gemv_lut", "gemm", "gemm_fp", "FP4_E2M1",
            "FP8_E4M3", "FP6_E3M2", "FP6_E2M3", "FP3_E1M1", "FP5_E2M2", "FP7_E3M3", "gemm_w4a8", "gemm_wka8", "quantize", "linear", "kv_append",
@@ -52,11 +52,11 @@ def _load():
         "qmm_gemm_w4a8": ([P, P, P, P, P, P, P, I64, I64, I64, I64, P], INT),
         "qmm_gemm_wka8": ([P, P, P, P, P, P, P, I64, I64, I64, INT, I64, P], INT),
         "qmm_quantize": ([P, P, P, P, I64, I64, INT, I64, P], INT),
-        "qmm_linear": ([ctypes.c_char_p, P], INT),
-        "qmm_linear_workspace": ([ctypes.c_char_p], I64),
-        "qmm_kv_append": ([ctypes.c_char_p, P], INT),
-        "qmm_paged_attention": ([ctypes.c_char_p, P], INT),
-        "qmm_paged_attention_workspace": ([ctypes.c_char_p], I64),
+        "qmm_linear": ([P, P], INT),
+        "qmm_linear_workspace": ([P], I64),
+        "qmm_kv_append": ([P, P], INT),
+        "qmm_paged_attention": ([P, P], INT),
+        "qmm_paged_attention_workspace": ([P], I64),
         "qmm_status_string": ([INT], ctypes.c_char_p),
         "qmm_last_error": ([], ctypes.c_char_p),
         "qmm_last_hip_error": ([], ctypes.c_char_p),
@@ -271,35 +271,22 @@ def quantize(W, bits: int, G: int, codes=None, s=None, z=None):
     return codes, s, z
 
 
-# Argument structs of the calls below, laid out as include/qmm.h declares them (native alignment).
-_LINEAR = struct.Struct("@9P5q2i")                   # qmm_linear_args
-_APPEND = struct.Struct("@11P8q6q8q3i4x")           # qmm_kv_append_args
-_ATTENTION = struct.Struct("@11Pq4q6qq8q2qqd2i")    # qmm_attention_args
+def _load_binding():
+    """The C++ side of the calls below: it checks the tensors, fills the library's argument blocks
+    and makes the call."""
+    if not os.path.exists(BINDING):
+        raise ImportError(f"{BINDING} is missing: build it first (python bit_weight_quantized_qmm_amd/_build.py)")
+    spec = importlib.util.spec_from_file_location("_binding", BINDING)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    entry = (_lib.qmm_linear, _lib.qmm_linear_workspace, _lib.qmm_kv_append, _lib.qmm_paged_attention, _lib.qmm_paged_attention_workspace)
+    mod.connect(*(ctypes.cast(f, ctypes.c_void_p).value for f in entry), _check, torch._C._cuda_getCurrentRawStream,
+                torch._C._cuda_getDevice, torch._C._cuda_setDevice)
+    return mod
+
+
+_binding = _load_binding()
 _ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
-_DTYPES = {torch.float16: 0, torch.bfloat16: 1}
-_E4M3 = torch.float8_e4m3fn
-
-
-def _at(t):
-    return 0 if t is None else t.data_ptr()
-
-
-def _call(fn, args, index):
-    """fn(args, the device's current stream) with that device current."""
-    stream = torch._C._cuda_getCurrentRawStream(index)
-    if index == torch._C._cuda_getDevice():
-        status = fn(args, stream)
-    else:
-        with torch.cuda.device(index):
-            status = fn(args, stream)
-    if status:
-        _check(status)
-
-
-def _expect(t, name, dtype, shape, index):
-    """_need for a shape and a device index; the usual case costs four attribute reads."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
-        _need(t, name, dtype, shape, torch.device("cuda", index))
 
 
 def linear(X, wq, s, z, bits: int, G: int, bias=None, act: str = "none", mul=None, residual=None, out=None) -> torch.Tensor:
@@ -311,90 +298,7 @@ def linear(X, wq, s, z, bits: int, G: int, bias=None, act: str = "none", mul=Non
     code = _ACTS.get(act)
     if code is None:
         raise ValueError(f"unknown activation {act!r}: expected one of {sorted(_ACTS)}")
-    if X.dim() != 2 or s.dim() != 2:
-        raise ValueError("X must be [M, K] and s [N, K / G]")
-    if G < 1:
-        raise ValueError("G must be positive")
-    M, K = X.shape
-    N = s.shape[0]
-    index = X.get_device()
-    if X.dtype is not torch.float16 or index < 0 or not X.is_contiguous():
-        _need(X, "X", torch.float16)
-    _expect(wq, "wq", torch.int32, (N, K * bits // 32), index)
-    _expect(s, "s", torch.float16, (N, K // G), index)
-    if z is not None:
-        _expect(z, "z", torch.float16, (N, K // G), index)
-    if bias is not None:
-        _expect(bias, "bias", torch.float16, (N,), index)
-    if mul is not None:
-        _expect(mul, "mul", torch.float16, (M, N), index)
-    if residual is not None:
-        _expect(residual, "residual", torch.float16, (M, N), index)
-    if out is None:
-        out = X.new_empty(M, N)
-    else:
-        _expect(out, "out", torch.float16, (M, N), index)
-    if M > 0:
-        head = (X.data_ptr(), wq.data_ptr(), s.data_ptr(), _at(z), out.data_ptr(), _at(bias), _at(mul), _at(residual))
-        args = _LINEAR.pack(*head, 0, 0, M, K, N, G, bits, code)
-        need = _lib.qmm_linear_workspace(args) if 1 < M <= 64 else 0
-        if need:
-            space = torch.empty(need, dtype=torch.uint8, device=X.device)
-            args = _LINEAR.pack(*head, space.data_ptr(), need, M, K, N, G, bits, code)
-        _call(_lib.qmm_linear, args, index)
-    return out
-
-
-def _rows(t, name, dtype, index, shape):
-    """Strides of token and head of [tokens, heads, D] whose rows' elements stand side by side."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != index:
-        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    a, b, c = t.stride()
-    if c != 1 and shape[2] > 1:
-        raise ValueError(f"{name}: the elements of a row must stand side by side")
-    return a, b
-
-
-def _caches(k_cache, v_cache, dtype, index, k_scale, v_scale):
-    """(strides of both, shape, type code) of two caches [pages, heads, page, D]."""
-    shape, kind = k_cache.shape, k_cache.dtype
-    if len(shape) != 4:
-        raise ValueError("k_cache must be [pages, heads, page, D]")
-    if v_cache.shape != shape or v_cache.dtype is not kind:
-        raise ValueError("k_cache and v_cache must have one shape and one type")
-    if kind is not dtype and kind is not _E4M3:
-        raise TypeError(f"the caches must be {dtype} or {_E4M3}, got {kind}")
-    if k_cache.get_device() != index or v_cache.get_device() != index:
-        raise ValueError(f"the caches are on {k_cache.device} and {v_cache.device}, expected cuda:{index}")
-    ka, kb, kc, kd = k_cache.stride()
-    va, vb, vc, vd = v_cache.stride()
-    if (kd != 1 or vd != 1) and shape[3] > 1:
-        raise ValueError("the elements of a cache's token must stand side by side")
-    if kind is _E4M3:
-        if k_scale is None or v_scale is None:
-            raise ValueError("e4m3 caches need k_scale and v_scale")
-        _expect(k_scale, "k_scale", torch.float32, (shape[1],), index)
-        _expect(v_scale, "v_scale", torch.float32, (shape[1],), index)
-    elif k_scale is not None or v_scale is not None:
-        raise ValueError("k_scale and v_scale are for e4m3 caches")
-    return (ka, kb, kc, va, vb, vc), shape, 2 if kind is _E4M3 else _DTYPES[dtype]
-
-
-def _gpu_rows(t, name):
-    """(type, type code, device index, shape) of the tensor [tokens, heads, D] that leads a call."""
-    code = _DTYPES.get(t.dtype)
-    if code is None:
-        raise TypeError(f"{name} must be float16 or bfloat16, got {t.dtype}")
-    index = t.get_device()
-    if index < 0:
-        raise ValueError(f"{name} must be a GPU tensor")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [tokens, heads, D]")
-    return t.dtype, code, index, t.shape
+    return _binding.linear(X, wq, s, z, bits, G, bias, code, mul, residual, out)
 
 
 def kv_append(q, k, v, k_cache, v_cache, slots, positions=None, rope=None, pairs: bool = False, k_scale=None, v_scale=None, out=None):
@@ -405,39 +309,7 @@ def kv_append(q, k, v, k_cache, v_cache, slots, positions=None, rope=None, pairs
     [T]: rows of rope, fp32 [rows, rot] with rot/2 cosines and then rot/2 sines (None: no rotation).
     pairs: elements 2i and 2i + 1 turn together (False: i and i + rot/2).  q may be None (k and v
     alone); q, k and v may be slices of one projection, out may be q."""
-    dtype, code, index, shape = _gpu_rows(k, "k")
-    T, Hkv, D = shape
-    ks, vs = _rows(k, "k", dtype, index, shape), _rows(v, "v", dtype, index, shape)
-    Hq, qs, outs = 0, (0, 0), (0, 0)
-    if q is not None:
-        if q.dim() != 3:
-            raise ValueError("q must be [tokens, heads, D]")
-        Hq = q.shape[1]
-        qs = _rows(q, "q", dtype, index, (T, Hq, D))
-        if out is None:
-            out = q.new_empty(T, Hq, D)
-        outs = _rows(out, "out", dtype, index, (T, Hq, D))
-    elif out is not None:
-        raise ValueError("out without q")
-    cs, (pages, heads, page, width), kind = _caches(k_cache, v_cache, dtype, index, k_scale, v_scale)
-    if heads != Hkv or width != D:
-        raise ValueError(f"k_cache has shape {tuple(k_cache.shape)}, expected [pages, {Hkv}, page, {D}]")
-    _expect(slots, "slots", torch.int64, (T,), index)
-    rot = rows = 0
-    if rope is not None:
-        if positions is None:
-            raise ValueError("rope needs positions")
-        if rope.dim() != 2:
-            raise ValueError("rope must be [rows, rot]")
-        rows, rot = rope.shape
-        _expect(rope, "rope", torch.float32, (rows, rot), index)
-        _expect(positions, "positions", torch.int32, (T,), index)
-    elif positions is not None:
-        raise ValueError("positions without rope")
-    _call(_lib.qmm_kv_append, _APPEND.pack(_at(q), k.data_ptr(), v.data_ptr(), _at(out), k_cache.data_ptr(), v_cache.data_ptr(),
-                                           slots.data_ptr(), _at(positions), _at(rope), _at(k_scale), _at(v_scale), *qs, *ks, *vs, *outs,
-                                           *cs, T, Hq, Hkv, D, rot, rows, page, pages, code, kind, bool(pairs)), index)
-    return out
+    return _binding.kv_append(q, k, v, k_cache, v_cache, slots, positions, rope, pairs, k_scale, v_scale, out)
 
 
 def paged_attention(q, k_cache, v_cache, page_table, cu_q, kv_lens, max_q: int, max_kv: int, scale=None, window: int = 0,
@@ -449,37 +321,8 @@ def paged_attention(q, k_cache, v_cache, page_table, cu_q, kv_lens, max_q: int, 
     is read back).  scale: D ** -0.5 if None; window > 0: a row sees its last `window` keys alone;
     lse fp32 [T, Hq] (written if given): the log of each row's sum.  A row that sees no key gives
     zeros and -inf.  One call serves decode (one row each), chunks and whole prompts mixed."""
-    dtype, code, index, shape = _gpu_rows(q, "q")
-    T, Hq, D = shape
-    qs = _rows(q, "q", dtype, index, shape)
-    cs, (pages, Hkv, page, width), kind = _caches(k_cache, v_cache, dtype, index, k_scale, v_scale)
-    if width != D:
-        raise ValueError(f"k_cache has shape {tuple(k_cache.shape)}, expected [pages, heads, page, {D}]")
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be [sequences, width]")
-    B, width = page_table.shape
-    row, step = page_table.stride()
-    if page_table.dtype is not torch.int32 or page_table.get_device() != index:
-        raise TypeError(f"page_table must be int32 on cuda:{index}")
-    if step != 1 and width > 1:
-        raise ValueError("page_table: the ids of a sequence must stand side by side")
-    _expect(cu_q, "cu_q", torch.int32, (B + 1,), index)
-    _expect(kv_lens, "kv_lens", torch.int32, (B,), index)
-    if out is None:
-        out = q.new_empty(T, Hq, D)
-    outs = _rows(out, "out", dtype, index, shape)
-    if lse is not None:
-        _expect(lse, "lse", torch.float32, (T, Hq), index)
-    head = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), _at(lse), page_table.data_ptr(), cu_q.data_ptr(),
-            kv_lens.data_ptr(), _at(k_scale), _at(v_scale))
-    tail = (*qs, *outs, *cs, row, T, B, Hq, Hkv, D, page, pages, width, max_q, max_kv, window, D ** -0.5 if scale is None else scale, code, kind)
-    args = _ATTENTION.pack(*head, 0, 0, *tail)
-    need = _lib.qmm_paged_attention_workspace(args)
-    if need:
-        space = torch.empty(need, dtype=torch.uint8, device=q.device)
-        args = _ATTENTION.pack(*head, space.data_ptr(), need, *tail)
-    _call(_lib.qmm_paged_attention, args, index)
-    return out
+    return _binding.paged_attention(q, k_cache, v_cache, page_table, cu_q, kv_lens, max_q, max_kv, scale, window, k_scale, v_scale, out,
+                                    lse)
 
 
 def probe_read(buf: torch.Tensor, grid: int, sink: torch.Tensor | None = None) -> None:

@@ -1,4 +1,5 @@
-"""Build libqmm.so (the C-ABI library) for gfx950 with hipcc, in-tree.
+"""Build libqmm.so (the C-ABI library) for gfx950 with hipcc, in-tree, and
+_binding.so, the CPython side of the decoder-layer calls.
 
 Every translation unit is compiled to an object under ``_build/`` in parallel,
 then linked into ``bit_weight_quantized_qmm_amd/libqmm.so``.  All HIP code is
@@ -16,6 +17,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIBRARY = os.path.join(PKG, "libqmm.so")
+BINDING = os.path.join(PKG, "_binding.so")
 # (source, object suffix, defines): the product kernels are compiled once without and once with an epilogue
 EPILOGUE = ["-DQMM_EPILOGUE"]
 SOURCES = [("gemv.hip", "", []), ("gemv.hip", ".linear", EPILOGUE), ("gemm.hip", "", []), ("gemm.hip", ".linear", EPILOGUE),
@@ -39,10 +41,31 @@ def _compile(item) -> str:
     return obj
 
 
+def build_binding() -> str:
+    """_binding.so: the CPython side of the decoder-layer calls, against torch's C++ headers (host code only)."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    inc = cpp_extension.include_paths() + [sysconfig.get_paths()["include"]]
+    libs = cpp_extension.library_paths()
+    tmp = BINDING + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    cmd += [f"-isystem{p}" for p in inc] + [os.path.join(CSRC, "binding.cpp"), "-o", tmp]
+    cmd += [f"-L{p}" for p in libs] + ["-ltorch_python", "-ltorch_cpu", "-lc10"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed for binding.cpp:\n{res.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(jobs: int = 8) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=min(jobs, len(SOURCES))) as ex:
+        binding = ex.submit(build_binding)
         objs = list(ex.map(_compile, SOURCES))
+        binding.result()
     tmp = LIBRARY + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp] + objs
     res = subprocess.run(cmd, capture_output=True, text=True)
