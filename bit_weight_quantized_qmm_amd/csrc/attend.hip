@@ -833,6 +833,8 @@ __global__ __launch_bounds__(256) void attend_join_kernel(const AttendArgs a)
 // beyond (O^T and Q^T alone take 192)
 __host__ __device__ constexpr int tiles_waves(int D) { return D <= 128 ? 8 : 4; }
 
+constexpr int ROWS_NW = 4;     // waves of a rows workgroup
+
 int64_t plan_attend(AttendArgs &a, bool e4m3)
 {
     // key / page by one multiplication: with l = ceil(log2 page), mul = floor(2^(31+l) / page) + 1
@@ -855,17 +857,22 @@ int64_t plan_attend(AttendArgs &a, bool e4m3)
         unit = 512;
         splits = std::min((512 + groups - 1) / groups, span / (4 * unit));
     } else {
-        // One launch without a join where it costs no more: up to 768 keys (one
-        // sequence of 513 with 8 key heads: 9.0 us, 11.7 in splits; of 1000: 12.7 and
-        // 11.7), more where the groups fill the GPU (32 sequences of up to 2048: 35 and
-        // 39 us).  Beyond, two workgroups a CU, at least 256 and at most 4 MB of keys
-        // each: larger shares measured best (4 sequences of up to 131071 keys, e4m3: 167
-        // us, with shares of 1 MB 177; 8 of up to 32768: 157 and 162).
-        unit = 128;
-        const int64_t key_bytes = 2 * a.D * (e4m3 ? 1 : 2), most = int64_t(4) << 20;
-        splits = std::max((512 + groups - 1) / groups, (span * key_bytes + most - 1) / most);
-        splits = std::min(splits, (span + 255) / 256);
-        if (span <= std::max<int64_t>(768, std::min<int64_t>(2048, 8 * groups)) + 15) splits = 1;
+        // A workgroup alone draws about 50 GB/s, so the keys are shared out early: one
+        // workgroup a CU with at least 64 KB of keys and values each, two with at least
+        // 128 KB (one sequence, 8 key heads of 128, fp16, us: 8000 keys in 64 shares 14.2,
+        // in 32 12.9; 1000 keys in 8 shares 8.6, in 4 9.6, in one 12.7).  Shares beyond
+        // 2.25 MB are cut into equal parts, so that their number stays a multiple of what
+        // the GPU holds at once (4 sequences of up to 131071 keys, e4m3: 167 us in 16
+        // shares of 2.1 MB, 177 in 32, 199 in 17; 64 of up to 8192: 203 in two shares of 2 MB,
+        // 222 in one).  One launch without a join is enough where the keys are few (300:
+        // 7.1 us against 8.6; 513: 9.1 and 8.7) or the groups fill the GPU (32 sequences
+        // of up to 2048: 35 and 39 us).
+        unit = 32 * ROWS_NW;
+        const int64_t bytes = (span - 15) * 2 * a.D * (e4m3 ? 1 : 2), kb = 1024;
+        splits = std::max(std::min(256 / groups, (bytes + 64 * kb - 1) / (64 * kb)),
+                          std::max<int64_t>(1, std::min((512 + groups - 1) / groups, (bytes + 128 * kb - 1) / (128 * kb))));
+        splits *= (std::max<int64_t>(1, bytes / splits) + 2304 * kb - 1) / (2304 * kb);
+        if (bytes <= std::max<int64_t>(224, std::min<int64_t>(1024, 4 * groups)) * kb) splits = 1;
     }
     splits = std::max<int64_t>(1, splits);
     a.chunk = (int)(((span + splits - 1) / splits + unit - 1) / unit * unit);
@@ -893,7 +900,7 @@ static hipError_t tiles_go(const AttendArgs &a, hipStream_t st)
 template <typename S, bool F8, int DP, bool P16, int QT>
 static hipError_t rows_go(const AttendArgs &a, hipStream_t st)
 {
-    constexpr int NW = 4;
+    constexpr int NW = ROWS_NW;
     static bool attr_set = false;
     const int nrow = (int)std::min<int64_t>(16 * QT, (int64_t)a.max_q * a.g);
     const size_t lds = (size_t)NW * nrow * (DP + 6) * 4;
