@@ -221,8 +221,7 @@ qmm_status qmm_linear(const qmm_linear_args *p, qmm_stream stream)
     if (!p->X || !p->wq || !p->s || !p->Y) return fail(QMM_ERR_INVALID_ARG, "%s: null pointer", fn);
     if (p->act < QMM_ACT_NONE || p->act > QMM_ACT_GELU_TANH) return fail(QMM_ERR_INVALID_ARG, "%s: unknown activation", fn);
     qmm::GemvArgs a{p->X, p->wq, p->s, p->z, p->Y, (int)p->M, (int)p->K, (int)p->N, p->bits, (int)p->G};
-    const bool vec = p->N % 8 == 0 && aligned(p->Y, 16) && aligned(p->mul, 16) && aligned(p->residual, 16);
-    a.ep = qmm::Epilogue{p->bias, p->mul, p->residual, p->act, vec};
+    a.ep = qmm::Epilogue{p->bias, p->mul, p->residual, p->act};
     if (qmm::stream_takes(a.M, a.K, a.N)) {
         const int64_t need = qmm::stream_workspace(a.M, a.K, a.N);
         if (need > 0 && (!p->workspace || p->workspace_bytes < need || !aligned(p->workspace, 16)))

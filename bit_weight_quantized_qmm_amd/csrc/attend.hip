@@ -500,7 +500,7 @@ constexpr int ATT_KB = 64;             // keys of a tile
 constexpr float ATT_LAZY = 8.f;        // a maximum may be exceeded by this much (base 2)
 
 template <typename S, bool F8, int DP, int NW>
-__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4, NW / 4))) void attend_tiles_kernel(const AttendArgs a)
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DP <= 128 ? 2 : 1, DP <= 128 ? 2 : 1))) void attend_tiles_kernel(const AttendArgs a)
 {
     constexpr int EB = F8 ? 1 : 2;
     constexpr int CH = DP / 8;                           // 16-byte chunks of a row in LDS
@@ -832,7 +832,6 @@ __global__ __launch_bounds__(256) void attend_join_kernel(const AttendArgs a)
 // waves of a tiles workgroup: two a SIMD up to D = 128 (256 registers each), one
 // beyond (O^T and Q^T alone take 192)
 __host__ __device__ constexpr int tiles_waves(int D) { return D <= 128 ? 8 : 4; }
-
 constexpr int ROWS_NW = 4;     // waves of a rows workgroup
 
 int64_t plan_attend(AttendArgs &a, bool e4m3)
@@ -852,10 +851,13 @@ int64_t plan_attend(AttendArgs &a, bool e4m3)
     const int64_t groups = (int64_t)a.B * a.Hkv * a.rblocks;
     int64_t splits, unit;
     if (tiles) {
-        // two workgroups a CU where rows alone do not give them, at least 2048 keys each:
-        // every split costs 8 bytes of fp32 sums for each output
-        unit = 512;
-        splits = std::min((512 + groups - 1) / groups, span / (4 * unit));
+        // One workgroup a CU where rows alone do not give them, with at least 320 keys
+        // each, two with at least 2048: every split costs 8 bytes of fp32 sums for each
+        // output (us: 50 tokens on 48752 keys, one key head of 2: 24 in 152 shares, 62 in 23;
+        // 15 x 124 tokens on up to 3078 keys, 4 heads of one: 39 in 8, 97 in one; 600 tokens,
+        // 8 heads of 4: 27 in one, 36 in two).
+        unit = 128;
+        splits = std::max(std::min(256 / groups, span / 320), std::min((512 + groups - 1) / groups, span / 2048));
     } else {
         // A workgroup alone draws about 50 GB/s, so the keys are shared out early: one
         // workgroup a CU with at least 64 KB of keys and values each, two with at least

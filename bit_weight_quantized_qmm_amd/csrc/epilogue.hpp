@@ -57,6 +57,12 @@ __device__ __forceinline__ float activate(float h, int act)
     }
 }
 
+// 8 fp16 at any element: rows of an odd number of columns start at 2-byte
+// multiples, where the 16-byte accesses still work, across two lines at times
+typedef _Float16 half8u_t __attribute__((ext_vector_type(8), aligned(2)));
+__device__ __forceinline__ half8_t load_half8(const uint16_t *p) { return *reinterpret_cast<const half8u_t *>(p); }
+__device__ __forceinline__ void store_half8(uint16_t *p, half8_t v) { *reinterpret_cast<half8u_t *>(p) = v; }
+
 // one output (row, col), its operands read here
 __device__ __forceinline__ float epilogue_at(const Epilogue &e, float h, int row, int col, int N)
 {

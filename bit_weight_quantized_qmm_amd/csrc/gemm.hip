@@ -342,10 +342,10 @@ __global__ __launch_bounds__(64 * WV) void gemm_kernel(const uint16_t *__restric
             const float4_t h0 = src[0], h1 = src[1];
             if (row >= M || col >= N) continue;
             const size_t at = (size_t)row * N + col;
-            if (ep.vec) {
+            if (col + 8 <= N) {
                 half8_t mv, rv, y;
-                if (ep.mul) mv = *reinterpret_cast<const half8_t *>(ep.mul + at);
-                if (ep.residual) rv = *reinterpret_cast<const half8_t *>(ep.residual + at);
+                if (ep.mul) mv = load_half8(ep.mul + at);
+                if (ep.residual) rv = load_half8(ep.residual + at);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     float h = activate((e < 4 ? h0[e & 3] : h1[e & 3]) + bias[e], ep.act);
@@ -353,16 +353,11 @@ __global__ __launch_bounds__(64 * WV) void gemm_kernel(const uint16_t *__restric
                     if (ep.residual) h += (float)rv[e];
                     y[e] = (_Float16)h;
                 }
-                *reinterpret_cast<half8_t *>(Y + at) = y;
+                store_half8(Y + at, y);
             } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    if (col + e >= N) break;
-                    float h = activate((e < 4 ? h0[e & 3] : h1[e & 3]) + bias[e], ep.act);
-                    if (ep.mul) h *= (float)as_half(ep.mul[at + e]);
-                    if (ep.residual) h += (float)as_half(ep.residual[at + e]);
-                    Y[at + e] = f32_to_f16_bits(h);
-                }
+                for (int e = 0; e < 7; ++e)
+                    if (col + e < N) Y[at + e] = f32_to_f16_bits(epilogue_at(ep, e < 4 ? h0[e & 3] : h1[e & 3], row, col + e, N));
             }
         }
         asm volatile("" ::: "memory");

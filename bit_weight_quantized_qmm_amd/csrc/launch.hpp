@@ -13,7 +13,6 @@ struct Epilogue {
     const uint16_t *mul;       // fp16 [M][N]
     const uint16_t *residual;  // fp16 [M][N]
     int act;
-    int vec;                   // N % 8 == 0, and Y, mul and residual at multiples of 16 bytes
 };
 
 struct GemvArgs {
