@@ -212,6 +212,12 @@ qmm_status qmm_quantize(const qmm_half *W, uint8_t *codes, qmm_half *s, qmm_half
     return hip_status(qmm::launch_quantize(W, codes, s, z, (int)K, (int)N, bits, (int)G, (hipStream_t)stream), fn);
 }
 
+static int64_t linear_workspace(int M, int K, int N)
+{
+    if (qmm::stream_takes(M, K, N)) return qmm::stream_workspace(M, K, N);
+    return M <= 16 ? 0 : qmm::gemm_workspace(M, K, N);
+}
+
 qmm_status qmm_linear(const qmm_linear_args *p, qmm_stream stream)
 {
     const char *fn = "qmm_linear";
@@ -222,20 +228,20 @@ qmm_status qmm_linear(const qmm_linear_args *p, qmm_stream stream)
     if (p->act < QMM_ACT_NONE || p->act > QMM_ACT_GELU_TANH) return fail(QMM_ERR_INVALID_ARG, "%s: unknown activation", fn);
     qmm::GemvArgs a{p->X, p->wq, p->s, p->z, p->Y, (int)p->M, (int)p->K, (int)p->N, p->bits, (int)p->G};
     a.ep = qmm::Epilogue{p->bias, p->mul, p->residual, p->act};
-    if (qmm::stream_takes(a.M, a.K, a.N)) {
-        const int64_t need = qmm::stream_workspace(a.M, a.K, a.N);
-        if (need > 0 && (!p->workspace || p->workspace_bytes < need || !aligned(p->workspace, 16)))
-            return fail(QMM_ERR_INVALID_ARG, "%s: workspace missing, too small or not 16-byte aligned", fn);
-        return hip_status(qmm::launch_stream(a, (float *)p->workspace, (hipStream_t)stream), fn);
-    }
-    const hipError_t e = p->M <= 16 ? qmm::launch_gemv_linear(a, (hipStream_t)stream) : qmm::launch_gemm_linear(a, (hipStream_t)stream);
+    const int64_t need = linear_workspace(a.M, a.K, a.N);
+    if (need > 0 && (!p->workspace || p->workspace_bytes < need || !aligned(p->workspace, 16)))
+        return fail(QMM_ERR_INVALID_ARG, "%s: workspace missing, too small or not 16-byte aligned", fn);
+    float *part = (float *)p->workspace;
+    const hipError_t e = qmm::stream_takes(a.M, a.K, a.N) ? qmm::launch_stream(a, part, (hipStream_t)stream)
+                         : a.M <= 16                      ? qmm::launch_gemv_linear(a, (hipStream_t)stream)
+                                                          : qmm::launch_gemm_linear(a, part, (hipStream_t)stream);
     return hip_status(e, fn);
 }
 
 int64_t qmm_linear_workspace(const qmm_linear_args *p)
 {
     if (!p || check_shape("qmm_linear_workspace", p->M, p->K, p->N, p->bits, p->G, true) != QMM_OK) return 0;
-    return qmm::stream_takes((int)p->M, (int)p->K, (int)p->N) ? qmm::stream_workspace((int)p->M, (int)p->K, (int)p->N) : 0;
+    return linear_workspace((int)p->M, (int)p->K, (int)p->N);
 }
 
 qmm_status qmm_kv_append(const qmm_kv_append_args *p, qmm_stream stream)

@@ -25,7 +25,14 @@
 
 namespace qmm {
 #ifdef QMM_EPILOGUE
+// qmm_linear's form also takes a slice of K (blockIdx.y: `slice` steps of 128 rows) and,
+// where there are several, leaves its sums in part [slices][M][N]
+#define QMM_GEMM_PARAM QMM_EPI_PARAM, float *__restrict__ part, int slice
+#define QMM_GEMM_ARG QMM_EPI_ARG, sums, slice
 namespace linear {
+#else
+#define QMM_GEMM_PARAM
+#define QMM_GEMM_ARG
 #endif
 
 // 32 activations (natural order, two per dword) -> 16 half2 in the
@@ -71,7 +78,7 @@ template <int BITS, bool PGZ, int FMT, int WV, int NS, int BM, int KP>
 __global__ __launch_bounds__(64 * WV) void gemm_kernel(const uint16_t *__restrict__ X, const uint32_t *__restrict__ wq,
                                                    const uint16_t *__restrict__ s, const uint16_t *__restrict__ z,
                                                    uint16_t *__restrict__ Y, int M, int K, int N, int G, int mtiles,
-                                                   int ntiles QMM_EPI_PARAM)
+                                                   int ntiles QMM_GEMM_PARAM)
 {
     using P = RunPlan<BITS>;
     constexpr int CW = WV / KP;                               // waves side by side in N per K part
@@ -92,7 +99,12 @@ __global__ __launch_bounds__(64 * WV) void gemm_kernel(const uint16_t *__restric
     // K part kp of the workgroup's waves takes steps kp TS .. kp TS + TS - 1
     // (past the last step every load is out of range and reads zeros)
     const int kp = wave / CW, cw = wave - kp * CW, tp = tid - kp * 64 * CW;
-    const int TS = (TT + KP - 1) / KP, t0 = kp * TS;
+#ifdef QMM_EPILOGUE
+    const int s0 = (int)blockIdx.y * slice, Rend = min(R, 4 * (s0 + slice));
+    const int TS = (min(slice, TT - s0) + KP - 1) / KP, t0 = s0 + kp * TS;
+#else
+    const int Rend = R, TS = (TT + KP - 1) / KP, t0 = kp * TS;
+#endif
     const uint32_t run_bytes = 4u * BITS, col_bytes = (uint32_t)R * run_bytes;
     const float zdef = (float)(1u << (BITS - 1));
     const float ginv = run_group_inv(G);
@@ -116,7 +128,7 @@ __global__ __launch_bounds__(64 * WV) void gemm_kernel(const uint16_t *__restric
             const int it = tp + 64 * CW * i;
             const int row = it >> 2, gg = it & 3;
             const int run = 4 * tt + gg;
-            const uint32_t off = (run < R && it < BM * 4) ? ((uint32_t)row * K + (uint32_t)run * 32u) * 2u : GEMM_OOB;
+            const uint32_t off = (run < Rend && it < BM * 4) ? ((uint32_t)row * K + (uint32_t)run * 32u) * 2u : GEMM_OOB;
             load_dwords<LOAD_DEFAULT>(xr, off, raw[i], 16);
         }
     };
@@ -150,9 +162,9 @@ __global__ __launch_bounds__(64 * WV) void gemm_kernel(const uint16_t *__restric
 #pragma unroll
         for (int ns = 0; ns < NS; ++ns) {
             const int col = ns * 16 + c;
-            const uint32_t off = (run < R) ? (uint32_t)col * col_bytes + (uint32_t)run * run_bytes : GEMM_OOB;
+            const uint32_t off = (run < Rend) ? (uint32_t)col * col_bytes + (uint32_t)run * run_bytes : GEMM_OOB;
             load_dwords<LOAD_STREAM>(wr, off, d[ns], BITS);
-            const uint32_t soff = (run < R) ? (uint32_t)(col * ng + run_group(run, ginv)) * 2u : GEMM_OOB;
+            const uint32_t soff = (run < Rend) ? (uint32_t)(col * ng + run_group(run, ginv)) * 2u : GEMM_OOB;
             sv[ns] = __builtin_amdgcn_raw_buffer_load_b16(sr, soff, 0, 0);
             zv[ns] = PGZ ? __builtin_amdgcn_raw_buffer_load_b16(zr, soff, 0, 0) : (uint16_t)0;
         }
@@ -342,7 +354,12 @@ __global__ __launch_bounds__(64 * WV) void gemm_kernel(const uint16_t *__restric
             const float4_t h0 = src[0], h1 = src[1];
             if (row >= M || col >= N) continue;
             const size_t at = (size_t)row * N + col;
-            if (col + 8 <= N) {
+            if (part) {
+                float *dst = part + (size_t)blockIdx.y * M * N + at;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (col + e < N) dst[e] = e < 4 ? h0[e & 3] : h1[e & 3];
+            } else if (col + 8 <= N) {
                 half8_t mv, rv, y;
                 if (ep.mul) mv = load_half8(ep.mul + at);
                 if (ep.residual) rv = load_half8(ep.residual + at);
@@ -366,18 +383,25 @@ __global__ __launch_bounds__(64 * WV) void gemm_kernel(const uint16_t *__restric
 #endif
 }
 
+#ifdef QMM_EPILOGUE
+#define QMM_SLICE_PARAM , float *sums = nullptr, int slices = 1, int slice = 1 << 20
+#define QMM_SLICE_GRID , (unsigned)slices
+#else
+#define QMM_SLICE_PARAM
+#define QMM_SLICE_GRID
+#endif
 template <int BITS, int FMT, int WV, int NS, int BM, int KP = 1>
-static hipError_t gemm_go(const GemvArgs &a, hipStream_t st)
+static hipError_t gemm_go(const GemvArgs &a, hipStream_t st QMM_SLICE_PARAM)
 {
     constexpr int BN = 16 * NS * (WV / KP);
     const int mtiles = (a.M + BM - 1) / BM, ntiles = (a.N + BN - 1) / BN;
-    const dim3 block(64 * WV), grid((unsigned)(mtiles * ntiles));
+    const dim3 block(64 * WV), grid((unsigned)(mtiles * ntiles) QMM_SLICE_GRID);
     if (FMT == 0 && a.z)
         hipLaunchKernelGGL((gemm_kernel<BITS, true, FMT, WV, NS, BM, KP>), grid, block, 0, st, a.X, a.wq, a.s, a.z, a.Y, a.M,
-                           a.K, a.N, a.G, mtiles, ntiles QMM_EPI_ARG);
+                           a.K, a.N, a.G, mtiles, ntiles QMM_GEMM_ARG);
     else
         hipLaunchKernelGGL((gemm_kernel<BITS, false, FMT, WV, NS, BM, KP>), grid, block, 0, st, a.X, a.wq, a.s, a.z, a.Y, a.M,
-                           a.K, a.N, a.G, mtiles, ntiles QMM_EPI_ARG);
+                           a.K, a.N, a.G, mtiles, ntiles QMM_GEMM_ARG);
     return hipGetLastError();
 }
 
@@ -419,7 +443,78 @@ static hipError_t gemm_dispatch(const GemvArgs &a, hipStream_t st)
 }  // namespace linear
 using namespace linear;
 
-hipError_t launch_gemm_linear(const GemvArgs &a, hipStream_t st)
+static hipError_t gemm_whole(const GemvArgs &a, hipStream_t st);
+
+// Slices of K for grids that leave CUs idle, or that cut the rows into small tiles
+// which dequantise every weight again.  The choice compares estimates (us) from the
+// step times of the tiles above, measured at K = N = 4096, k 4: a workgroup's step of
+// 128 rows of K takes 2.3 at 128 x 256, 1.6 at 128 x 128 (2 K parts), 1.03 at 64 x 128,
+// 0.75 at 64 x 64 (2 parts), 0.5 at 64 x 32 (4 parts), 0.3 at 32 x 16 (8 parts); slices
+// cost their sums' way to the workspace and back and a launch.
+struct GemmSlices {
+    int tile, slices, slice;
+};
+static GemmSlices gemm_slices(int M, int K, int N)
+{
+    static const struct { int bm, bn; double step; } kTiles[] = {{128, 256, 2.3}, {128, 128, 1.6}, {64, 128, 1.03},
+                                                                 {64, 64, 0.75}, {64, 32, 0.5}, {32, 16, 0.3}};
+    const long long cus = gemm_cus(), need = (4 * cus + 4) / 5, steps = (K / 32 + 3) / 4;
+    auto tiles = [&](int i) { return (long long)((M + kTiles[i].bm - 1) / kTiles[i].bm) * ((N + kTiles[i].bn - 1) / kTiles[i].bn); };
+    auto cost = [&](int i, long long s) {
+        return (double)((tiles(i) * s + cus - 1) / cus) * (double)((steps + s - 1) / s) * kTiles[i].step +
+               (s > 1 ? 3.0 + (double)s * M * N * 8 / 4e6 : 0.0);
+    };
+    GemmSlices best{0, 1, (int)steps};
+    while (best.tile < 5 && tiles(best.tile) < need) ++best.tile;     // the rule of gemm_dispatch
+    double t = 0.9 * cost(best.tile, 1);
+    for (int i = 0; i < 3; ++i)
+        for (long long s = 1; s <= 16 && (s == 1 || s * 4 <= steps); ++s)
+            if (cost(i, s) < t) {
+                t = cost(i, s);
+                best = GemmSlices{i, (int)s, (int)((steps + s - 1) / s)};
+            }
+    best.slices = (int)((steps + best.slice - 1) / best.slice);
+    return best;
+}
+
+int64_t gemm_workspace(int M, int K, int N)
+{
+    const GemmSlices g = gemm_slices(M, K, N);
+    return g.slices > 1 ? (int64_t)g.slices * M * N * 4 : 0;
+}
+
+template <int BITS>
+static hipError_t gemm_sliced(const GemvArgs &a, float *part, const GemmSlices &g, hipStream_t st)
+{
+    const hipError_t e = g.tile == 0 ? gemm_go<BITS, 0, 8, 2, 128, 1>(a, st, part, g.slices, g.slice)
+                       : g.tile == 1 ? gemm_go<BITS, 0, 8, 2, 128, 2>(a, st, part, g.slices, g.slice)
+                                     : gemm_go<BITS, 0, 8, 1, 64, 1>(a, st, part, g.slices, g.slice);
+    return e != hipSuccess || g.slices == 1 ? e : launch_join(a, part, g.slices, st);
+}
+
+hipError_t launch_gemm_linear(const GemvArgs &a, float *part, hipStream_t st)
+{
+    const GemmSlices g = gemm_slices(a.M, a.K, a.N);
+    if (g.tile < 3) {
+        if (g.slices == 1) part = nullptr;
+        switch (a.bits) {
+            case 1: return gemm_sliced<1>(a, part, g, st);
+            case 2: return gemm_sliced<2>(a, part, g, st);
+            case 3: return gemm_sliced<3>(a, part, g, st);
+            case 4: return gemm_sliced<4>(a, part, g, st);
+            case 5: return gemm_sliced<5>(a, part, g, st);
+            case 6: return gemm_sliced<6>(a, part, g, st);
+            case 7: return gemm_sliced<7>(a, part, g, st);
+            case 8: return gemm_sliced<8>(a, part, g, st);
+            default: return hipErrorInvalidValue;
+        }
+    }
+    return gemm_whole(a, st);
+}
+#endif
+
+#ifdef QMM_EPILOGUE
+static hipError_t gemm_whole(const GemvArgs &a, hipStream_t st)
 #else
 hipError_t launch_gemm(const GemvArgs &a, hipStream_t st)
 #endif

@@ -96,11 +96,13 @@ hipError_t launch_unpack(const uint32_t *wq, uint8_t *codes, int K, int N, int b
 hipError_t launch_gemv(const GemvArgs &a, hipStream_t st);
 hipError_t launch_gemm(const GemvArgs &a, hipStream_t st);
 hipError_t launch_gemv_linear(const GemvArgs &a, hipStream_t st);   // with a.ep; M <= 16
-hipError_t launch_gemm_linear(const GemvArgs &a, hipStream_t st);   // with a.ep
+hipError_t launch_gemm_linear(const GemvArgs &a, float *part, hipStream_t st);   // with a.ep; part: gemm_workspace() bytes
+int64_t gemm_workspace(int M, int K, int N);
 // qmm_linear for 2 <= M <= 64 (part: stream_workspace() bytes of fp32 sums)
 bool stream_takes(int M, int K, int N);
 int64_t stream_workspace(int M, int K, int N);
 hipError_t launch_stream(const GemvArgs &a, float *part, hipStream_t st);
+hipError_t launch_join(const GemvArgs &a, const float *part, int slices, hipStream_t st);   // slices' sums, epilogue
 hipError_t launch_gemm_fp(const GemvArgs &a, int fmt, hipStream_t st);
 hipError_t launch_gemv_grouped(const GroupArgs &a, hipStream_t st);
 hipError_t launch_gemv_lut(const GemvArgs &a, hipStream_t st);   // M = 1, 1-bit codes; NotSupported otherwise

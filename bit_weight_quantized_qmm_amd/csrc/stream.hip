@@ -222,6 +222,16 @@ __global__ __launch_bounds__(256) void stream_join_kernel(const float *__restric
     for (int e = 0; e < V; ++e) Y[at + e] = f32_to_f16_bits(epilogue_at(ep, h[e], row, col + e, N));
 }
 
+hipError_t launch_join(const GemvArgs &a, const float *part, int slices, hipStream_t st)
+{
+    const int64_t n = (int64_t)a.M * a.N;
+    if (a.N % 4 == 0)
+        hipLaunchKernelGGL((stream_join_kernel<4>), dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0, st, part, a.Y, slices, a.M, a.N, a.ep);
+    else
+        hipLaunchKernelGGL((stream_join_kernel<1>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, part, a.Y, slices, a.M, a.N, a.ep);
+    return hipGetLastError();
+}
+
 struct StreamPlan {
     int RB, W, steps, slices, groups;
 };
@@ -248,7 +258,10 @@ bool stream_takes(int M, int K, int N)
     // weight again for each tile of rows; it is quicker for small products alone, where
     // the join's launch counts (17 rows, 4096 x 4096: 10.0 and 11.3 us; 33 rows: 18.7
     // and 12.7; 32 rows, 4096 x 11008: 30 and 15.7).
-    if (M < 2 || M > 64 || (M <= 16 ? K <= 8192 : (int64_t)K * N < 14000000)) return false;
+    // A few columns of long K are one or two workgroups' work for either of them (16 rows,
+    // K 7808, N 2: 14.8 us, in slices 9.3).
+    if (M < 2 || M > 64) return false;
+    if (!(K >= 6144 && N <= 512) && (M <= 16 ? K <= 8192 : (int64_t)K * N < 14000000)) return false;
     return stream_plan(M, K, N).slices < 65536;
 }
 
@@ -286,13 +299,7 @@ static hipError_t stream_go(const GemvArgs &a, float *part, hipStream_t st)
     float *sums = p.slices > 1 ? part : nullptr;
     hipError_t e = p.RB == 1 ? stream_groups<BITS, PGZ, 1>(a, p, sums, st)
                              : p.RB == 2 ? stream_groups<BITS, PGZ, 2>(a, p, sums, st) : stream_groups<BITS, PGZ, 4>(a, p, sums, st);
-    if (e != hipSuccess || p.slices == 1) return e;
-    const int64_t n = (int64_t)a.M * a.N;
-    if (a.N % 4 == 0)
-        hipLaunchKernelGGL((stream_join_kernel<4>), dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0, st, part, a.Y, p.slices, a.M, a.N, a.ep);
-    else
-        hipLaunchKernelGGL((stream_join_kernel<1>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, part, a.Y, p.slices, a.M, a.N, a.ep);
-    return hipGetLastError();
+    return e != hipSuccess || p.slices == 1 ? e : launch_join(a, part, p.slices, st);
 }
 
 hipError_t launch_stream(const GemvArgs &a, float *part, hipStream_t st)

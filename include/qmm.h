@@ -308,12 +308,12 @@ typedef struct qmm_linear_args {
 
 /* Y = act(X . dequant(Wq) + bias) * mul + residual for any M >= 1: f16 products
  * with fp32 sums, everything after them in fp32 on those sums, rounded once to
- * fp16.  At M = 1 the product is qmm_gemv's, beyond 64 rows qmm_gemm's; between,
- * the weights are streamed once, each rounded to fp16 at most once as in qmm_gemm.
+ * fp16.  At M = 1 the product is qmm_gemv's; beyond, every weight is rounded to
+ * fp16 at most once as in qmm_gemm (up to 16 rows and K = 8192: as in qmm_gemv).
  * relu takes NaN to 0.
  *   args   HOST struct, read during the call only
  * The workspace (scratch during the call: one for each stream that has calls in
- * flight) needs qmm_linear_workspace() bytes, where K is long and M is 2 to 64.
+ * flight) needs qmm_linear_workspace() bytes: fp32 sums where K is cut into slices.
  * Shapes, alignment and errors as for qmm_gemm; a NULL args, an unknown act or a
  * workspace too small gives QMM_ERR_INVALID_ARG.  Y may be mul or residual
  * itself (every element is read before it is written), and must overlap

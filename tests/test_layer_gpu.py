@@ -96,7 +96,7 @@ def linear_reference(X, wq, s, z, bits, G, bias, act, mul, residual):
 
 
 LINEAR = [(1, 256, 40, 64), (1, 4096, 1000, 128), (1, 9216, 33, 32), (1, 16384, 70, 128), (2, 96, 19, 32), (3, 1024, 130, 64), (7, 2080, 50, 32),
-          (16, 1152, 264, 128), (16, 8320, 17, 128), (17, 256, 8, 32), (37, 2080, 1000, 32), (64, 4224, 4000, 128), (20, 8192, 2001, 64), (33, 28800, 600, 96), (5, 16384, 33, 32), (2, 9344, 130, 64), (50, 512, 28680, 32), (129, 512, 264, 128), (300, 128, 777, 64),
+          (16, 1152, 264, 128), (16, 8320, 17, 128), (17, 256, 8, 32), (37, 2080, 1000, 32), (64, 4224, 4000, 128), (20, 8192, 2001, 64), (33, 28800, 600, 96), (5, 16384, 33, 32), (2, 9344, 130, 64), (50, 512, 28680, 32), (111, 5760, 2001, 64), (130, 8192, 1032, 32), (263, 10240, 700, 128), (129, 512, 264, 128), (300, 128, 777, 64),
           (1100, 256, 1032, 128)]
 
 
