@@ -496,17 +496,19 @@ __device__ __forceinline__ float16v_t mfma_32(int4_t a, int4_t b, float16v_t c, 
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8x_t, a), __builtin_bit_cast(bf8x_t, b), c, 0, 0, 0);
 }
 
-constexpr int ATT_KB = 64;             // keys of a tile
+// keys of a tile: 64, and 32 beyond D = 128, where O^T and Q^T leave no registers for more
+__host__ __device__ constexpr int tiles_keys(int D) { return D <= 128 ? 64 : 32; }
 constexpr float ATT_LAZY = 8.f;        // a maximum may be exceeded by this much (base 2)
 
 template <typename S, bool F8, int DP, int NW>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DP <= 128 ? 2 : 1, DP <= 128 ? 2 : 1))) void attend_tiles_kernel(const AttendArgs a)
 {
+    constexpr int KB = tiles_keys(DP), KT = KB / 32;     // keys of a tile, halves of 32 of them
     constexpr int EB = F8 ? 1 : 2;
     constexpr int CH = DP / 8;                           // 16-byte chunks of a row in LDS
-    constexpr int LN = ATT_KB * CH / (64 * NW);          // chunks of K (and of V) a thread stages
+    constexpr int LN = KB * CH / (64 * NW);          // chunks of K (and of V) a thread stages
     constexpr int QJ = DP / 16, XT = DP / 32;
-    constexpr int TILE = ATT_KB * DP * 2;                // bytes
+    constexpr int TILE = KB * DP * 2;                // bytes
     auto swizzle_k = [](int row) { return CH == 8 ? (row >> 1) & 7 : row & 15; };
     auto swizzle_v = [](int row) { return CH == 8 ? 4 * ((row >> 1) & 1) : 4 * (row & 3); };
     extern __shared__ __attribute__((aligned(16))) uint8_t att_tiles[];   // K [2][TILE], V [2][TILE]
@@ -555,7 +557,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DP <= 1
     // Lane l looks up the tile's key number l: its page id, then its row's place in
     // both caches, which the lanes that stage the row take from it.  A key past the
     // end reads the last one's row and a bad page id page 0's: in bounds, and hidden.
-    auto key_of = [&](int tile) { return max(0, min(begin + ATT_KB * tile + lane, end - 1)); };
+    auto key_of = [&](int tile) { return max(0, min(begin + KB * tile + lane, end - 1)); };
     auto ids_of = [&](int tile) { return table[key_page(a, key_of(tile))]; };
     const int srow = tid / CH, sp = tid % CH;             // this thread stages rows srow + SSTEP n, chunk sp
     constexpr int SSTEP = 64 * NW / CH;
@@ -564,7 +566,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DP <= 1
     int kst[LN][PD], vst[LN][PD];
     uint64_t vlive = 0;                                   // staged keys that a row may see
     auto load_tile = [&](int tile, int pid) {
-        const int key = begin + ATT_KB * tile + lane, at = key_of(tile) - key_page(a, key_of(tile)) * a.page;
+        const int key = begin + KB * tile + lane, at = key_of(tile) - key_page(a, key_of(tile)) * a.page;
         const bool ok = (uint32_t)pid < (uint32_t)a.pages;
         vlive = __ballot(ok && key >= kr.lo && key < end);
         const int pg = ok ? pid : 0;
@@ -634,64 +636,64 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DP <= 1
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[x][e] = 0.f;
 
-    const int tiles = (max(0, end - begin) + ATT_KB - 1) / ATT_KB;
+    const int tiles = (max(0, end - begin) + KB - 1) / KB;
     int pid = ids_of(0), pid1 = ids_of(1);
     load_tile(0, pid);
     store_tile(0);
     __syncthreads();
     for (int tile = 0; tile < tiles; ++tile) {
-        const int buf = tile & 1, key0 = begin + ATT_KB * tile;
+        const int buf = tile & 1, key0 = begin + KB * tile;
         const uint64_t bad = __ballot((uint32_t)pid >= (uint32_t)a.pages);
         pid = pid1;
         load_tile(tile + 1, pid);
         pid1 = ids_of(tile + 2);
-        if (key0 < whi && key0 + ATT_KB > wlo) {
+        if (key0 < whi && key0 + KB > wlo) {
             const uint8_t *kl = att_tiles + buf * TILE;
             // operands are read from LDS KA steps ahead of the products that take them
-            auto read_k = [&](int n) {     // step n of 2 QJ: tile n / QJ, step n % QJ
+            auto read_k = [&](int n) {     // step n of KT QJ: tile n / QJ, step n % QJ
                 const int t = n / QJ, j = n % QJ;
                 return *reinterpret_cast<const int4_t *>(kl + ka[j % KA] + 256 * (j / KA) + t * 32 * DP * 2);
             };
-            auto read_v = [&](int n) {     // step n of 4 XT: keys 16 (n / XT), columns 32 (n % XT)
+            auto read_v = [&](int n) {     // step n of 2 KT XT: keys 16 (n / XT), columns 32 (n % XT)
                 const int u = n / XT, x = n % XT;
                 const uint32_t at = va[x % VA] + buf * TILE + 256 * (x / VA) + u * 16 * DP * 2;
                 const int2v_t w0 = __builtin_bit_cast(int2v_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4_t *)(att_tiles + at)));
                 const int2v_t w1 = __builtin_bit_cast(int2v_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4_t *)(att_tiles + at + 8 * DP * 2)));
                 return int4_t{w0[0], w0[1], w1[0], w1[1]};
             };
-            float16v_t s[2];
+            float16v_t s[KT];
             int4_t kf[KA], vf[VA];
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int n = 0; n < KA; ++n) kf[n] = read_k(n);
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < KT; ++t)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) s[t][e] = 0.f;
 #pragma unroll
-            for (int n = 0; n < 2 * QJ; ++n) {
+            for (int n = 0; n < KT * QJ; ++n) {
                 s[n / QJ] = mfma_32(kf[n % KA], q[n % QJ], s[n / QJ], tag);
-                if (n + KA < 2 * QJ)
+                if (n + KA < KT * QJ)
                     kf[n % KA] = read_k(n + KA);
-                else if (n + KA - 2 * QJ < VA)
-                    vf[n + KA - 2 * QJ] = read_v(n + KA - 2 * QJ);
+                else if (n + KA - KT * QJ < VA)
+                    vf[n + KA - KT * QJ] = read_v(n + KA - KT * QJ);
             }
             __builtin_amdgcn_sched_group_barrier(0x100, KA, 0);
 #pragma unroll
-            for (int n = 0; n < 2 * QJ; ++n) {
+            for (int n = 0; n < KT * QJ; ++n) {
                 __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-                if (n + KA < 2 * QJ)
+                if (n + KA < KT * QJ)
                     __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-                else if (n + KA - 2 * QJ < VA)
+                else if (n + KA - KT * QJ < VA)
                     __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
             }
             __builtin_amdgcn_sched_barrier(0);
-            if (key0 + ATT_KB > min(wall_hi, end) || key0 < wall_lo || bad) {
+            if (key0 + KB > min(wall_hi, end) || key0 < wall_lo || bad) {
                 // element e of tile t is key key0 + 4 h + kt, kt a constant
                 const int to = min(vhi, end) - key0 - 4 * h, from = vlo - key0 - 4 * h;
                 const uint64_t hide = bad >> (4 * h);
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+                for (int t = 0; t < KT; ++t)
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const int kt = 32 * t + (e & 3) + 8 * (e >> 2);
@@ -701,7 +703,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DP <= 1
             }
             float mx = s[0][0];
 #pragma unroll
-            for (int e = 1; e < 32; ++e) mx = fmaxf(mx, s[e >> 4][e & 15]);
+            for (int e = 1; e < 16 * KT; ++e) mx = fmaxf(mx, s[e >> 4][e & 15]);
             mx = fmaxf(mx, __shfl_xor(mx, 32));
             mx *= sl;
             if (__any(mx > m + ATT_LAZY)) {              // also the first finite maximum: m is -inf
@@ -714,14 +716,14 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DP <= 1
             const float ms = m == -INFINITY ? 0.f : m;
             float sum = 0.f;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
+            for (int e = 0; e < 16 * KT; ++e) {
                 const float p = __builtin_amdgcn_exp2f(fmaf(s[e >> 4][e & 15], sl, -ms));
                 sum += p;
                 s[e >> 4][e & 15] = p;
             }
             l += sum;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < 2 * KT; ++u) {
                 int4_t p;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) p[e] = pack2(s[u >> 1][8 * (u & 1) + 2 * e], s[u >> 1][8 * (u & 1) + 2 * e + 1], tag);
@@ -729,7 +731,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DP <= 1
                 for (int x = 0; x < XT; ++x) {
                     const int n = u * XT + x;
                     o[x] = mfma_32(vf[n % VA], p, o[x], tag);
-                    if (n + VA < 4 * XT) vf[n % VA] = read_v(n + VA);
+                    if (n + VA < 2 * KT * XT) vf[n % VA] = read_v(n + VA);
                 }
             }
         }
@@ -887,7 +889,7 @@ static hipError_t tiles_go(const AttendArgs &a, hipStream_t st)
 {
     constexpr int NW = tiles_waves(DP);
     static bool attr_set = false;
-    const size_t lds = (size_t)4 * ATT_KB * DP * 2;
+    const size_t lds = (size_t)4 * tiles_keys(DP) * DP * 2;
     if (!attr_set) {
         hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&attend_tiles_kernel<S, F8, DP, NW>),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
