@@ -520,3 +520,59 @@ def test_layer_step_in_a_graph(q):
         torch.cuda.synchronize()
         assert same(got, want), i
     assert not same(want, eager)
+
+
+def test_decoder_layer_example(q):
+    """Prompts and graph-replayed decode steps through the paged cache against the layer in fp32.  The
+    fp16 roundings on the way (projections, q, k, v, probabilities, outputs) are some ten of 2^-11
+    in a row, and weights rounded once; their root sum of squares stays below 2^-8."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "decoder_layer.py")
+    spec = importlib.util.spec_from_file_location("decoder_layer", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    for users, prompt, steps, page in ((3, 75, 6, 16), (1, 1, 3, 1), (5, 300, 2, 64)):
+        _, error = example.run(hidden=512, heads=8, kv_heads=2, head_dim=64, inner=1024, users=users, prompt=prompt, steps=steps, page=page)
+        assert error < 2.0 ** -8
+
+
+# -------------------------------------------------------------- refusals --
+def test_refusals_on_the_gpu(q):
+    """Shapes, types and devices that do not fit, named in the error; nothing is written."""
+    c = Paged([(1, 20)], 4, 2, 64, 16, torch.float16)
+    out = torch.full((1, 4, 64), 7.0, device=DEV).half()
+    ok = dict(q=c.q, k_cache=c.kc, v_cache=c.vc, page_table=c.table, cu_q=c.cu_q, kv_lens=c.kv_lens, max_q=1, max_kv=20, out=out)
+    bad = [(dict(q=c.q[:, :3]), ValueError), (dict(q=c.q.float()), TypeError), (dict(k_cache=c.kc[..., :32]), ValueError), (dict(v_cache=c.vc[1:]), ValueError),
+           (dict(k_cache=c.kc.transpose(2, 3)), ValueError), (dict(page_table=c.table.long()), TypeError), (dict(cu_q=c.cu_q[:1]), ValueError),
+           (dict(kv_lens=c.kv_lens.cpu()), ValueError), (dict(out=out[:, :2]), ValueError), (dict(out=out.to(torch.bfloat16)), TypeError),
+           (dict(lse=torch.zeros(1, 3, device=DEV)), ValueError), (dict(k_scale=torch.ones(2, device=DEV)), ValueError), (dict(max_q=0), q.QmmError),
+           (dict(window=-1), q.QmmError), (dict(scale=-1.0), q.QmmError), (dict(scale=math.nan), q.QmmError), (dict(max_q=1.5), TypeError),
+           (dict(k_cache=c.kc.to(E4M3), v_cache=c.vc.to(E4M3)), ValueError)]
+    for change, kind in bad:
+        with pytest.raises(kind):
+            q.paged_attention(**{**ok, **change})
+    k, v = (torch.zeros(1, 2, 64, device=DEV).half() for _ in range(2))
+    slots, pos, table = torch.zeros(1, dtype=torch.int64, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV), rope_table(4, 64)
+    before = c.kc.clone()
+    ok = dict(q=c.q, k=k, v=v, k_cache=c.kc, v_cache=c.vc, slots=slots, positions=pos, rope=table, out=out)
+    bad = [(dict(k=k[:, :1]), ValueError), (dict(v=v[..., :32]), ValueError), (dict(slots=slots.int()), TypeError), (dict(positions=None), ValueError),
+           (dict(rope=None), ValueError), (dict(rope=table.half()), TypeError), (dict(rope=table[:, ::2]), ValueError), (dict(q=None), ValueError),
+           (dict(rope=rope_table(4, 66)), q.QmmError), (dict(k=k.transpose(1, 2)), ValueError), (dict(k_cache=c.kc[:, :1]), ValueError)]
+    for change, kind in bad:
+        with pytest.raises(kind):
+            q.kv_append(**{**ok, **change})
+    assert (out == 7).all() and same(c.kc, before)
+    X = torch.zeros(2, 64, device=DEV).half()
+    wq, s, z = weights(64, 10, 4, 32, True, gen(1))
+    y = torch.full((2, 10), 7.0, device=DEV).half()
+    ok = dict(X=X, wq=wq, s=s, z=z, bits=4, G=32, out=y)
+    bad = [(dict(X=X[0]), ValueError), (dict(X=X.float()), TypeError), (dict(X=torch.zeros(64, 2, device=DEV).half().t()), ValueError), (dict(wq=wq[:9]), ValueError),
+           (dict(bits=5), ValueError), (dict(bits=9), ValueError), (dict(G=64), ValueError), (dict(s=s.float()), TypeError), (dict(z=z[:, :1]), ValueError),
+           (dict(bias=torch.zeros(9, device=DEV).half()), ValueError), (dict(mul=y[:1]), ValueError), (dict(residual=y.float()), TypeError),
+           (dict(act="swish"), ValueError), (dict(out=y.t()), ValueError), (dict(bias=torch.zeros(10).half()), ValueError)]
+    for change, kind in bad:
+        with pytest.raises(kind):
+            q.linear(**{**ok, **change})
+    torch.cuda.synchronize()
+    assert (y == 7).all()
