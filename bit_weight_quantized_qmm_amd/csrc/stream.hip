@@ -11,6 +11,12 @@
 // rounding by s; each dequantised run meets the RB blocks of 16 rows in turn.
 // Where there is more than one slice the sums go to the workspace in fp32 and
 // stream_join_kernel adds the slices in order and applies the epilogue.
+// Measured at K 28672, N 8192, 4 bits, G 128 with zero-points, 16 rows: 27 us (and 4.6
+// for the join) where the weights come from the last-level cache, 38.9 a call with
+// weights from HBM, 3.2 TB/s; without the unpacking 23.5, without X too 22.7, 2 steps in
+// flight instead of 4: 30.9.  16 waves hold the whole column tiles of a CU's share; K
+// split over the waves of a workgroup instead (X fragments in registers, sums joined in
+// LDS) took 81.
 #define QMM_EPILOGUE
 #include <algorithm>
 
