@@ -566,29 +566,40 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DP <= 1
     const char *kbase = (const char *)a.k + (int64_t)hk * a.k_hs, *vbase = (const char *)a.v + (int64_t)hk * a.v_hs;
     const int32_t *table = a.table + (int64_t)b * a.table_s;
 
-    // Lane l looks up the tile's key number l: its page id, then its row's place in
-    // both caches, which the lanes that stage the row take from it.  A key past the
-    // end reads the last one's row and a bad page id page 0's: in bounds, and hidden.
-    auto key_of = [&](int tile) { return max(0, min(begin + KB * tile + lane, end - 1)); };
+    // Where the rows stand: every NW tiles each wave looks up one of the NW tiles after
+    // the current ones, lane l the key number l of it, and leaves the key's place in both
+    // caches in LDS (2 NW slots), with two masks: keys that some row may see, keys on
+    // bad pages.  A key past the end takes the last one's place and a bad page id page
+    // 0's: in bounds, and hidden.
+    constexpr int SLOTS = 2 * NW;
+    int4_t *places = reinterpret_cast<int4_t *>(att_tiles + 4 * TILE);                 // [SLOTS][KB]: K low, high, V low, high
+    int4_t *masks = places + SLOTS * KB;                                               // [SLOTS]: seen low, high, bad low, high
+    auto key_of = [&](int tile) { return max(0, min(begin + KB * tile + (lane & (KB - 1)), end - 1)); };
     auto ids_of = [&](int tile) { return table[key_page(a, key_of(tile))]; };
+    auto look_up = [&](int tile, int pid) {
+        const int key = begin + KB * tile + (lane & (KB - 1)), at = key_of(tile) - key_page(a, key_of(tile)) * a.page;
+        const bool ok = (uint32_t)pid < (uint32_t)a.pages;
+        const uint64_t seen = __ballot(ok && key >= kr.lo && key < end), bad = __ballot(!ok);
+        const int pg = ok ? pid : 0, slot = tile % SLOTS;
+        const int64_t ko = (int64_t)pg * a.k_ps + (int64_t)at * a.k_ts, vo = (int64_t)pg * a.v_ps + (int64_t)at * a.v_ts;
+        if (lane < KB) places[slot * KB + lane] = int4_t{(int)(uint32_t)ko, (int)(ko >> 32), (int)(uint32_t)vo, (int)(vo >> 32)};
+        if (lane == 0) masks[slot] = int4_t{(int)(uint32_t)seen, (int)(uint32_t)(seen >> 32), (int)(uint32_t)bad, (int)(uint32_t)(bad >> 32)};
+    };
     const int srow = tid / CH, sp = tid % CH;             // this thread stages rows srow + SSTEP n, chunk sp
     constexpr int SSTEP = 64 * NW / CH;
     constexpr int PD = EB * 2;                            // dwords of a piece
     const int in_row = 8 * sp < a.D ? 8 * EB * sp : 0;
     int kst[LN][PD], vst[LN][PD];
-    uint64_t vlive = 0;                                   // staged keys that a row may see
-    auto load_tile = [&](int tile, int pid) {
-        const int key = begin + KB * tile + lane, at = key_of(tile) - key_page(a, key_of(tile)) * a.page;
-        const bool ok = (uint32_t)pid < (uint32_t)a.pages;
-        vlive = __ballot(ok && key >= kr.lo && key < end);
-        const int pg = ok ? pid : 0;
-        const int64_t ko = (int64_t)pg * a.k_ps + (int64_t)at * a.k_ts, vo = (int64_t)pg * a.v_ps + (int64_t)at * a.v_ts;
+    uint64_t vlive = 0, hidden = 0;                       // the masks of the staged tile
+    auto uniform64 = [](int lo, int hi) {
+        return ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane(hi) << 32) | (uint32_t)__builtin_amdgcn_readfirstlane(lo);
+    };
+    auto load_tile = [&](int tile) {
+        const int slot = tile % SLOTS;
+        const int4_t mk = masks[slot];
 #pragma unroll
         for (int n = 0; n < LN; ++n) {
-            auto row_at = [&](const char *base, int64_t off) {
-                const uint32_t lo = (uint32_t)__shfl((int)(uint32_t)off, srow + SSTEP * n), hi = (uint32_t)__shfl((int)(off >> 32), srow + SSTEP * n);
-                return base + (int64_t)(((uint64_t)hi << 32) | lo) + in_row;
-            };
+            const int4_t at = places[slot * KB + srow + SSTEP * n];
             auto load = [&](const char *src, int (&dst)[PD]) {
                 if constexpr (PD == 4) {
                     const int4_t w = *reinterpret_cast<const int4_t *>(src);
@@ -600,9 +611,11 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DP <= 1
                     dst[1] = w[1];
                 }
             };
-            load(row_at(kbase, ko), kst[n]);
-            load(row_at(vbase, vo), vst[n]);
+            load(kbase + (int64_t)(((uint64_t)(uint32_t)at[1] << 32) | (uint32_t)at[0]) + in_row, kst[n]);
+            load(vbase + (int64_t)(((uint64_t)(uint32_t)at[3] << 32) | (uint32_t)at[2]) + in_row, vst[n]);
         }
+        vlive = uniform64(mk[0], mk[1]);
+        hidden = uniform64(mk[2], mk[3]);
     };
     auto store_tile = [&](int buf) {
         auto put = [&](const int (&w)[PD], uint8_t *dst) {
@@ -649,16 +662,20 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DP <= 1
         for (int e = 0; e < 16; ++e) o[x][e] = 0.f;
 
     const int tiles = (max(0, end - begin) + KB - 1) / KB;
-    int pid = ids_of(0), pid1 = ids_of(1);
-    load_tile(0, pid);
+    look_up(wave, ids_of(wave));
+    int pid = ids_of(NW + wave);
+    __syncthreads();
+    load_tile(0);
+    uint64_t bad = hidden;
     store_tile(0);
     __syncthreads();
     for (int tile = 0; tile < tiles; ++tile) {
         const int buf = tile & 1, key0 = begin + KB * tile;
-        const uint64_t bad = __ballot((uint32_t)pid >= (uint32_t)a.pages);
-        pid = pid1;
-        load_tile(tile + 1, pid);
-        pid1 = ids_of(tile + 2);
+        load_tile(tile + 1);
+        if (tile % NW == 0) {
+            look_up(tile + NW + wave, pid);
+            pid = ids_of(tile + 2 * NW + wave);
+        }
         if (key0 < whi && key0 + KB > wlo) {
             const uint8_t *kl = att_tiles + buf * TILE;
             // operands are read from LDS KA steps ahead of the products that take them
@@ -747,6 +764,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DP <= 1
                 }
             }
         }
+        bad = hidden;
         store_tile(buf ^ 1);
         __syncthreads();
     }
@@ -901,7 +919,7 @@ static hipError_t tiles_go(const AttendArgs &a, hipStream_t st)
 {
     constexpr int NW = tiles_waves(DP);
     static bool attr_set = false;
-    const size_t lds = (size_t)4 * tiles_keys(DP) * DP * 2;
+    const size_t lds = (size_t)4 * tiles_keys(DP) * DP * 2 + 2 * NW * (tiles_keys(DP) + 1) * 16;   // tiles, places, masks
     if (!attr_set) {
         hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&attend_tiles_kernel<S, F8, DP, NW>),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
