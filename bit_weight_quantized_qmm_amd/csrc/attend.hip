@@ -512,14 +512,15 @@ __device__ __forceinline__ float16v_t mfma_32(int4_t a, int4_t b, float16v_t c, 
 __host__ __device__ constexpr int tiles_keys(int D) { return D <= 128 ? 64 : 32; }
 constexpr float ATT_LAZY = 8.f;        // a maximum may be exceeded by this much (base 2)
 
-template <typename S, bool F8, int DP, int NW>
-__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DP <= 128 ? 2 : 1, DP <= 128 ? 2 : 1))) void attend_tiles_kernel(const AttendArgs a)
+template <typename S, bool F8, int DC, int NW>
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DC <= 128 ? 2 : 1, DC <= 128 ? 2 : 1))) void attend_tiles_kernel(const AttendArgs a)
 {
+    constexpr int DP = DC == 96 ? 128 : DC;              // pitch of a row in LDS; DC elements of it are computed
     constexpr int KB = tiles_keys(DP), KT = KB / 32;     // keys of a tile, halves of 32 of them
     constexpr int EB = F8 ? 1 : 2;
     constexpr int CH = DP / 8;                           // 16-byte chunks of a row in LDS
     constexpr int LN = KB * CH / (64 * NW);          // chunks of K (and of V) a thread stages
-    constexpr int QJ = DP / 16, XT = DP / 32;
+    constexpr int QJ = DC / 16, XT = DC / 32;
     constexpr int TILE = KB * DP * 2;                // bytes
     auto swizzle_k = [](int row) { return CH == 8 ? (row >> 1) & 7 : row & 15; };
     auto swizzle_v = [](int row) { return CH == 8 ? 4 * ((row >> 1) & 1) : 4 * (row & 3); };
@@ -914,19 +915,19 @@ int64_t plan_attend(AttendArgs &a, bool e4m3)
     return a.splits > 1 ? (int64_t)a.T * a.Hq * a.splits * (a.D + 1) * 4 : 0;
 }
 
-template <typename S, bool F8, int DP>
+template <typename S, bool F8, int DC>
 static hipError_t tiles_go(const AttendArgs &a, hipStream_t st)
 {
-    constexpr int NW = tiles_waves(DP);
+    constexpr int DP = DC == 96 ? 128 : DC, NW = tiles_waves(DP);
     static bool attr_set = false;
     const size_t lds = (size_t)4 * tiles_keys(DP) * DP * 2 + 2 * NW * (tiles_keys(DP) + 1) * 16;   // tiles, places, masks
     if (!attr_set) {
-        hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&attend_tiles_kernel<S, F8, DP, NW>),
+        hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&attend_tiles_kernel<S, F8, DC, NW>),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
         if (e != hipSuccess) return e;
         attr_set = true;
     }
-    hipLaunchKernelGGL((attend_tiles_kernel<S, F8, DP, NW>), dim3((unsigned)((int64_t)a.B * a.rblocks * a.Hkv * a.splits)),
+    hipLaunchKernelGGL((attend_tiles_kernel<S, F8, DC, NW>), dim3((unsigned)((int64_t)a.B * a.rblocks * a.Hkv * a.splits)),
                        dim3(64 * NW), lds, st, a);
     return hipGetLastError();
 }
@@ -952,7 +953,6 @@ static hipError_t rows_go(const AttendArgs &a, hipStream_t st)
 template <typename S, bool F8, int DP, bool P16>
 static hipError_t rows_pick(const AttendArgs &a, hipStream_t st)
 {
-    if (a.rows > 32) return tiles_go<S, F8, DP>(a, st);
     if constexpr (DP <= 128) {
         if (a.rows == 32) return rows_go<S, F8, DP, P16, 2>(a, st);
     }
@@ -977,7 +977,10 @@ static hipError_t attend_type(const AttendArgs &a, hipStream_t st)
 {
     hipError_t e;
     const bool p16 = a.page % 16 == 0;
-    if (a.D <= 64)
+    if (a.rows > 32)
+        e = a.D <= 64 ? tiles_go<S, F8, 64>(a, st) : a.D <= 96 ? tiles_go<S, F8, 96>(a, st)
+                      : a.D <= 128 ? tiles_go<S, F8, 128>(a, st) : tiles_go<S, F8, 256>(a, st);
+    else if (a.D <= 64)
         e = p16 ? rows_pick<S, F8, 64, true>(a, st) : rows_pick<S, F8, 64, false>(a, st);
     else if (a.D <= 128)
         e = p16 ? rows_pick<S, F8, 128, true>(a, st) : rows_pick<S, F8, 128, false>(a, st);
