@@ -487,14 +487,16 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(rows_oc
 // stays below 2^8, O and l are rarely scaled, and nothing else changes.
 // Measured on two prompts of 4096 tokens, 32 heads of 128, fp16 (cycles of an XCD):
 // LDS operands read one by one as the compiler places them 899k, read ahead in
-// rings 799k, row places by one key a lane instead of scalar address chains 724k:
-// 356 us, 770 TFLOP/s.  Of 335 us in that form 67 go with the loads, their stores
-// to LDS and the K reads, 20 with the V reads, 26 with the softmax; the MFMAs and the
-// barriers alone take 222, twice the time of the instruction's nominal rate (a large fp16
-// matrix product reaches 1159 TFLOP/s).  Two waves of a SIMD in alternate phases
-// (two barriers a tile) were slower (356 against 335), as were raised wave
-// priorities for the products (no change) and one pair's row blocks on one XCD
-// (387).
+// rings 799k, row places by one key a lane instead of scalar address chains 724k
+// (348 us), looked up once for all waves 334 us: 823 TFLOP/s.  In the form before, of
+// 335 us (on a card with a higher clock) 67 went with the loads, their stores to LDS and
+// the K reads, 20 with the V reads, 26 with the softmax; the MFMAs and the barriers alone
+// took 222, twice the time of the instruction's nominal rate (a large fp16 matrix product
+// reaches 1159 TFLOP/s).  Slower: the two waves of a SIMD in alternate phases with two
+// barriers a tile (356 against 335), one pair's row blocks on one XCD (387), 256
+// workgroups with equal stretches of all tiles (453 against 334: row blocks of a head then
+// no longer read the same keys at the same time).  No change: raised wave priorities for
+// the products.
 // ---------------------------------------------------------------------------
 typedef float float16v_t __attribute__((ext_vector_type(16)));
 typedef short short4v_t __attribute__((ext_vector_type(4)));
