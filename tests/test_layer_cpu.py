@@ -84,9 +84,11 @@ def test_linear_refuses(kw):
 def test_linear_workspace():
     fn = lib().qmm_linear_workspace
     need = lambda **kw: fn(ctypes.cast(ctypes.pointer(linear(**kw)), P))
-    assert need(M=1, K=32768) == 0 and need(M=8, K=4096) == 0 and need(M=100, K=32768) == 0 and need(M=4, K=100) == 0
-    bytes_ = need(M=16, K=28672, N=8192)
-    assert bytes_ > 0 and bytes_ % (16 * 8192 * 4) == 0
+    assert need(M=1, K=32768) == 0 and need(M=8, K=4096) == 0 and need(M=4, K=100) == 0
+    assert need(M=100, K=64) == 0 and need(M=2048, K=4096, N=4096) == 0        # one step of K; a grid that fills the CUs
+    for M, K, N in (16, 28672, 8192), (100, 32768, 64):                        # streamed; K cut because one tile would leave CUs idle
+        bytes_ = need(M=M, K=K, N=N)
+        assert bytes_ > 0 and bytes_ % (M * N * 4) == 0
     assert fn(None) == 0
 
 
