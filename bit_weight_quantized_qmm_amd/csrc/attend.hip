@@ -4,7 +4,9 @@
 //
 // over the keys j that row i sees: j <= L - n + i (L keys in the sequence, n
 // of them new), and j > L - n + i - window where there is a window.  A row
-// that sees no key gives zeros and a log sum of -inf.
+// that sees no key gives zeros and a log sum of -inf.  A row whose scores are
+// all NaN, or all -inf by overflow, leaves m at -inf too: whether it sees a key is
+// asked of the table then, and if it does its output and log sum are NaN.
 //
 // One pass over the keys with a running maximum m and sum l (fp32), in base 2:
 // x is scaled by log2(e), so p is one v_exp_f32; O and l are scaled by
@@ -72,6 +74,18 @@ __device__ __forceinline__ KeyRange key_range(const AttendArgs &a, int b, int rb
 __device__ __forceinline__ int key_page(const AttendArgs &a, int key)
 {
     return (int)(((uint64_t)(uint32_t)key * a.page_mul) >> a.page_sh);
+}
+
+// Whether one of the keys [lo, hi) of sequence b stands on a page of the cache.
+// Asked of rows without a sum alone.
+__device__ __forceinline__ bool sees_key(const AttendArgs &a, int b, int64_t lo, int64_t hi)
+{
+    for (int64_t key = lo > 0 ? lo : 0; key < hi;) {
+        const int pg = key_page(a, (int)key);
+        if ((uint32_t)a.table[b * a.table_s + pg] < (uint32_t)a.pages) return true;
+        key = ((int64_t)pg + 1) * a.page;
+    }
+    return false;
 }
 
 // What turns a product into a base-2 exponent.  Never zero: a hidden key's -inf
@@ -447,10 +461,15 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(rows_oc
             tot += f * ml[(w * nrow + row) * 2 + 1];
             sum += f * *reinterpret_cast<const float4_t *>(att_lds + (w * nrow + row) * LD + d);
         }
-        const bool none = mm == -INFINITY;
-        const float inv = none ? 0.f : vs / tot;
         const int r = rb * a.rows + row, i = r / a.g, hq = hk * a.g + (r - i * a.g);
         const int64_t t = kr.t0 + i;
+        bool none = false;
+        if (!(tot > 0.f)) {     // (of a split only NaN: whether the others have a sum, the join sees)
+            const int hi = kr.L - kr.n + i + 1, lo = a.window > 0 ? hi - a.window : 0;
+            none = (a.splits > 1 && tot == 0.f) || !sees_key(a, b, max(begin, lo), min(end, hi));
+            tot = NAN;
+        }
+        const float inv = none ? 0.f : vs / tot;
 #pragma unroll
         for (int e = 0; e < 4; ++e) sum[e] = none ? 0.f : sum[e] * inv;
         const float lse2 = none ? -INFINITY : mm + __builtin_amdgcn_logf(tot);
@@ -774,7 +793,11 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DC <= 1
 
     l += __shfl_xor(l, 32);
     if (!live) return;
-    const bool none = m == -INFINITY;
+    bool none = false;
+    if (!(l > 0.f)) {     // (of a split only NaN: whether the others have a sum, the join sees)
+        none = (a.splits > 1 && l == 0.f) || !sees_key(a, b, max(begin, vlo), min(end, vhi));
+        l = NAN;
+    }
     const float inv = none ? 0.f : (F8 ? a.v_scale[hk] : 1.f) / l;
     const float lse2 = none ? -INFINITY : m + __builtin_amdgcn_logf(l);
     const int64_t t = kr.t0 + i, at = (t * a.Hq + hq) * a.splits + split;
@@ -857,11 +880,18 @@ __global__ __launch_bounds__(256) void attend_join_kernel(const AttendArgs a)
         }
     }
     if (!live) return;
-    sum *= mm == -INFINITY ? 0.f : 1.f / tot;
+    bool none = false;
+    if (!(tot > 0.f)) {
+        const int hi = kr.L - kr.n + i + 1, lo = a.window > 0 ? hi - a.window : 0;
+        none = !sees_key(a, b, lo, min(kr.L, hi));
+        tot = NAN;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] = none ? 0.f : sum[e] * (1.f / tot);
     if (lane < LN && d < a.D)
         *reinterpret_cast<int2v_t *>((char *)a.out + (int64_t)(kr.t0 + i) * a.o_ts + (int64_t)hq * a.o_hs + 2 * d) =
             int2v_t{pack2(sum[0], sum[1], (S)0.f), pack2(sum[2], sum[3], (S)0.f)};
-    if (a.lse && lane == 0) a.lse[row] = mm == -INFINITY ? -INFINITY : (mm + __builtin_amdgcn_logf(tot)) * ATT_LN2;
+    if (a.lse && lane == 0) a.lse[row] = none ? -INFINITY : (mm + __builtin_amdgcn_logf(tot)) * ATT_LN2;
 }
 
 // waves of a tiles workgroup: two a SIMD up to D = 128 (256 registers each), one

@@ -382,7 +382,8 @@ typedef struct qmm_attention_args {
  *     out_i = sum_j softmax_j(scale q_i . k_j) v_j,
  * query head h reading key head h / (Hq / Hkv).  n = 1 is decode, n = kv_len a
  * whole prompt.  A row that sees no key (kv_len 0, or below n) gives zeros and
- * an lse of -inf.  What stands in the caches behind a sequence's last key, or
+ * an lse of -inf; a row of q that holds NaN, and one whose scores all leave fp32
+ * for -inf, give NaN in both where they see a key.  What stands in the caches behind a sequence's last key, or
  * before every row's window, takes no part whatever it holds; a page id outside
  * 0 .. pages - 1 hides the keys of that page.  Keys and values that some row of
  * the sequence sees must be finite.  Products on f16 / bf16 MFMA with fp32 sums,

@@ -1,0 +1,80 @@
+"""Values at which the decoder-layer calls can go wrong without a fault.  On an MI355X."""
+import math
+
+import pytest
+import torch
+
+from test_layer_gpu import DEV, E4M3, SEQS, Paged, _announce, q  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# --------------------------------------------------------------- attention --
+def refill(c):
+    """c.k and c.v into the pages of the caches."""
+    for b, (_, L) in enumerate(c.seqs):
+        ids = c.table[b].tolist()
+        for p in range(-(-L // c.page)):
+            for cache, x in ((c.kc, c.k[b]), (c.vc, c.v[b])):
+                raw = (lambda t: t.view(torch.uint8)) if x.dtype == E4M3 else (lambda t: t)
+                part = raw(x)[p * c.page:(p + 1) * c.page].transpose(0, 1)
+                raw(cache[ids[p]])[:, :part.shape[1]] = part
+
+
+def rows_of(c):
+    """(row of q, whether it sees a key) of each sequence's first and last new token."""
+    t = 0
+    for n, L in c.seqs:
+        for i in {0, n - 1} if n else ():
+            yield t + i, L - n + i >= 0
+        t += n
+
+
+def spoiled(q, c, value, heads):
+    """Runs with `value` in the heads of some rows of q: those rows are NaN, or zeros and -inf where they see no key;
+    the others are as they would be without."""
+    good, good_lse = c.run(q)
+    clean = c.q.clone()
+    for t, _ in rows_of(c):
+        c.q[t, heads, 5 % c.D] = value
+    out, lse = c.run(q)
+    c.q.copy_(clean)
+    for t, sees in rows_of(c):
+        if sees:
+            assert torch.isnan(out[t, heads]).all() and torch.isnan(lse[t, heads]).all(), t
+            out[t, heads], lse[t, heads] = good[t, heads], good_lse[t, heads]
+    c.check(out, lse)      # rows without a key among them
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["plain", "e4m3"])
+@pytest.mark.parametrize("seqs", list(SEQS))
+@pytest.mark.parametrize("Hq,Hkv,D,page,dtype", [(8, 2, 128, 16, torch.float16), (32, 32, 64, 16, torch.bfloat16), (6, 2, 80, 7, torch.float16),
+                                                 (8, 1, 256, 64, torch.bfloat16)])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_attention_keeps_nan(q, seqs, e4m3, Hq, Hkv, D, page, dtype, value):
+    spoiled(q, Paged(SEQS[seqs], Hq, Hkv, D, page, dtype, e4m3, seed=D), value, [1, Hq - 1])
+
+
+@pytest.mark.parametrize("seqs", list(SEQS))
+def test_attention_overflow_is_nan(q, seqs):
+    """Scores that leave fp32 for -inf, all of a row's: not a row without keys."""
+    c = Paged(SEQS[seqs], 8, 2, 64, 16, torch.bfloat16, seed=3)
+    c.q[..., 5] = 0
+    for k in c.k:
+        k[..., 5] = -1e30
+    refill(c)
+    spoiled(q, c, 1e30, [0, 6])
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_attention_hidden_pages_of_a_nan_row(q, n):
+    """A NaN row whose keys all stand on bad pages sees none; one good page is enough to make it NaN."""
+    c = Paged([(n, 500), (n, 90)], 4, 2, 64, 16, torch.float16, seed=7)
+    c.q[:] = math.nan
+    good = c.table[1, 1].item()
+    c.table[:] = -1
+    c.table[1, 1] = good
+    out, lse = c.run(q)
+    assert (out[:n] == 0).all() and (lse[:n] == -math.inf).all()
+    sees = torch.arange(90 - n, 90, device=DEV) >= 16
+    assert torch.isnan(out[n:][sees]).all() and torch.isnan(lse[n:][sees]).all()
