@@ -88,11 +88,19 @@ __device__ __forceinline__ bool sees_key(const AttendArgs &a, int b, int64_t lo,
     return false;
 }
 
-// What turns a product into a base-2 exponent.  Never zero: a hidden key's -inf
-// stays -inf under it (a scale of 0 still gives every key the same weight).
+// What turns a product into a base-2 exponent.  Positive, or NaN as it is given: a
+// hidden key's -inf stays -inf under it and the maximum may be taken before it (a scale
+// of 0 still gives every key the same weight).  The sign of a head's scale goes into
+// q's: flip_q changes both elements of a dword.
 __device__ __forceinline__ float score_scale(const AttendArgs &a, bool f8, int hk)
 {
-    return fmaxf(a.scale * (f8 ? a.k_scale[hk] : 1.f) * ATT_LOG2E, 1e-37f);
+    const float x = __builtin_fabsf(a.scale * (f8 ? a.k_scale[hk] : 1.f) * ATT_LOG2E);
+    return x < 1e-37f ? 1e-37f : x;
+}
+__device__ __forceinline__ int4_t flip_q(const AttendArgs &a, int hk, int4_t q)
+{
+    const int flip = a.k_scale[hk] < 0.f ? (int)0x80008000u : 0;
+    return q ^ int4_t{flip, flip, flip, flip};
 }
 
 // ---------------------------------------------------------------------------
@@ -163,6 +171,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(rows_oc
         for (int j = 0; j < KJ; ++j) {
             const int d = F8 ? 64 * (j / 2) + 16 * g + 8 * (j & 1) : 32 * j + 8 * g;
             q[qt][j] = *reinterpret_cast<const int4_t *>(row + (d < a.D ? 2 * d : 0));
+            if constexpr (F8) q[qt][j] = flip_q(a, hk, q[qt][j]);
             if (!live || d >= a.D) q[qt][j] = int4_t{0, 0, 0, 0};
         }
     }
@@ -575,6 +584,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DC <= 1
         for (int j = 0; j < QJ; ++j) {
             const int d = 16 * j + 8 * h;
             q[j] = *reinterpret_cast<const int4_t *>(row + (d < a.D ? 2 * d : 0));
+            if constexpr (F8) q[j] = flip_q(a, hk, q[j]);
             if (!live || d >= a.D) q[j] = int4_t{0, 0, 0, 0};
         }
     }

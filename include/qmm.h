@@ -279,8 +279,8 @@ qmm_status qmm_quantize(const qmm_half *W, uint8_t *codes, qmm_half *s, qmm_half
  * (page: tokens a page, any number from 1 on); the strides of page, head and
  * token are given, the D elements of a token stand in a row.  A token's slot is
  * page_id * page + its place in the page.  Elements are fp16 or bf16 like q, or
- * e4m3 (OCP: largest 448, no infinity) with one fp32 scale a key head: an
- * element stands for its e4m3 value times the scale.
+ * e4m3 (OCP: largest 448, no infinity) with one fp32 scale a key head, of either
+ * sign: an element stands for its e4m3 value times the scale.
  * ------------------------------------------------------------------------- */
 
 /* element types */

@@ -78,3 +78,32 @@ def test_attention_hidden_pages_of_a_nan_row(q, n):
     assert (out[:n] == 0).all() and (lse[:n] == -math.inf).all()
     sees = torch.arange(90 - n, 90, device=DEV) >= 16
     assert torch.isnan(out[n:][sees]).all() and torch.isnan(lse[n:][sees]).all()
+
+
+@pytest.mark.parametrize("seqs", list(SEQS))
+@pytest.mark.parametrize("page", [16, 7])
+@pytest.mark.parametrize("factor", [-1.0, 0.0, -1e-30])
+def test_attention_scale_of_any_sign(q, seqs, page, factor):
+    """A key stands for its e4m3 value times the scale, whatever its sign."""
+    c = Paged(SEQS[seqs], 8, 2, 128, page, torch.float16, True, seed=9)
+    c.ks[1] *= factor
+    c.vs[0] *= -1
+    c.check(*c.run(q))
+
+
+@pytest.mark.parametrize("seqs", list(SEQS))
+def test_attention_nan_scale(q, seqs):
+    c = Paged(SEQS[seqs], 8, 2, 128, 16, torch.float16, True, seed=9)
+    good, good_lse = c.run(q)
+    scale = c.ks[1].clone()
+    c.ks[1] = math.nan
+    out, lse = c.run(q)
+    c.ks[1] = scale
+    t = 0
+    for n, L in c.seqs:
+        for i in range(n):
+            if L - n + i >= 0:
+                assert torch.isnan(out[t + i, 4:]).all() and torch.isnan(lse[t + i, 4:]).all()
+                out[t + i, 4:], lse[t + i, 4:] = good[t + i, 4:], good_lse[t + i, 4:]
+        t += n
+    c.check(out, lse)
