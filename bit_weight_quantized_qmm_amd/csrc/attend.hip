@@ -40,6 +40,16 @@ __device__ __forceinline__ float4_t mfma_16(int4_t a, int4_t b, float4_t c, bf16
 __device__ __forceinline__ int pack2(float x, float y, _Float16) { return __builtin_bit_cast(int, half2_t{(_Float16)x, (_Float16)y}); }
 __device__ __forceinline__ int pack2(float x, float y, bf16_t) { return __builtin_bit_cast(int, bf2x_t{(bf16_t)x, (bf16_t)y}); }
 
+// Probabilities meet the values in S.  fp16 is in full down to 2^-14 and ends at 2^-25:
+// with a row's largest at 1, keys more than 10 below it in the exponent would lose bits and
+// keys more than 17 below it would count in l alone, and beside a largest key without a
+// value a long row of them is all there is.  In fp16 p and l are therefore scaled by 2^15:
+// in full down to 2^-29 of the largest, off by 2^-40 of it beyond (2000 keys 15 below one
+// of value 0: 2.6 % off without).  bf16 has fp32's exponents.  No time: it is part of the
+// maximum that is subtracted.
+template <typename S> constexpr float ATT_TOP = 0.f;
+template <> constexpr float ATT_TOP<_Float16> = 15.f;
+
 // two e4m3 (low or high half of a dword) -> two elements; exact in both types
 template <bool HI> __device__ __forceinline__ int widen(int w, _Float16)
 {
@@ -392,10 +402,11 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(rows_oc
                     for (int xx = 0; xx < XT; ++xx) o[qt][xx] *= al;
                     m[qt] = mn;
                 }
+                const float base = ms - ATT_TOP<S>;
                 float sum = 0.f;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    x[e] = __builtin_amdgcn_exp2f(x[e] - ms);
+                    x[e] = __builtin_amdgcn_exp2f(x[e] - base);
                     sum += x[e];
                 }
                 l[qt] += sum;
@@ -481,7 +492,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(rows_oc
         const float inv = none ? 0.f : vs / tot;
 #pragma unroll
         for (int e = 0; e < 4; ++e) sum[e] = none ? 0.f : sum[e] * inv;
-        const float lse2 = none ? -INFINITY : mm + __builtin_amdgcn_logf(tot);
+        const float lse2 = none ? -INFINITY : mm - ATT_TOP<S> + __builtin_amdgcn_logf(tot);
         if (a.splits == 1) {
             *reinterpret_cast<int2v_t *>((char *)a.out + t * a.o_ts + (int64_t)hq * a.o_hs + 2 * d) =
                 int2v_t{pack2(sum[0], sum[1], tag), pack2(sum[2], sum[3], tag)};
@@ -511,8 +522,9 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(rows_oc
 // 16 lanes that read one chunk of 16 keys of K, and by 32 lanes that read four
 // chunks of 4 keys of V (with XORs that reach 8 chunks only, every read took
 // twice its time).
-// The maximum is raised only when a tile's exceeds it by more than 2^8: p then
-// stays below 2^8, O and l are rarely scaled, and nothing else changes.
+// The maximum is raised only when a tile's exceeds it by more than 2^4: O and l are
+// rarely scaled, and nothing else changes.  fp16 probabilities then keep 2^25 below the
+// largest in full and are off by 2^-36 of it beyond.
 // Measured on two prompts of 4096 tokens, 32 heads of 128, fp16 (cycles of an XCD):
 // LDS operands read one by one as the compiler places them 899k, read ahead in
 // rings 799k, row places by one key a lane instead of scalar address chains 724k
@@ -540,7 +552,7 @@ __device__ __forceinline__ float16v_t mfma_32(int4_t a, int4_t b, float16v_t c, 
 
 // keys of a tile: 64, and 32 beyond D = 128, where O^T and Q^T leave no registers for more
 __host__ __device__ constexpr int tiles_keys(int D) { return D <= 128 ? 64 : 32; }
-constexpr float ATT_LAZY = 8.f;        // a maximum may be exceeded by this much (base 2)
+constexpr float ATT_LAZY = 4.f;        // a maximum may be exceeded by this much (base 2)
 
 template <typename S, bool F8, int DC, int NW>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DC <= 128 ? 2 : 1, DC <= 128 ? 2 : 1))) void attend_tiles_kernel(const AttendArgs a)
@@ -552,6 +564,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DC <= 1
     constexpr int LN = KB * CH / (64 * NW);          // chunks of K (and of V) a thread stages
     constexpr int QJ = DC / 16, XT = DC / 32;
     constexpr int TILE = KB * DP * 2;                // bytes
+    constexpr float TOP = ATT_TOP<S> > 0.f ? ATT_TOP<S> - ATT_LAZY : 0.f;
     auto swizzle_k = [](int row) { return CH == 8 ? (row >> 1) & 7 : row & 15; };
     auto swizzle_v = [](int row) { return CH == 8 ? 4 * ((row >> 1) & 1) : 4 * (row & 3); };
     extern __shared__ __attribute__((aligned(16))) uint8_t att_tiles[];   // K [2][TILE], V [2][TILE]
@@ -774,11 +787,11 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DC <= 1
                 for (int x = 0; x < XT; ++x) o[x] *= al;
                 m = mn;
             }
-            const float ms = m == -INFINITY ? 0.f : m;
+            const float base = (m == -INFINITY ? 0.f : m) - TOP;
             float sum = 0.f;
 #pragma unroll
             for (int e = 0; e < 16 * KT; ++e) {
-                const float p = __builtin_amdgcn_exp2f(fmaf(s[e >> 4][e & 15], sl, -ms));
+                const float p = __builtin_amdgcn_exp2f(fmaf(s[e >> 4][e & 15], sl, -base));
                 sum += p;
                 s[e >> 4][e & 15] = p;
             }
@@ -809,7 +822,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DC <= 1
         l = NAN;
     }
     const float inv = none ? 0.f : (F8 ? a.v_scale[hk] : 1.f) / l;
-    const float lse2 = none ? -INFINITY : m + __builtin_amdgcn_logf(l);
+    const float lse2 = none ? -INFINITY : m - TOP + __builtin_amdgcn_logf(l);
     const int64_t t = kr.t0 + i, at = (t * a.Hq + hq) * a.splits + split;
     char *out = (char *)a.out + t * a.o_ts + (int64_t)hq * a.o_hs;
 #pragma unroll

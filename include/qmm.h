@@ -383,12 +383,14 @@ typedef struct qmm_attention_args {
  * query head h reading key head h / (Hq / Hkv).  n = 1 is decode, n = kv_len a
  * whole prompt.  A row that sees no key (kv_len 0, or below n) gives zeros and
  * an lse of -inf; a row of q that holds NaN, and one whose scores all leave fp32
- * for -inf, give NaN in both where they see a key.  What stands in the caches behind a sequence's last key, or
- * before every row's window, takes no part whatever it holds; a page id outside
- * 0 .. pages - 1 hides the keys of that page.  Keys and values that some row of
- * the sequence sees must be finite.  Products on f16 / bf16 MFMA with fp32 sums,
- * softmax in fp32, probabilities rounded once to q's type for the second
- * product.  Rows of q that no sequence has are left alone in out and lse.
+ * for -inf, give NaN in both where they see a key.  What stands in the caches
+ * behind a sequence's last key, or before every row's window, takes no part
+ * whatever it holds; a page id outside 0 .. pages - 1 hides the keys of that page.
+ * Keys and values that some row of the sequence sees must be finite.  Products on
+ * f16 / bf16 MFMA with fp32 sums, softmax in fp32, probabilities rounded once to
+ * q's type for the second product (in fp16 by half a step, or by 2^-36 of the
+ * row's largest where that is more).  Rows of q that no sequence has are left
+ * alone in out and lse.
  *   args   HOST struct, read during the call only
  * The workspace (scratch during the call: one for each stream that has calls in
  * flight) needs qmm_paged_attention_workspace() bytes; no call depends on what

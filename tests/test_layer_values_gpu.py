@@ -4,7 +4,7 @@ import math
 import pytest
 import torch
 
-from test_layer_gpu import DEV, E4M3, SEQS, Paged, _announce, q  # noqa: F401
+from test_layer_gpu import DEV, E4M3, SEQS, U, Paged, _announce, close, q  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -107,3 +107,34 @@ def test_attention_nan_scale(q, seqs):
                 out[t + i, 4:], lse[t + i, 4:] = good[t + i, 4:], good_lse[t + i, 4:]
         t += n
     c.check(out, lse)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("e4m3", [False, True], ids=["plain", "e4m3"])
+@pytest.mark.parametrize("n,B,L,Hkv", [(1, 8, 2000, 32), (20, 8, 2000, 32), (40, 8, 2000, 32), (1, 1, 5000, 32), (300, 1, 5000, 32)])
+def test_attention_far_below_the_largest(q, dtype, e4m3, n, B, L, Hkv):
+    """One key 11 to 19 above all others in the exponent, its value zero: the output is the others' share alone.
+
+    A probability is rounded once, by half a step of itself or, in fp16, by 2^-36 of the row's largest
+    where that is more (2^-25, half the smallest step, of a scale that puts the largest at 2^11 or above)."""
+    D, page, u = 64, 16, U[dtype]
+    c = Paged([(n, L)] * B, Hkv, Hkv, D, page, dtype, e4m3, seed=1)
+    c.q.fill_(1.0)
+    far = torch.linspace(11, 19, Hkv, device=DEV)
+    one = c.ks if e4m3 else torch.ones(Hkv, device=DEV)
+    for k, v in zip(c.k, c.v):
+        k.copy_(torch.zeros(L, Hkv, D, device=DEV).to(k.dtype))
+        v.copy_(torch.full((L, Hkv, D), 64.0, device=DEV).to(v.dtype))
+        k[0] = (far / 8 / one)[:, None].expand(Hkv, D).to(k.dtype)
+        v[0] = torch.zeros(Hkv, D, device=DEV).to(v.dtype)
+    refill(c)
+    out, lse = c.run(q)
+    top = c.k[0][0, :, 0].double() * one.double() * D * c.scale                       # [Hkv]
+    value = 64.0 * (c.vs.double() if e4m3 else torch.ones_like(top))
+    others = torch.arange(L - n, L, device=DEV, dtype=torch.float64)[:, None]         # keys but the first that row i sees
+    part = others * torch.exp(-top)
+    o = (part / (1 + part) * value).repeat(B, 1)[..., None].expand(B * n, Hkv, D)
+    rel = 2 * (D + 8) * 2.0 ** -24 * top + (L + 64) * 2.0 ** -24 + 2.0 ** -20
+    floor = L * 2.0 ** -36 * value if dtype is torch.float16 else torch.zeros_like(value)
+    close(out, o, (2 * u + rel[:, None]) * o + floor[:, None] + 2.0 ** -24)
+    close(lse, (top + torch.log1p(part)).repeat(B, 1), (rel + 2.0 ** -21 * (top + 1)).expand(B * n, Hkv))
