@@ -45,7 +45,7 @@ __device__ __forceinline__ float normal_tail(float x)
 __device__ __forceinline__ float activate(float h, int act)
 {
     switch (act) {
-        case ACT_RELU: return h > 0.f ? h : 0.f;
+        case ACT_RELU: return h < 0.f ? 0.f : h;   // NaN passes
         case ACT_SILU: return h * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * h));
         case ACT_GELU: {
             const float q = normal_tail(h);

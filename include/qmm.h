@@ -310,7 +310,7 @@ typedef struct qmm_linear_args {
  * with fp32 sums, everything after them in fp32 on those sums, rounded once to
  * fp16.  At M = 1 the product is qmm_gemv's; beyond, every weight is rounded to
  * fp16 at most once as in qmm_gemm (up to 16 rows and K = 8192: as in qmm_gemv).
- * relu takes NaN to 0.
+ * Every activation hands NaN on.
  *   args   HOST struct, read during the call only
  * The workspace (scratch during the call: one for each stream that has calls in
  * flight) needs qmm_linear_workspace() bytes: fp32 sums where K is cut into slices.

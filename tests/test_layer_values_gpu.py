@@ -4,7 +4,7 @@ import math
 import pytest
 import torch
 
-from test_layer_gpu import DEV, E4M3, SEQS, U, Paged, _announce, close, q  # noqa: F401
+from test_layer_gpu import DEV, E4M3, SEQS, U, Paged, _announce, close, gen, q, same, weights  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -138,3 +138,30 @@ def test_attention_far_below_the_largest(q, dtype, e4m3, n, B, L, Hkv):
     floor = L * 2.0 ** -36 * value if dtype is torch.float16 else torch.zeros_like(value)
     close(out, o, (2 * u + rel[:, None]) * o + floor[:, None] + 2.0 ** -24)
     close(lse, (top + torch.log1p(part)).repeat(B, 1), (rel + 2.0 ** -21 * (top + 1)).expand(B * n, Hkv))
+
+
+# ------------------------------------------------------------------ linear --
+# one token; the GEMVs; the streaming kernel with 16, 32 and 64 rows, with groups of 128 and others; the GEMM whole and in slices of K
+SHAPES = [(1, 4096, 1000, 128), (1, 16384, 70, 128), (3, 1024, 130, 64), (16, 1152, 264, 128), (7, 2080, 50, 32),
+          (2, 8320, 40, 128), (5, 16384, 33, 32), (16, 28672, 264, 128), (16, 8320, 17, 128), (11, 6144, 300, 64),
+          (17, 4096, 4100, 128), (32, 8320, 2001, 128), (20, 8192, 2001, 64), (29, 6272, 130, 128), (33, 28800, 600, 96), (64, 4224, 4000, 128), (50, 8192, 130, 128),
+          (40, 2080, 1000, 32), (130, 8192, 1032, 32), (111, 5760, 2001, 64), (263, 10240, 700, 128), (300, 4096, 1100, 128), (70, 256, 136, 64),
+          (1100, 256, 1032, 128)]
+
+
+@pytest.mark.parametrize("M,K,N,G", SHAPES, ids=lambda v: str(v))
+def test_linear_keeps_nan(q, M, K, N, G):
+    """A NaN activation reaches every output of its row through every epilogue, and no other row."""
+    g = gen(M)
+    X = torch.randn(M, K, generator=g, device=DEV).half()
+    wq, s, z = weights(K, N, 4, G, True, g)
+    mul, res = (torch.randn(M, N, generator=g, device=DEV).half() for _ in range(2))
+    row = M // 2
+    for act, m, r in (("none", None, None), ("relu", None, None), ("silu", mul, None), ("gelu", mul, res), ("gelu_tanh", None, res), ("relu", mul, res)):
+        X[row, K - 7] = 0.5
+        clean = q.linear(X, wq, s, z, 4, G, act=act, mul=m, residual=r)
+        X[row, K - 7] = math.nan
+        Y = q.linear(X, wq, s, z, 4, G, act=act, mul=m, residual=r)
+        assert torch.isnan(Y[row]).all(), act
+        rest = torch.arange(M, device=DEV) != row
+        assert same(Y[rest], clean[rest])
