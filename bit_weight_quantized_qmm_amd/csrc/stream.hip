@@ -82,8 +82,14 @@ __global__ __launch_bounds__(64 * stream_waves(RB)) void stream_kernel(const uin
     auto four = [&](const uint32_t (&w)[3], int st, uint16_t (&v)[D]) {
         const int first = first_group(st);
         const bool odd = (c * ng + first + (G128 ? 0 : 4 * g)) & 1;
-        const uint32_t lo = odd ? __builtin_amdgcn_alignbit(w[1], w[0], 16) : w[0];
-        const uint32_t hi = odd ? __builtin_amdgcn_alignbit(w[2], w[1], 16) : w[1];
+        uint32_t lo = odd ? __builtin_amdgcn_alignbit(w[1], w[0], 16) : w[0];
+        uint32_t hi = odd ? __builtin_amdgcn_alignbit(w[2], w[1], 16) : w[1];
+        if constexpr (G128) {
+            // past the slice's last step stand the next column's, which may be no numbers
+            const int left = (run1 - run0) / 4 - st;
+            lo &= left >= 2 ? 0xffffffffu : left == 1 ? 0xffffu : 0u;
+            hi &= left >= 4 ? 0xffffffffu : left == 3 ? 0xffffu : 0u;
+        }
 #pragma unroll
         for (int i = 0; i < D; ++i) {
             if constexpr (G128) {

@@ -165,3 +165,22 @@ def test_linear_keeps_nan(q, M, K, N, G):
         assert torch.isnan(Y[row]).all(), act
         rest = torch.arange(M, device=DEV) != row
         assert same(Y[rest], clean[rest])
+
+
+@pytest.mark.parametrize("M,K,N,G", [s for s in SHAPES if s[0] > 1], ids=lambda v: str(v))
+@pytest.mark.parametrize("what", ["s", "z"])
+def test_linear_columns_stand_alone(q, M, K, N, G, what):
+    """Scales or zero-points of one column that are infinite or NaN reach no other column."""
+    g = gen(N)
+    X = torch.randn(M, K, generator=g, device=DEV).half()
+    wq, s, z = weights(K, N, 4, G, True, g)
+    clean = q.linear(X, wq, s, z, 4, G)
+    for col, value in ((N // 2, math.inf), (N // 3, math.nan), (N - 1, math.inf), (0, math.nan)):
+        (s if what == "s" else z)[col] = value
+        Y = q.linear(X, wq, s, z, 4, G)
+        assert not torch.isfinite(Y[:, col]).any()
+        clean[:, col] = Y[:, col]
+        bad = ~torch.isfinite(Y)
+        assert torch.equal(bad, ~torch.isfinite(clean)), torch.unique(bad.nonzero()[:, 1]).tolist()[:8]
+        keep = ~bad
+        assert torch.equal(Y[keep], clean[keep])
