@@ -1,10 +1,13 @@
-"""Values at which the decoder-layer calls can go wrong without a fault.  On an MI355X."""
+"""Values at which the decoder-layer calls can go wrong without a fault: NaN and overflow, scales
+of any sign, keys far below a row's largest, and products that are exact, so that one lost
+code, run, group or slice shows.  On an MI355X.
+"""
 import math
 
 import pytest
 import torch
 
-from test_layer_gpu import DEV, E4M3, SEQS, U, Paged, _announce, close, gen, q, same, weights  # noqa: F401
+from test_layer_gpu import DEV, E4M3, SEQS, U, Paged, _announce, close, decoded, gen, q, same, weights  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -147,6 +150,45 @@ SHAPES = [(1, 4096, 1000, 128), (1, 16384, 70, 128), (3, 1024, 130, 64), (16, 11
           (17, 4096, 4100, 128), (32, 8320, 2001, 128), (20, 8192, 2001, 64), (29, 6272, 130, 128), (33, 28800, 600, 96), (64, 4224, 4000, 128), (50, 8192, 130, 128),
           (40, 2080, 1000, 32), (130, 8192, 1032, 32), (111, 5760, 2001, 64), (263, 10240, 700, 128), (300, 4096, 1100, 128), (70, 256, 136, 64),
           (1100, 256, 1032, 128)]
+
+
+@pytest.mark.parametrize("M,K,N,G", SHAPES, ids=lambda v: str(v))
+@pytest.mark.parametrize("bits", range(1, 9))
+@pytest.mark.parametrize("z", [False, True], ids=["", "z"])
+def test_linear_exact(q, M, K, N, G, bits, z):
+    """One +-1 in each run of 32 rows of K, powers of two as scales: every sum is exact in fp32 in
+    any order, so Y is the exact value rounded once, bit for bit."""
+    g = gen(K + bits)
+    runs = K // 32
+    assert runs * (1024 + 2 * 2 ** bits) * 8 < 2 ** 24     # in units of the smallest scale, the codes' offset of 1024 with them
+    X = torch.zeros(M, runs, 32, device=DEV, dtype=torch.float16)
+    at = torch.randint(0, 32, (M, runs, 1), generator=g, device=DEV)
+    X.scatter_(2, at, (torch.randint(0, 2, at.shape, generator=g, device=DEV) * 2 - 1).half())
+    X = X.view(M, K)
+    wq, s, zz = weights(K, N, bits, G, z, g)
+    s = 2.0 ** -torch.randint(4, 8, s.shape, generator=g, device=DEV).half()
+    w = (decoded(wq, K, bits) - (2.0 ** (bits - 1) if zz is None else zz.double().repeat_interleave(G, 1))) * s.double().repeat_interleave(G, 1)
+    h = X.double() @ w.T
+    assert same(q.linear(X, wq, s, zz, bits, G), h.half())
+    bias, res = (torch.randint(-8, 9, sh, generator=g, device=DEV).half() for sh in ((N,), (M, N)))
+    mul = (torch.randint(0, 2, (M, N), generator=g, device=DEV) * 1.5 - 1).half()          # -1 or 1/2
+    y = (h + bias.double()).clamp(min=0) * mul.double() + res.double()
+    Y = q.linear(X, wq, s, zz, bits, G, bias=bias, act="relu", mul=mul, residual=res)
+    assert torch.equal(Y.double(), y.half().double())
+
+
+@pytest.mark.parametrize("M,K,N,G", [s for s in SHAPES if s[0] > 16 or (s[0] > 1 and s[1] > 8192)], ids=lambda v: str(v))
+@pytest.mark.parametrize("bits,z", [(1, False), (2, True), (4, True), (5, False), (8, True)])
+def test_linear_rounding(q, M, K, N, G, bits, z):
+    """Weights rounded to fp16 once at most and fp32 sums.  X has random signs, so that the sum of the K roundings
+    has a standard deviation of 2^-11 (sum x^2 w^2)^(1/2) at most, and that of the sums one of 2^-24 K^(1/2) of
+    the same; 8 of them are allowed."""
+    g = gen(K + 10 * bits)
+    X = torch.randn(M, K, generator=g, device=DEV).half()
+    wq, s, zz = weights(K, N, bits, G, z, g)
+    w = (decoded(wq, K, bits) - (2.0 ** (bits - 1) if zz is None else zz.double().repeat_interleave(G, 1))) * s.double().repeat_interleave(G, 1)
+    h, size = X.double() @ w.T, (X.double() ** 2 @ (w.T ** 2).contiguous()).sqrt()
+    close(q.linear(X, wq, s, zz, bits, G), h, 8 * (2.0 ** -11 + 2.0 ** -24 * K ** 0.5) * size + 2.0 ** -11 * h.abs() + 2.0 ** -24)
 
 
 @pytest.mark.parametrize("M,K,N,G", SHAPES, ids=lambda v: str(v))
