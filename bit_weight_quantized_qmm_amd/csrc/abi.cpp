@@ -359,9 +359,6 @@ qmm_status qmm_paged_attention(const qmm_attention_args *p, qmm_stream stream)
     if (need > 0 && (!p->workspace || p->workspace_bytes < need || !aligned(p->workspace, 16)))
         return fail(QMM_ERR_INVALID_ARG, "%s: workspace missing, too small or not 16-byte aligned", fn);
     a.part = (float *)p->workspace;
-    const int64_t most = (int64_t(1) << 31) - 1;
-    if ((int64_t)a.B * a.rblocks > most / a.Hkv / a.splits || (int64_t)a.B > most / a.max_q / a.Hq)
-        return fail(QMM_ERR_UNSUPPORTED, "%s: grid beyond the supported range", fn);
     return hip_status(qmm::launch_attend(a, p->dtype == QMM_BF16, e4m3, (hipStream_t)stream), fn);
 }
 

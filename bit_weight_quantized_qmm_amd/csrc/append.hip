@@ -175,7 +175,7 @@ static hipError_t append_go(const AppendArgs &a, hipStream_t st)
 {
     constexpr int HP = 2;
     const int64_t blocks = ((int64_t)a.T * (a.D / (2 * V)) + 255) / 256 * ((a.Hq + 2 * a.Hkv + HP - 1) / HP);
-    if (blocks >= (int64_t(1) << 31)) return hipErrorNotSupported;
+    if (blocks * 256 >= (int64_t(1) << 32)) return hipErrorNotSupported;   // threads of a launch
     hipLaunchKernelGGL((append_kernel<S, C, PAIRS, V, HP>), dim3((unsigned)blocks), dim3(256), 0, st, a);
     return hipGetLastError();
 }

@@ -1016,14 +1016,20 @@ static hipError_t rows_pick(const AttendArgs &a, hipStream_t st)
 
 // A wave a row where the splits are few, the workgroup's four where a single
 // wave would read them in more than four rounds.
+static int join_waves(const AttendArgs &a) { return a.splits <= 4 * (256 / (a.D <= 64 ? 64 : a.D <= 128 ? 128 : 256)) ? 1 : 4; }
+static int64_t join_blocks(const AttendArgs &a)     // for each sequence
+{
+    const int64_t rows = (int64_t)a.max_q * a.Hq;
+    return join_waves(a) == 1 ? (rows + 3) / 4 : rows;
+}
 template <typename S, int DP>
 static hipError_t join_go(const AttendArgs &a, hipStream_t st)
 {
-    const int64_t rows = (int64_t)a.max_q * a.Hq;
-    if (a.splits <= 4 * (256 / DP))
-        hipLaunchKernelGGL((attend_join_kernel<S, DP, 1>), dim3((unsigned)((rows + 3) / 4 * a.B)), dim3(256), 0, st, a);
+    const dim3 grid((unsigned)(join_blocks(a) * a.B));
+    if (join_waves(a) == 1)
+        hipLaunchKernelGGL((attend_join_kernel<S, DP, 1>), grid, dim3(256), 0, st, a);
     else
-        hipLaunchKernelGGL((attend_join_kernel<S, DP, 4>), dim3((unsigned)(rows * a.B)), dim3(256), 0, st, a);
+        hipLaunchKernelGGL((attend_join_kernel<S, DP, 4>), grid, dim3(256), 0, st, a);
     return hipGetLastError();
 }
 
@@ -1047,8 +1053,19 @@ static hipError_t attend_type(const AttendArgs &a, hipStream_t st)
     return join_go<S, 256>(a, st);
 }
 
+// A launch takes fewer than 2^32 threads.  Both launches of a call are looked at before
+// the first: a call is made whole or not at all.
+static bool attend_fits(const AttendArgs &a)
+{
+    const int64_t most = (int64_t(1) << 32) - 1, groups = (int64_t)a.B * a.Hkv;
+    const int64_t threads = 64 * (a.rows > 32 ? tiles_waves(a.D) : ROWS_NW);
+    if (groups > most || a.rblocks * groups > most / threads / a.splits) return false;
+    return a.splits == 1 || join_blocks(a) <= most / 256 / a.B;
+}
+
 hipError_t launch_attend(const AttendArgs &a, bool bf16, bool e4m3, hipStream_t st)
 {
+    if (!attend_fits(a)) return hipErrorNotSupported;
     if (bf16) return e4m3 ? attend_type<bf16_t, true>(a, st) : attend_type<bf16_t, false>(a, st);
     return e4m3 ? attend_type<_Float16, true>(a, st) : attend_type<_Float16, false>(a, st);
 }

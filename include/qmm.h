@@ -350,7 +350,8 @@ typedef struct qmm_kv_append_args {
  * rot may be 0 (no rotation: positions and rope NULL).  T = 0 does nothing.
  * Errors: QMM_ERR_INVALID_ARG for null pointers, D odd or < 2, rot odd or
  * outside 0..D, sizes < 1, unknown types; QMM_ERR_UNSUPPORTED for pages * page
- * or T * D at 2^31 and beyond, or more than 65535 heads.  Rows whose starts and
+ * or T * D at 2^31 and beyond, more than 65535 heads, or a launch of 2^32 threads
+ * (one for every 4 to 32 elements of q, k and v).  Rows whose starts and
  * strides are multiples of 16 bytes, with rot and D - rot multiples of 16, move
  * fastest. */
 qmm_status qmm_kv_append(const qmm_kv_append_args *args, qmm_stream stream);
@@ -399,7 +400,8 @@ typedef struct qmm_attention_args {
  * negative or zero sizes, a bad scale or window, unknown types, a workspace too
  * small, starts or strides that are no multiples of 16 bytes;
  * QMM_ERR_UNSUPPORTED for D not a multiple of 16 in 16..256, or sizes beyond
- * 32-bit indexes (T * max(1, splits), keys, grid). */
+ * 32-bit indexes (T * Hq, keys) or a launch of 2^32 threads (B * Hkv * max_q /
+ * 256 workgroups and more). */
 qmm_status qmm_paged_attention(const qmm_attention_args *args, qmm_stream stream);
 
 /* Bytes of workspace that qmm_paged_attention takes for these arguments (from

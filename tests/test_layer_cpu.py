@@ -126,6 +126,24 @@ def test_attention_refuses(kw, want):
     assert status == want and "qmm_paged_attention" in text
 
 
+@pytest.mark.parametrize("kw", [
+    dict(B=1 << 23, max_kv=64, max_q=40, T=1 << 20, Hq=16),            # 2^23 blocks of 512 threads
+    dict(B=1 << 24, max_q=1, T=1 << 20, Hq=1, Hkv=1),                  # 2^24 blocks of 256
+    dict(B=1 << 14, max_q=1 << 17, T=1 << 17, Hq=2, Hkv=1, max_kv=64),
+    dict(B=1 << 22, max_q=1, T=1 << 20, Hq=16, Hkv=1, max_kv=12000, width=750),           # 2^23 blocks, two shares of the keys; 2^24 of the join
+    dict(B=(1 << 31) - 65536, max_q=1 << 20, T=1 << 20, Hq=64, Hkv=64)], ids=str)
+def test_attention_refuses_more_threads_than_a_launch_has(kw):
+    a = attention(**kw)
+    a.workspace, a.workspace_bytes = FAKE, 1 << 62
+    fn = lib().qmm_paged_attention
+    assert fn(ctypes.cast(ctypes.pointer(a), P), None) == UNSUPPORTED
+
+
+def test_append_refuses_more_threads_than_a_launch_has():
+    a = append(T=1 << 24, D=64, rot=2, Hq=16, Hkv=1)                   # single elements: 2^29 units for each pair of 18 heads
+    assert call("qmm_kv_append", a)[0] == UNSUPPORTED
+
+
 def test_attention_of_nothing():
     assert call("qmm_paged_attention", attention(T=0))[0] == OK
     assert call("qmm_paged_attention", attention(B=0))[0] == OK
