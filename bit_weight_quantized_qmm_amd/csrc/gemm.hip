@@ -450,7 +450,9 @@ static hipError_t gemm_whole(const GemvArgs &a, hipStream_t st);
 // step times of the tiles above, measured at K = N = 4096, k 4: a workgroup's step of
 // 128 rows of K takes 2.3 at 128 x 256, 1.6 at 128 x 128 (2 K parts), 1.03 at 64 x 128,
 // 0.75 at 64 x 64 (2 parts), 0.5 at 64 x 32 (4 parts), 0.3 at 32 x 16 (8 parts); slices
-// cost their sums' way to the workspace and back and a launch.
+// cost their sums' way to the workspace and back and a launch.  All of it from the sizes
+// and the MI355X's 256 CUs: the workspace that a caller asks for is then the launch's on
+// every device, and asking makes no HIP call.
 struct GemmSlices {
     int tile, slices, slice;
 };
@@ -458,7 +460,7 @@ static GemmSlices gemm_slices(int M, int K, int N)
 {
     static const struct { int bm, bn; double step; } kTiles[] = {{128, 256, 2.3}, {128, 128, 1.6}, {64, 128, 1.03},
                                                                  {64, 64, 0.75}, {64, 32, 0.5}, {32, 16, 0.3}};
-    const long long cus = gemm_cus(), need = (4 * cus + 4) / 5, steps = (K / 32 + 3) / 4;
+    const long long cus = 256, need = (4 * cus + 4) / 5, steps = (K / 32 + 3) / 4;
     auto tiles = [&](int i) { return (long long)((M + kTiles[i].bm - 1) / kTiles[i].bm) * ((N + kTiles[i].bn - 1) / kTiles[i].bn); };
     auto cost = [&](int i, long long s) {
         return (double)((tiles(i) * s + cus - 1) / cus) * (double)((steps + s - 1) / s) * kTiles[i].step +

@@ -2,6 +2,8 @@
 arithmetic of the planner's page division."""
 import ctypes
 import math
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -79,6 +81,33 @@ def attention(**kw):
 def test_linear_refuses(kw):
     status, text = call("qmm_linear", linear(**kw))
     assert status == INVALID and "qmm_linear" in text
+
+
+SHIM = """
+static int calls;
+int hipGetDevice(int *d) { (void)d; ++calls; return 100; }
+int hipDeviceGetAttribute(int *v, int a, int d) { (void)v, (void)a, (void)d; ++calls; return 100; }
+int made(void) { return calls; }
+"""
+PLAN = """
+import ctypes, sys
+shim = ctypes.CDLL(sys.argv[1], ctypes.RTLD_GLOBAL)      # its symbols come before the HIP library's
+lib = ctypes.CDLL(sys.argv[2])
+args = ctypes.create_string_buffer(bytes.fromhex(sys.argv[3]))
+lib.qmm_linear_workspace.restype = ctypes.c_int64
+print(lib.qmm_linear_workspace(args), lib.qmm_linear(args, None), shim.made())
+"""
+
+
+def test_linear_plans_without_hip_calls(tmp_path):
+    """The workspace follows from the sizes alone and a missing one is refused before any HIP call."""
+    (tmp_path / "shim.c").write_text(SHIM)
+    subprocess.run(["gcc", "-shared", "-fPIC", "-o", str(tmp_path / "shim.so"), str(tmp_path / "shim.c")], check=True)
+    for M, K, N in (100, 32768, 64), (300, 4096, 2000):
+        text = subprocess.run([sys.executable, "-c", PLAN, str(tmp_path / "shim.so"), qmm.library_path(), bytes(linear(M=M, K=K, N=N)).hex()], check=True,
+                              capture_output=True, text=True, timeout=120).stdout
+        need, status, calls = map(int, text.split())
+        assert need > 0 and status == INVALID and calls == 0
 
 
 def test_linear_workspace():
