@@ -231,6 +231,8 @@ PyObject *kv_append(PyObject *, PyObject *const *a, Py_ssize_t n)
                          &slots = tensor(a[5], "slots");
         qmm_kv_append_args p{};
         int index;
+        p.pairs = PyObject_IsTrue(a[8]);
+        if (p.pairs < 0) throw Raised{};
         p.dtype = leading(k, "k", index);
         const at::ScalarType type = k.scalar_type();
         p.T = k.size(0), p.Hkv = k.size(1), p.D = k.size(2);
@@ -262,7 +264,6 @@ PyObject *kv_append(PyObject *, PyObject *const *a, Py_ssize_t n)
         } else if (positions) {
             bad_value("positions without rope");
         }
-        p.pairs = PyObject_IsTrue(a[8]);
         p.k = at(&k), p.v = at(&v), p.k_cache = kc.mutable_data_ptr(), p.v_cache = vc.mutable_data_ptr();
         p.slots = (const int64_t *)at(&slots), p.positions = (const int32_t *)at(positions), p.rope = (const float *)at(rope);
         p.k_scale = (const float *)at(k_scale), p.v_scale = (const float *)at(v_scale);

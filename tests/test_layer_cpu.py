@@ -208,6 +208,13 @@ CPU = [(lambda x: qmm.linear(x, x, x, None, 4, 32), ValueError), (lambda x: qmm.
        (lambda x: qmm.paged_attention(x.float(), x, x, x, x, x, 1, 1), TypeError), (lambda x: qmm.paged_attention(x, x, [1], x, x, x, 1, 1), TypeError)]
 
 
+def test_binding_hands_on_an_error_of_pairs():
+    """A flag without a truth value (an array of several) ends the call with its own error."""
+    x = torch.zeros(2, 1, 64, dtype=torch.float16)
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        qmm.kv_append(None, x, x, x, x, x, pairs=torch.tensor([True, False]))
+
+
 @pytest.mark.parametrize("i", range(len(CPU)))
 def test_binding_refuses_cpu_tensors(i):
     """Tensors of the host, of other types and no tensors at all: an error of Python, no call."""
