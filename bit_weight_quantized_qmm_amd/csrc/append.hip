@@ -24,13 +24,6 @@
 
 namespace qmm {
 
-template <typename S>
-__device__ __forceinline__ void put(S *p, const float *x, int n)
-{
-#pragma unroll
-    for (int i = 0; i < n; ++i) p[i] = from_f32<S>(x[i]);
-}
-
 template <int V> struct VecBytes;
 template <> struct VecBytes<16> { typedef int4_t t; };
 template <> struct VecBytes<8> { typedef int t __attribute__((ext_vector_type(2))); };
