@@ -308,7 +308,8 @@ def kv_append(q, k, v, k_cache, v_cache, slots, positions=None, rope=None, pairs
     slots int64 [T]: page id * page + place, or -1 (padding: nothing is stored); positions int32
     [T]: rows of rope, fp32 [rows, rot] with rot/2 cosines and then rot/2 sines (None: no rotation).
     pairs: elements 2i and 2i + 1 turn together (False: i and i + rot/2).  q may be None (k and v
-    alone); q, k and v may be slices of one projection, out may be q."""
+    alone); q, k and v may be slices of one projection, out may be q.  D may be any even number
+    here; paged_attention reads caches of D a multiple of 16 up to 256."""
     return _binding.kv_append(q, k, v, k_cache, v_cache, slots, positions, rope, pairs, k_scale, v_scale, out)
 
 

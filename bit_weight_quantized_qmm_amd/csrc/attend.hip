@@ -132,7 +132,10 @@ __device__ __forceinline__ int4_t flip_q(const AttendArgs &a, int hk, int4_t q)
 // lies behind it reads as zeros.  Other page sizes take a lane's key from its
 // own page; the rows' offsets are computed once for each key and handed round.
 // Measured: 64 users of up to 8192 keys, 8 key heads of 128 for 32, fp16: 203 us,
-// 5.2 TB/s (a plain streaming read reaches 6.1); 4 of up to 131071, e4m3: 168 us, 5.6 TB/s.
+// 5.2 TB/s (a plain streaming read of 1 GB reaches 7.1); 4 of up to 131071, e4m3: 167 us, 5.6 TB/s.
+// The registers of two waves a SIMD do not hold D = 256 in fp16 or bf16: 27 are spilled (45
+// with other page sizes; 7 with those at D = 128 and three waves).  64 users of up to 4096
+// keys, D 256: 375 us, 4.3 TB/s.
 // ---------------------------------------------------------------------------
 __host__ __device__ constexpr int rows_occupancy(int DP, int QT) { return DP <= 128 && QT == 1 ? 3 : 2; }
 

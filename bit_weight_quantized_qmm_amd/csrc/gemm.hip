@@ -450,7 +450,13 @@ static hipError_t gemm_whole(const GemvArgs &a, hipStream_t st);
 // step times of the tiles above, measured at K = N = 4096, k 4: a workgroup's step of
 // 128 rows of K takes 2.3 at 128 x 256, 1.6 at 128 x 128 (2 K parts), 1.03 at 64 x 128,
 // 0.75 at 64 x 64 (2 parts), 0.5 at 64 x 32 (4 parts), 0.3 at 32 x 16 (8 parts); slices
-// cost their sums' way to the workspace and back and a launch.  All of it from the sizes
+// cost their sums' way to the workspace and back and a launch.  Taken for every width: the
+// dispatch's tile and this choice, us, at 1 bit, 4 bits and 8 bits with zero-points:
+//   300 rows, 4096 x 11008   93 66    86 66   119 96
+//   111 rows, 11392 x 8246  107 61   105 58   140 69
+//   263 rows, 10240 x 700    44 25    43 25    54 31
+//   200 rows, 8192 x 4096    44 47    43 45    53 53
+// All of it from the sizes
 // and the MI355X's 256 CUs: the workspace that a caller asks for is then the launch's on
 // every device, and asking makes no HIP call.
 struct GemmSlices {

@@ -268,8 +268,17 @@ bool stream_takes(int M, int K, int N)
     // to K = 8192; beyond, they take K in passes (K 28672, N 8192, 16 rows, 4 bits: 60 us,
     // here 39).  From 17 on the GEMM's smallest tiles leave CUs idle or dequantise every
     // weight again for each tile of rows; it is quicker for small products alone, where
-    // the join's launch counts (17 rows, 4096 x 4096: 10.0 and 11.3 us; 33 rows: 18.7
-    // and 12.7; 32 rows, 4096 x 11008: 30 and 15.7).
+    // the join's launch counts.  The GEMM and here, 4 bits, us:
+    //   K x N            17 rows      32           33           64
+    //   2048 x 4096    6.8   9.1   7.7   9.7   12.6  10.4   13.6  11.4
+    //   4096 x 3000   11.2   9.0  10.9   9.6   13.5  10.6   18.0  12.5
+    //   4096 x 4096   11.4   9.5  11.1  10.3   13.4  11.4   18.1  14.3
+    //   8192 x 2048   11.7   9.5  13.5  10.7   13.9  12.0   19.6  14.5
+    //   2048 x 8192   10.1   9.9  10.3  10.9   11.1  12.1   12.2  14.4
+    //   4096 x 6000   14.7  10.9  16.4  11.9   16.6  14.0   20.7  15.6
+    //   4096 x 11008  22.2  13.4  22.6  14.1   22.9  22.4   26.9  24.5
+    // K N = 14M parts these but for the second row and, by up to a fifth, for long rows of
+    // few steps (K 2048, N 8192) and 33 rows and more of the first; 2 and 8 bits lie alike.
     // A few columns of long K are one or two workgroups' work for either of them (16 rows,
     // K 7808, N 2: 14.8 us, in slices 9.3).
     if (M < 2 || M > 64) return false;
