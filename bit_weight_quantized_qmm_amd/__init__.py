@@ -321,7 +321,9 @@ def paged_attention(q, k_cache, v_cache, page_table, cu_q, kv_lens, max_q: int, 
     keys, the new tokens' among them; max_q and max_kv: upper bounds of both (host integers: nothing
     is read back).  scale: D ** -0.5 if None; window > 0: a row sees its last `window` keys alone;
     lse fp32 [T, Hq] (written if given): the log of each row's sum.  A row that sees no key gives
-    zeros and -inf.  One call serves decode (one row each), chunks and whole prompts mixed."""
+    zeros and -inf.  One call serves decode (one row each), chunks and whole prompts mixed; it is
+    planned by max_q, so that decode rows on long contexts beside a prompt are quicker in a call of
+    their own (one row on 131072 keys, a prompt of 2048: 2429 us in one call, 171 in two)."""
     return _binding.paged_attention(q, k_cache, v_cache, page_table, cu_q, kv_lens, max_q, max_kv, scale, window, k_scale, v_scale, out,
                                     lse)
 
