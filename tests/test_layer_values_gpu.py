@@ -58,6 +58,14 @@ def test_attention_keeps_nan(q, seqs, e4m3, Hq, Hkv, D, page, dtype, value):
     spoiled(q, Paged(SEQS[seqs], Hq, Hkv, D, page, dtype, e4m3, seed=D), value, [1, Hq - 1])
 
 
+@pytest.mark.parametrize("e4m3", [False, True], ids=["plain", "e4m3"])
+@pytest.mark.parametrize("page", [16, 7])
+@pytest.mark.parametrize("window", [0, 100])
+def test_attention_keeps_nan_short_chunks(q, e4m3, page, window):
+    """Two blocks of 16 rows a key head, and a window before which pages are gone."""
+    spoiled(q, Paged([(5, 5), (4, 300), (8, 2000), (3, 0), (7, 4)], 8, 2, 128, page, torch.float16, e4m3, window=window, seed=2), math.nan, [1, 7])
+
+
 @pytest.mark.parametrize("seqs", list(SEQS))
 def test_attention_overflow_is_nan(q, seqs):
     """Scores that leave fp32 for -inf, all of a row's: not a row without keys."""
