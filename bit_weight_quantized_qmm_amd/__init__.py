@@ -14,6 +14,7 @@ from __future__ import annotations
 import ctypes
 import importlib.util
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -21,10 +22,11 @@ from ._build import BINDING, LIBRARY
 
 __all__ = ["QmmError", "packed_bytes", "pack", "pack_signed", "unpack", "gemv", "gemv_grouped", "gemv_lut", "gemm", "gemm_fp", "FP4_E2M1",
            "FP8_E4M3", "FP6_E3M2", "FP6_E2M3", "FP3_E1M1", "FP5_E2M2", "FP7_E3M3", "gemm_w4a8", "gemm_wka8", "quantize", "linear", "kv_append",
-           "paged_attention", "probe_read", "probe_mfma", "library_path", "SYMBOLS"]
+           "paged_attention", "qk_norm", "KV4Cache", "kv4_cache", "kv4_append", "kv4_read", "kv4_attention", "probe_read", "probe_mfma", "library_path", "SYMBOLS"]
 
 SYMBOLS = ("qmm_packed_bytes", "qmm_pack", "qmm_pack_signed", "qmm_unpack", "qmm_gemv", "qmm_gemv_grouped", "qmm_gemv_lut", "qmm_gemm", "qmm_gemm_fp", "qmm_gemm_w4a8", "qmm_gemm_wka8",
-           "qmm_quantize", "qmm_linear", "qmm_linear_workspace", "qmm_kv_append", "qmm_paged_attention", "qmm_paged_attention_workspace", "qmm_status_string", "qmm_last_error", "qmm_last_hip_error", "qmm_probe_read",
+           "qmm_quantize", "qmm_linear", "qmm_linear_workspace", "qmm_kv_append", "qmm_paged_attention", "qmm_paged_attention_workspace",
+           "qmm_qk_norm", "qmm_kv4_append", "qmm_kv4_read", "qmm_kv4_attention", "qmm_kv4_attention_workspace", "qmm_status_string", "qmm_last_error", "qmm_last_hip_error", "qmm_probe_read",
            "qmm_probe_mfma")
 
 
@@ -57,6 +59,11 @@ def _load():
         "qmm_kv_append": ([P, P], INT),
         "qmm_paged_attention": ([P, P], INT),
         "qmm_paged_attention_workspace": ([P], I64),
+        "qmm_qk_norm": ([P, P], INT),
+        "qmm_kv4_append": ([P, P], INT),
+        "qmm_kv4_read": ([P, P], INT),
+        "qmm_kv4_attention": ([P, P], INT),
+        "qmm_kv4_attention_workspace": ([P], I64),
         "qmm_status_string": ([INT], ctypes.c_char_p),
         "qmm_last_error": ([], ctypes.c_char_p),
         "qmm_last_hip_error": ([], ctypes.c_char_p),
@@ -279,7 +286,8 @@ def _load_binding():
     spec = importlib.util.spec_from_file_location("_binding", BINDING)
     mod = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(mod)
-    entry = (_lib.qmm_linear, _lib.qmm_linear_workspace, _lib.qmm_kv_append, _lib.qmm_paged_attention, _lib.qmm_paged_attention_workspace)
+    entry = (_lib.qmm_linear, _lib.qmm_linear_workspace, _lib.qmm_kv_append, _lib.qmm_paged_attention, _lib.qmm_paged_attention_workspace,
+             _lib.qmm_qk_norm, _lib.qmm_kv4_append, _lib.qmm_kv4_read, _lib.qmm_kv4_attention, _lib.qmm_kv4_attention_workspace)
     mod.connect(*(ctypes.cast(f, ctypes.c_void_p).value for f in entry), _check, torch._C._cuda_getCurrentRawStream,
                 torch._C._cuda_getDevice, torch._C._cuda_setDevice)
     return mod
@@ -326,6 +334,65 @@ def paged_attention(q, k_cache, v_cache, page_table, cu_q, kv_lens, max_q: int, 
     their own (one row on 131072 keys, a prompt of 2048: 2429 us in one call, 171 in two)."""
     return _binding.paged_attention(q, k_cache, v_cache, page_table, cu_q, kv_lens, max_q, max_kv, scale, window, k_scale, v_scale, out,
                                     lse)
+
+
+def qk_norm(q, k, q_weight=None, k_weight=None, eps: float = 1e-6, positions=None, rope=None, pairs: bool = False, q_out=None, k_out=None):
+    """RMS norms of q [T, Hq, D] and k [T, Hkv, D] for each head, x / sqrt(mean(x^2) + eps) * weight, and
+    their rotary positions, in one pass.  Returns (q, k).
+
+    q_weight and k_weight: [D] of q's type (None: no norm); positions, rope and pairs as in kv_append.
+    q and k may be slices of one projection, q_out and k_out may be q and k.  D and rope's width:
+    multiples of 16, D up to 256."""
+    return _binding.qk_norm(q, k, q_weight, k_weight, eps, positions, rope, pairs, q_out, k_out)
+
+
+class KV4Cache(NamedTuple):
+    """A paged cache of 4-bit codes (any tuple of four such tensors will do where one is asked for).
+
+    The D elements of a token and head are D / 2 bytes, the lower half of each first; x = (code - z) s with
+    the s and z of its group of G elements."""
+    k: torch.Tensor            # uint8 [pages, heads, page, D / 2]
+    v: torch.Tensor
+    k_scale: torch.Tensor      # fp16 [pages, heads, page, D / G, 2]: s and z
+    v_scale: torch.Tensor
+
+
+def kv4_cache(pages: int, heads: int, page: int, D: int, G: int | None = None, device="cuda") -> KV4Cache:
+    """An empty cache of 4-bit codes: G (32, 64 or 128; None: the largest that divides D) elements share a scale."""
+    if G is None:
+        G = next((g for g in (128, 64, 32) if D % g == 0), 0)
+    if G not in (32, 64, 128) or D % G or not 0 < D <= 256:
+        raise ValueError(f"G must be 32, 64 or 128 and D a multiple of it up to 256, got D = {D}, G = {G}")
+    codes = [torch.zeros(pages, heads, page, D // 2, dtype=torch.uint8, device=device) for _ in range(2)]
+    return KV4Cache(*codes, *(torch.zeros(pages, heads, page, D // G, 2, dtype=torch.float16, device=device) for _ in range(2)))
+
+
+def kv4_append(q, k, v, cache, slots, positions=None, rope=None, pairs: bool = False, q_norm=None, k_norm=None, eps: float = 1e-6, out=None):
+    """qk_norm's norms and rotations of q [T, Hq, D] and k [T, Hkv, D], each where it is asked for, and k and v
+    [T, Hkv, D] into a cache of 4-bit codes.  Returns q after them (None without q).
+
+    Each group of G elements is mapped as quantize maps weights, min to max with zero in the range, with
+    a scale of 7 significant bits: what the cache then stands for are numbers of fp16.  Elements beyond
+    +-57344 are stored as that; a group with NaN reads as NaN.  slots, positions, rope and pairs as in
+    kv_append; two tokens of a call must not share a slot.  out may be q."""
+    return _binding.kv4_append(q, k, v, cache, slots, positions, rope, pairs, q_norm, k_norm, eps, out)
+
+
+def kv4_read(cache, slots, dtype: torch.dtype = torch.float16, k_out=None, v_out=None):
+    """The keys and values at these slots (int64 [T]) of a cache of 4-bit codes: two tensors [T, Hkv, D] of fp16
+    (exactly what kv4_attention multiplies by) or bf16.  A slot outside the cache, as -1, gives zeros."""
+    if dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError(f"dtype must be float16 or bfloat16, got {dtype}")
+    return _binding.kv4_read(cache, slots, dtype == torch.bfloat16, k_out, v_out)
+
+
+def kv4_attention(q, cache, page_table, cu_q, kv_lens, max_q: int, max_kv: int, scale=None, window: int = 0, sinks: int = 0, out=None,
+                  lse=None) -> torch.Tensor:
+    """paged_attention over a cache of 4-bit codes.
+
+    window > 0: a row sees its last `window` keys and, of those before them, the sequence's first
+    `sinks`.  The other arguments as in paged_attention."""
+    return _binding.kv4_attention(q, cache, page_table, cu_q, kv_lens, max_q, max_kv, scale, window, sinks, out, lse)
 
 
 def probe_read(buf: torch.Tensor, grid: int, sink: torch.Tensor | None = None) -> None:

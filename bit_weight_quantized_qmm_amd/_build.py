@@ -22,7 +22,7 @@ BINDING = os.path.join(PKG, "_binding.so")
 EPILOGUE = ["-DQMM_EPILOGUE"]
 SOURCES = [("gemv.hip", "", []), ("gemv.hip", ".linear", EPILOGUE), ("gemm.hip", "", []), ("gemm.hip", ".linear", EPILOGUE),
            ("w4a8.hip", "", []), ("stream.hip", "", []), ("abi.cpp", "", []), ("pack.hip", "", []), ("quantize.hip", "", []), ("probe.hip", "", []),
-           ("lut.hip", "", []), ("append.hip", "", []), ("attend.hip", "", [])]
+           ("lut.hip", "", []), ("append.hip", "", []), ("attend.hip", "", []), ("heads.hip", "", []), ("attend4.hip", "", [])]
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 DEVICE_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]

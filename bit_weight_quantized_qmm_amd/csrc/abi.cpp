@@ -7,6 +7,9 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <initializer_list>
+#include <utility>
+
 #include "launch.hpp"
 
 namespace {
@@ -360,6 +363,190 @@ qmm_status qmm_paged_attention(const qmm_attention_args *p, qmm_stream stream)
         return fail(QMM_ERR_INVALID_ARG, "%s: workspace missing, too small or not 16-byte aligned", fn);
     a.part = (float *)p->workspace;
     return hip_status(qmm::launch_attend(a, p->dtype == QMM_BF16, e4m3, (hipStream_t)stream), fn);
+}
+
+// A cache of 4-bit codes: sizes, groups, then pointers and strides.
+static qmm_status kv4_shape(const char *fn, const qmm_kv4_cache &c)
+{
+    if (c.Hkv < 1 || c.page < 1 || c.pages < 1 || c.D < 1 || c.G < 1)
+        return fail(QMM_ERR_INVALID_ARG, "%s: the cache's sizes must be >= 1", fn);
+    if (c.D % c.G != 0) return fail(QMM_ERR_INVALID_ARG, "%s: D must be a multiple of G", fn);
+    if ((c.G != 32 && c.G != 64 && c.G != 128) || c.D > 256)
+        return fail(QMM_ERR_UNSUPPORTED, "%s: G must be 32, 64 or 128, D a multiple of it up to 256", fn);
+    const int64_t lim = int64_t(1) << 31;
+    if (c.Hkv > 65535 || c.page > (1 << 20) || c.pages >= lim || c.pages * c.page >= lim)
+        return fail(QMM_ERR_UNSUPPORTED, "%s: size beyond the supported range", fn);
+    return QMM_OK;
+}
+static qmm_status kv4_places(const char *fn, const qmm_kv4_cache &c)
+{
+    if (!c.k || !c.v || !c.k_scale || !c.v_scale) return fail(QMM_ERR_INVALID_ARG, "%s: null pointer", fn);
+    bool even = aligned(c.k, 16) && aligned(c.v, 16) && aligned(c.k_scale, 4) && aligned(c.v_scale, 4);
+    for (int i = 0; i < 3; ++i) even = even && c.k_stride[i] % 16 == 0 && c.v_stride[i] % 16 == 0;
+    for (int i = 0; i < 2; ++i) even = even && c.k_scale_stride[i] % 2 == 0 && c.v_scale_stride[i] % 2 == 0;
+    if (!even)
+        return fail(QMM_ERR_INVALID_ARG, "%s: codes must start at multiples of 16 bytes, scales at multiples of 4", fn);
+    if (c.k_stride[2] < 0 || c.v_stride[2] < 0 || c.k_stride[2] > (1 << 24) || c.v_stride[2] > (1 << 24))   // 64 tokens of it stay below 2^31
+        return fail(QMM_ERR_UNSUPPORTED, "%s: token strides of the codes must be 0 to 2^24 bytes", fn);
+    return QMM_OK;
+}
+static qmm_status heads_shape(const char *fn, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t rot, int64_t table_rows, double eps, int dtype)
+{
+    if (T < 0 || Hq < 0 || Hkv < 0) return fail(QMM_ERR_INVALID_ARG, "%s: T and the heads must be >= 0", fn);
+    if (D < 1 || rot < 0 || rot % 2 != 0 || rot > D) return fail(QMM_ERR_INVALID_ARG, "%s: D >= 1, rot even and 0 to D", fn);
+    if (!(eps >= 0) || !isfinite((float)eps)) return fail(QMM_ERR_INVALID_ARG, "%s: eps must be finite and >= 0", fn);
+    if (dtype != QMM_F16 && dtype != QMM_BF16) return fail(QMM_ERR_INVALID_ARG, "%s: dtype must be fp16 or bf16", fn);
+    if (D % 16 != 0 || rot % 16 != 0 || D > 256) return fail(QMM_ERR_UNSUPPORTED, "%s: D and rot must be multiples of 16, D up to 256", fn);
+    const int64_t lim = int64_t(1) << 31;
+    if (Hq > 65535 || Hkv > 65535 || Hq + 2 * Hkv > 65535) return fail(QMM_ERR_UNSUPPORTED, "%s: more than 65535 heads", fn);
+    if (T >= lim) return fail(QMM_ERR_UNSUPPORTED, "%s: size beyond the supported range", fn);
+    if (rot > 0 && (table_rows < 1 || table_rows >= lim)) return fail(QMM_ERR_INVALID_ARG, "%s: the table must have 1 to 2^31 - 1 rows", fn);
+    return QMM_OK;
+}
+// whether the rows of tensors [tokens][heads][D] stand at multiples of 16 bytes
+static bool even_rows(std::initializer_list<std::pair<const void *, const int64_t *>> tensors)
+{
+    for (const auto &t : tensors)
+        if (t.first && (!aligned(t.first, 16) || t.second[0] % 8 != 0 || t.second[1] % 8 != 0)) return false;
+    return true;
+}
+
+qmm_status qmm_qk_norm(const qmm_qk_norm_args *p, qmm_stream stream)
+{
+    const char *fn = "qmm_qk_norm";
+    if (!p) return fail(QMM_ERR_INVALID_ARG, "%s: null arguments", fn);
+    qmm_status st = heads_shape(fn, p->T, p->Hq, p->Hkv, p->D, p->rot, p->table_rows, p->eps, p->dtype);
+    if (st != QMM_OK) return st;
+    if (p->T == 0 || p->Hq + p->Hkv == 0) return hip_status(hipSuccess, fn);
+    if ((p->Hq > 0 && (!p->q || !p->q_out)) || (p->Hkv > 0 && (!p->k || !p->k_out)) || (p->rot > 0 && (!p->positions || !p->rope)))
+        return fail(QMM_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if (!aligned(p->q_weight, 16) || !aligned(p->k_weight, 16) || !aligned(p->rope, 16))
+        return fail(QMM_ERR_INVALID_ARG, "%s: weights and table must start at multiples of 16 bytes", fn);
+    qmm::HeadsArgs a{};
+    a.q = p->q, a.k = p->k, a.q_out = p->q_out, a.k_out = p->k_out, a.q_weight = p->q_weight, a.k_weight = p->k_weight;
+    a.positions = p->positions, a.rope = p->rope;
+    a.q_ts = p->q_stride[0], a.q_hs = p->q_stride[1], a.k_ts = p->k_stride[0], a.k_hs = p->k_stride[1];
+    a.qo_ts = p->q_out_stride[0], a.qo_hs = p->q_out_stride[1], a.ko_ts = p->k_out_stride[0], a.ko_hs = p->k_out_stride[1];
+    a.T = (int)p->T, a.Hq = (int)p->Hq, a.Hk = (int)p->Hkv, a.D = (int)p->D, a.rot = (int)p->rot, a.table_rows = (int)p->table_rows;
+    a.eps = (float)p->eps, a.pairs = p->pairs != 0;
+    const bool vec = even_rows({{p->Hq ? p->q : nullptr, p->q_stride}, {p->Hkv ? p->k : nullptr, p->k_stride}, {p->Hq ? p->q_out : nullptr, p->q_out_stride},
+                                {p->Hkv ? p->k_out : nullptr, p->k_out_stride}});
+    return hip_status(qmm::launch_heads(a, p->dtype == QMM_BF16, vec, false, (hipStream_t)stream), fn);
+}
+
+qmm_status qmm_kv4_append(const qmm_kv4_append_args *p, qmm_stream stream)
+{
+    const char *fn = "qmm_kv4_append";
+    if (!p) return fail(QMM_ERR_INVALID_ARG, "%s: null arguments", fn);
+    const qmm_kv4_cache &c = p->cache;
+    qmm_status st = kv4_shape(fn, c);
+    if (st == QMM_OK) st = heads_shape(fn, p->T, p->Hq, c.Hkv, c.D, p->rot, p->table_rows, p->eps, p->dtype);
+    if (st != QMM_OK) return st;
+    if (p->T == 0) return hip_status(hipSuccess, fn);
+    if ((p->Hq > 0 && (!p->q || !p->out)) || !p->k || !p->v || !p->slots || (p->rot > 0 && (!p->positions || !p->rope)))
+        return fail(QMM_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if (!aligned(p->q_norm, 16) || !aligned(p->k_norm, 16) || !aligned(p->rope, 16))
+        return fail(QMM_ERR_INVALID_ARG, "%s: weights and table must start at multiples of 16 bytes", fn);
+    if ((st = kv4_places(fn, c)) != QMM_OK) return st;
+    qmm::HeadsArgs a{};
+    a.q = p->q, a.k = p->k, a.v = p->v, a.q_out = p->out, a.q_weight = p->q_norm, a.k_weight = p->k_norm;
+    a.positions = p->positions, a.rope = p->rope, a.slots = p->slots;
+    a.k_codes = c.k, a.v_codes = c.v, a.k_scale = c.k_scale, a.v_scale = c.v_scale;
+    a.q_ts = p->q_stride[0], a.q_hs = p->q_stride[1], a.k_ts = p->k_stride[0], a.k_hs = p->k_stride[1];
+    a.v_ts = p->v_stride[0], a.v_hs = p->v_stride[1], a.qo_ts = p->out_stride[0], a.qo_hs = p->out_stride[1];
+    a.kc_ps = c.k_stride[0], a.kc_hs = c.k_stride[1], a.kc_ts = c.k_stride[2], a.vc_ps = c.v_stride[0], a.vc_hs = c.v_stride[1], a.vc_ts = c.v_stride[2];
+    a.ks_ps = c.k_scale_stride[0], a.ks_hs = c.k_scale_stride[1], a.vs_ps = c.v_scale_stride[0], a.vs_hs = c.v_scale_stride[1];
+    a.T = (int)p->T, a.Hq = (int)p->Hq, a.Hk = 0, a.Hkv = (int)c.Hkv, a.D = (int)c.D, a.G = (int)c.G, a.rot = (int)p->rot;
+    a.page = (int)c.page, a.pages = (int)c.pages, a.table_rows = (int)p->table_rows, a.eps = (float)p->eps, a.pairs = p->pairs != 0;
+    const bool vec = even_rows({{p->k, p->k_stride}, {p->v, p->v_stride}, {p->Hq ? p->q : nullptr, p->q_stride}, {p->Hq ? p->out : nullptr, p->out_stride}});
+    return hip_status(qmm::launch_heads(a, p->dtype == QMM_BF16, vec, true, (hipStream_t)stream), fn);
+}
+
+qmm_status qmm_kv4_read(const qmm_kv4_read_args *p, qmm_stream stream)
+{
+    const char *fn = "qmm_kv4_read";
+    if (!p) return fail(QMM_ERR_INVALID_ARG, "%s: null arguments", fn);
+    const qmm_kv4_cache &c = p->cache;
+    qmm_status st = kv4_shape(fn, c);
+    if (st != QMM_OK) return st;
+    if (p->T < 0) return fail(QMM_ERR_INVALID_ARG, "%s: T must be >= 0", fn);
+    if (p->dtype != QMM_F16 && p->dtype != QMM_BF16) return fail(QMM_ERR_INVALID_ARG, "%s: dtype must be fp16 or bf16", fn);
+    if (p->T >= (int64_t(1) << 31)) return fail(QMM_ERR_UNSUPPORTED, "%s: size beyond the supported range", fn);
+    if (p->T == 0) return hip_status(hipSuccess, fn);
+    if (!p->slots || !p->k_out || !p->v_out) return fail(QMM_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if ((st = kv4_places(fn, c)) != QMM_OK) return st;
+    qmm::Read4Args a{};
+    a.k_codes = c.k, a.v_codes = c.v, a.k_scale = c.k_scale, a.v_scale = c.v_scale, a.slots = p->slots, a.k_out = p->k_out, a.v_out = p->v_out;
+    a.kc_ps = c.k_stride[0], a.kc_hs = c.k_stride[1], a.kc_ts = c.k_stride[2], a.vc_ps = c.v_stride[0], a.vc_hs = c.v_stride[1], a.vc_ts = c.v_stride[2];
+    a.ks_ps = c.k_scale_stride[0], a.ks_hs = c.k_scale_stride[1], a.vs_ps = c.v_scale_stride[0], a.vs_hs = c.v_scale_stride[1];
+    a.ko_ts = p->k_out_stride[0], a.ko_hs = p->k_out_stride[1], a.vo_ts = p->v_out_stride[0], a.vo_hs = p->v_out_stride[1];
+    a.T = (int)p->T, a.Hkv = (int)c.Hkv, a.D = (int)c.D, a.G = (int)c.G, a.page = (int)c.page, a.pages = (int)c.pages;
+    return hip_status(qmm::launch_read4(a, p->dtype == QMM_BF16, even_rows({{p->k_out, p->k_out_stride}, {p->v_out, p->v_out_stride}}), (hipStream_t)stream), fn);
+}
+
+// Sizes and types of an attention call over 4-bit codes; fills what the planner reads.
+static qmm_status attention4_shape(const char *fn, const qmm_kv4_attention_args *p, qmm::Attend4Args &a)
+{
+    if (!p) return fail(QMM_ERR_INVALID_ARG, "%s: null arguments", fn);
+    const qmm_kv4_cache &c = p->cache;
+    qmm_status st = kv4_shape(fn, c);
+    if (st != QMM_OK) return st;
+    if (p->T < 0 || p->B < 0 || p->Hq < 1 || p->width < 1)
+        return fail(QMM_ERR_INVALID_ARG, "%s: T and B must be >= 0, the other sizes >= 1", fn);
+    if (p->max_q < 1 || p->max_kv < 0) return fail(QMM_ERR_INVALID_ARG, "%s: max_q must be >= 1, max_kv >= 0", fn);
+    if (p->Hq % c.Hkv != 0) return fail(QMM_ERR_INVALID_ARG, "%s: Hq must be a multiple of Hkv", fn);
+    if (p->window < 0 || p->sinks < 0) return fail(QMM_ERR_INVALID_ARG, "%s: window and sinks must be >= 0", fn);
+    if (!(p->scale >= 0) || !isfinite((float)p->scale)) return fail(QMM_ERR_INVALID_ARG, "%s: scale must be finite and >= 0", fn);
+    if (p->dtype != QMM_F16 && p->dtype != QMM_BF16) return fail(QMM_ERR_INVALID_ARG, "%s: dtype must be fp16 or bf16", fn);
+    const int64_t lim = (int64_t(1) << 31) - 65536;
+    if (p->T > lim || p->B > lim || p->Hq > 65536 || p->width > lim || p->max_q > lim || p->max_kv > lim)
+        return fail(QMM_ERR_UNSUPPORTED, "%s: size beyond the supported range", fn);
+    a.T = (int)p->T, a.B = (int)p->B, a.Hq = (int)p->Hq, a.Hkv = (int)c.Hkv, a.g = (int)(p->Hq / c.Hkv), a.D = (int)c.D;
+    a.lg_G = c.G == 32 ? 5 : c.G == 64 ? 6 : 7, a.s_ts = (uint32_t)(4 * (c.D / c.G));
+    a.page = (int)c.page, a.pages = (int)c.pages, a.width = (int)p->width;
+    // no sequence has more new tokens than there are rows: smaller bounds, smaller grids
+    a.max_q = (int)(p->T > 0 && p->T < p->max_q ? p->T : p->max_q);
+    a.max_kv = (int)p->max_kv;
+    a.window = (int)(p->window > lim ? 0 : p->window);
+    a.sinks = a.window > 0 ? (int)(p->sinks > lim ? lim : p->sinks) : 0;   // without a window every key before a row is seen
+    a.scale = (float)p->scale;
+    a.halves = c.page % 16 == 0;
+    if (p->T * p->Hq > lim || (int64_t)a.max_q * p->Hq > lim) return fail(QMM_ERR_UNSUPPORTED, "%s: size beyond the supported range", fn);
+    return QMM_OK;
+}
+
+int64_t qmm_kv4_attention_workspace(const qmm_kv4_attention_args *args)
+{
+    qmm::Attend4Args a{};
+    if (attention4_shape("qmm_kv4_attention_workspace", args, a) != QMM_OK || a.T == 0 || a.B == 0) return 0;
+    return qmm::plan_attend4(a);
+}
+
+qmm_status qmm_kv4_attention(const qmm_kv4_attention_args *p, qmm_stream stream)
+{
+    const char *fn = "qmm_kv4_attention";
+    qmm::Attend4Args a{};
+    qmm_status st = attention4_shape(fn, p, a);
+    if (st != QMM_OK) return st;
+    if (a.T == 0 || a.B == 0) return hip_status(hipSuccess, fn);
+    const qmm_kv4_cache &c = p->cache;
+    if (!p->q || !p->out || !p->page_table || !p->cu_q || !p->kv_lens) return fail(QMM_ERR_INVALID_ARG, "%s: null pointer", fn);
+    bool even = aligned(p->q, 16) && aligned(p->out, 16);
+    for (int i = 0; i < 2; ++i) even = even && p->q_stride[i] % 8 == 0 && p->out_stride[i] % 8 == 0;
+    if (!even) return fail(QMM_ERR_INVALID_ARG, "%s: starts and strides of q and out must be multiples of 16 bytes", fn);
+    if ((st = kv4_places(fn, c)) != QMM_OK) return st;
+    a.q = p->q, a.k = c.k, a.v = c.v, a.ks = c.k_scale, a.vs = c.v_scale, a.out = p->out, a.lse = p->lse;
+    a.table = p->page_table, a.cu_q = p->cu_q, a.kv_lens = p->kv_lens;
+    a.q_ts = p->q_stride[0] * 2, a.q_hs = p->q_stride[1] * 2, a.o_ts = p->out_stride[0] * 2, a.o_hs = p->out_stride[1] * 2;
+    a.k_ps = c.k_stride[0], a.k_hs = c.k_stride[1], a.k_ts = (uint32_t)c.k_stride[2];
+    a.v_ps = c.v_stride[0], a.v_hs = c.v_stride[1], a.v_ts = (uint32_t)c.v_stride[2];
+    a.ks_ps = c.k_scale_stride[0] * 2, a.ks_hs = c.k_scale_stride[1] * 2, a.vs_ps = c.v_scale_stride[0] * 2, a.vs_hs = c.v_scale_stride[1] * 2;
+    a.table_s = p->table_stride;
+    const int64_t need = qmm::plan_attend4(a);
+    if (need > 0 && (!p->workspace || p->workspace_bytes < need || !aligned(p->workspace, 16)))
+        return fail(QMM_ERR_INVALID_ARG, "%s: workspace missing, too small or not 16-byte aligned", fn);
+    a.part = (float *)p->workspace;
+    return hip_status(qmm::launch_attend4(a, p->dtype == QMM_BF16, (hipStream_t)stream), fn);
 }
 
 qmm_status qmm_probe_read(const void *buf, uint64_t bytes, uint32_t *sink, int grid, qmm_stream stream)

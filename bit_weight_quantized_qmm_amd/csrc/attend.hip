@@ -14,31 +14,9 @@
 #include <algorithm>
 #include <math.h>
 
-#include "launch.hpp"
-#include "qmm_device.hpp"
-#include "elem.hpp"
+#include "attend.hpp"
 
 namespace qmm {
-
-typedef __bf16 bf8x_t __attribute__((ext_vector_type(8)));
-typedef __bf16 bf2x_t __attribute__((ext_vector_type(2)));
-typedef int int2v_t __attribute__((ext_vector_type(2)));
-
-constexpr uint32_t ATT_OOB = 0x80000000u;
-constexpr float ATT_LOG2E = 1.44269504088896340736f, ATT_LN2 = 0.69314718055994530942f;
-
-__device__ __forceinline__ float4_t mfma_16(int4_t a, int4_t b, float4_t c, _Float16)
-{
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, a), __builtin_bit_cast(half8_t, b), c, 0, 0, 0);
-}
-__device__ __forceinline__ float4_t mfma_16(int4_t a, int4_t b, float4_t c, bf16_t)
-{
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8x_t, a), __builtin_bit_cast(bf8x_t, b), c, 0, 0, 0);
-}
-
-// two fp32 -> a dword of two elements, each rounded to nearest even
-__device__ __forceinline__ int pack2(float x, float y, _Float16) { return __builtin_bit_cast(int, half2_t{(_Float16)x, (_Float16)y}); }
-__device__ __forceinline__ int pack2(float x, float y, bf16_t) { return __builtin_bit_cast(int, bf2x_t{(bf16_t)x, (bf16_t)y}); }
 
 // Probabilities meet the values in S.  fp16 is in full down to 2^-14 and ends at 2^-25:
 // with a row's largest at 1, keys more than 10 below it in the exponent would lose bits and
@@ -79,23 +57,6 @@ __device__ __forceinline__ KeyRange key_range(const AttendArgs &a, int b, int rb
     r.lo = a.window > 0 ? max(0, r.L - n + first - a.window + 1) : 0;
     r.start = r.lo & ~15;
     return r;
-}
-
-__device__ __forceinline__ int key_page(const AttendArgs &a, int key)
-{
-    return (int)(((uint64_t)(uint32_t)key * a.page_mul) >> a.page_sh);
-}
-
-// Whether one of the keys [lo, hi) of sequence b stands on a page of the cache.
-// Asked of rows without a sum alone.
-__device__ __forceinline__ bool sees_key(const AttendArgs &a, int b, int64_t lo, int64_t hi)
-{
-    for (int64_t key = lo > 0 ? lo : 0; key < hi;) {
-        const int pg = key_page(a, (int)key);
-        if ((uint32_t)a.table[b * a.table_s + pg] < (uint32_t)a.pages) return true;
-        key = ((int64_t)pg + 1) * a.page;
-    }
-    return false;
 }
 
 // What turns a product into a base-2 exponent.  Positive, or NaN as it is given: a
@@ -541,18 +502,6 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(rows_oc
 // no longer read the same keys at the same time).  No change: raised wave priorities for
 // the products.
 // ---------------------------------------------------------------------------
-typedef float float16v_t __attribute__((ext_vector_type(16)));
-typedef short short4v_t __attribute__((ext_vector_type(4)));
-
-__device__ __forceinline__ float16v_t mfma_32(int4_t a, int4_t b, float16v_t c, _Float16)
-{
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, a), __builtin_bit_cast(half8_t, b), c, 0, 0, 0);
-}
-__device__ __forceinline__ float16v_t mfma_32(int4_t a, int4_t b, float16v_t c, bf16_t)
-{
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8x_t, a), __builtin_bit_cast(bf8x_t, b), c, 0, 0, 0);
-}
-
 // keys of a tile: 64, and 32 beyond D = 128, where O^T and Q^T leave no registers for more
 __host__ __device__ constexpr int tiles_keys(int D) { return D <= 128 ? 64 : 32; }
 constexpr float ATT_LAZY = 4.f;        // a maximum may be exceeded by this much (base 2)

@@ -1,5 +1,5 @@
 // binding.cpp -- argument marshalling of the decoder-layer calls (qmm_linear,
-// qmm_kv_append, qmm_paged_attention) for Python: checks the tensors, fills the
+// qmm_kv_append, qmm_paged_attention, qmm_qk_norm, qmm_kv4_*) for Python: checks the tensors, fills the
 // C ABI's argument blocks and calls the library.  In C++ because these calls
 // are made many times for each token, where reading 30 tensor attributes from
 // Python costs more than the kernels of a short step (one token: 4.5 to 5.8 us
@@ -24,6 +24,11 @@ struct Library {
     decltype(&qmm_kv_append) kv_append;
     decltype(&qmm_paged_attention) attention;
     decltype(&qmm_paged_attention_workspace) attention_workspace;
+    decltype(&qmm_qk_norm) qk_norm;
+    decltype(&qmm_kv4_append) kv4_append;
+    decltype(&qmm_kv4_read) kv4_read;
+    decltype(&qmm_kv4_attention) kv4_attention;
+    decltype(&qmm_kv4_attention_workspace) kv4_attention_workspace;
 } lib;
 PyObject *raise_status, *raw_stream, *get_device, *set_device;   // Python callables, held for the process
 
@@ -158,6 +163,14 @@ PyObject *give(PyObject *given, const at::Tensor &made)
         return given;
     }
     return THPVariable_Wrap(made);
+}
+
+PyObject *pair(PyObject *x, PyObject *y)
+{
+    PyObject *r = x && y ? PyTuple_Pack(2, x, y) : nullptr;
+    Py_XDECREF(x);
+    Py_XDECREF(y);
+    return r;
 }
 
 template <typename F>
@@ -318,17 +331,228 @@ PyObject *paged_attention(PyObject *, PyObject *const *a, Py_ssize_t n)
     });
 }
 
-// (addresses of the five entry points, raise_status, raw_stream, get_device, set_device)
+// a cache of 4-bit codes: four tensors (k, v, k_scale, v_scale)
+qmm_kv4_cache cache4(PyObject *o, int &index, bool leads)
+{
+    if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 4) bad_type("cache must be a tuple of k, v, k_scale and v_scale");
+    const at::Tensor &k = tensor(PyTuple_GET_ITEM(o, 0), "cache.k"), &v = tensor(PyTuple_GET_ITEM(o, 1), "cache.v"),
+                     &ks = tensor(PyTuple_GET_ITEM(o, 2), "cache.k_scale"), &vs = tensor(PyTuple_GET_ITEM(o, 3), "cache.v_scale");
+    typed(k, "cache.k", at::kByte);
+    typed(v, "cache.v", at::kByte);
+    typed(ks, "cache.k_scale", at::kHalf);
+    typed(vs, "cache.v_scale", at::kHalf);
+    if (leads) {
+        if (!k.is_cuda()) bad_value("cache.k must be a GPU tensor");
+        index = (int)k.get_device();
+    }
+    if (k.dim() != 4 || ks.dim() != 5) bad_value("cache.k must be [pages, heads, page, D / 2] and cache.k_scale [pages, heads, page, D / G, 2]");
+    shaped(v, "cache.v", k.sizes());
+    const int64_t D = 2 * k.size(3), groups = ks.size(3);
+    if (groups < 1 || D % groups != 0) bad_value("cache.k_scale has " + std::to_string(groups) + " groups for D = " + std::to_string(D));
+    shaped(ks, "cache.k_scale", {k.size(0), k.size(1), k.size(2), groups, 2});
+    shaped(vs, "cache.v_scale", ks.sizes());
+    for (const at::Tensor *t : {&k, &v, &ks, &vs}) same_device(*t, "cache", index);
+    if ((k.stride(3) != 1 || v.stride(3) != 1) && k.size(3) > 1) bad_value("the codes of a cache's token must stand side by side");
+    for (const at::Tensor *t : {&ks, &vs})
+        if (t->stride(4) != 1 || (t->stride(3) != 2 && groups > 1) || (t->stride(2) != 2 * groups && k.size(2) > 1))
+            bad_value("the scales of a page's head must stand side by side");
+    qmm_kv4_cache c{};
+    c.k = (uint8_t *)k.mutable_data_ptr(), c.v = (uint8_t *)v.mutable_data_ptr();
+    c.k_scale = (qmm_half *)ks.mutable_data_ptr(), c.v_scale = (qmm_half *)vs.mutable_data_ptr();
+    for (int i = 0; i < 3; ++i) c.k_stride[i] = k.stride(i), c.v_stride[i] = v.stride(i);
+    for (int i = 0; i < 2; ++i) c.k_scale_stride[i] = ks.stride(i), c.v_scale_stride[i] = vs.stride(i);
+    c.pages = k.size(0), c.Hkv = k.size(1), c.page = k.size(2), c.D = D, c.G = D / groups;
+    return c;
+}
+// positions and table of a rotation, each given with the other
+void rotation(const at::Tensor *positions, const at::Tensor *rope, int64_t T, int index, int64_t &rot, int64_t &rows)
+{
+    if (!rope) {
+        if (positions) bad_value("positions without rope");
+        return;
+    }
+    if (!positions) bad_value("rope needs positions");
+    if (rope->dim() != 2) bad_value("rope must be [rows, rot]");
+    rows = rope->size(0), rot = rope->size(1);
+    dense(*rope, "rope", at::kFloat, rope->sizes(), index);
+    dense(*positions, "positions", at::kInt, {T}, index);
+}
+double number(PyObject *o)
+{
+    const double x = PyFloat_AsDouble(o);
+    if (x == -1.0 && PyErr_Occurred()) throw Raised{};
+    return x;
+}
+int truth(PyObject *o)
+{
+    const int x = PyObject_IsTrue(o);
+    if (x < 0) throw Raised{};
+    return x;
+}
+
+// (q, k, q_weight, k_weight, eps, positions, rope, pairs, q_out, k_out)
+PyObject *qk_norm(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject * {
+        count(n, 10);
+        const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k");
+        const at::Tensor *qw = maybe(a[2], "q_weight"), *kw = maybe(a[3], "k_weight"), *positions = maybe(a[5], "positions"), *rope = maybe(a[6], "rope"),
+                         *q_out = maybe(a[8], "q_out"), *k_out = maybe(a[9], "k_out");
+        qmm_qk_norm_args p{};
+        int index;
+        p.pairs = truth(a[7]);
+        p.dtype = leading(q, "q", index);
+        const at::ScalarType type = q.scalar_type();
+        p.T = q.size(0), p.Hq = q.size(1), p.D = q.size(2);
+        if (k.dim() != 3) bad_value("k must be [tokens, heads, D]");
+        p.Hkv = k.size(1);
+        rows(q, "q", type, q.sizes(), index, p.q_stride);
+        rows(k, "k", type, {p.T, p.Hkv, p.D}, index, p.k_stride);
+        if (qw) dense(*qw, "q_weight", type, {p.D}, index);
+        if (kw) dense(*kw, "k_weight", type, {p.D}, index);
+        rotation(positions, rope, p.T, index, p.rot, p.table_rows);
+        if (q_out) rows(*q_out, "q_out", type, q.sizes(), index, p.q_out_stride);
+        if (k_out) rows(*k_out, "k_out", type, k.sizes(), index, p.k_out_stride);
+        p.eps = number(a[4]);
+        const at::Tensor y = q_out ? *q_out : at::empty({p.T, p.Hq, p.D}, q.options()), x = k_out ? *k_out : at::empty({p.T, p.Hkv, p.D}, k.options());
+        for (int i = 0; i < 2; ++i) p.q_out_stride[i] = y.stride(i), p.k_out_stride[i] = x.stride(i);
+        p.q = at(&q), p.k = at(&k), p.q_out = y.mutable_data_ptr(), p.k_out = x.mutable_data_ptr(), p.q_weight = at(qw), p.k_weight = at(kw);
+        p.positions = (const int32_t *)at(positions), p.rope = (const float *)at(rope);
+        on_device(index, [&](void *stream) { return lib.qk_norm(&p, stream); });
+        return pair(give(a[8], y), give(a[9], x));
+    });
+}
+
+// (q, k, v, cache, slots, positions, rope, pairs, q_norm, k_norm, eps, out)
+PyObject *kv4_append(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject * {
+        count(n, 12);
+        const at::Tensor *q = maybe(a[0], "q"), *positions = maybe(a[5], "positions"), *rope = maybe(a[6], "rope"), *qw = maybe(a[8], "q_norm"),
+                         *kw = maybe(a[9], "k_norm"), *out = maybe(a[11], "out");
+        const at::Tensor &k = tensor(a[1], "k"), &v = tensor(a[2], "v"), &slots = tensor(a[4], "slots");
+        qmm_kv4_append_args p{};
+        int index;
+        p.pairs = truth(a[7]);
+        p.dtype = leading(k, "k", index);
+        const at::ScalarType type = k.scalar_type();
+        p.T = k.size(0);
+        const int64_t Hkv = k.size(1), D = k.size(2);
+        rows(k, "k", type, k.sizes(), index, p.k_stride);
+        rows(v, "v", type, k.sizes(), index, p.v_stride);
+        at::Tensor y;
+        p.cache = cache4(a[3], index, false);
+        if (p.cache.Hkv != Hkv || p.cache.D != D)
+            bad_value("the cache has " + std::to_string(p.cache.Hkv) + " heads of " + std::to_string(p.cache.D) + ", k " + std::to_string(Hkv) + " of " + std::to_string(D));
+        dense(slots, "slots", at::kLong, {p.T}, index);
+        rotation(positions, rope, p.T, index, p.rot, p.table_rows);
+        if (qw && !q) bad_value("q_norm without q");
+        if (qw) dense(*qw, "q_norm", type, {D}, index);
+        if (kw) dense(*kw, "k_norm", type, {D}, index);
+        p.eps = number(a[10]);
+        if (q) {
+            if (q->dim() != 3) bad_value("q must be [tokens, heads, D]");
+            p.Hq = q->size(1);
+            rows(*q, "q", type, {p.T, p.Hq, D}, index, p.q_stride);
+            if (out) rows(*out, "out", type, {p.T, p.Hq, D}, index, p.out_stride);
+            y = out ? *out : at::empty({p.T, p.Hq, D}, q->options());
+            p.out_stride[0] = y.stride(0), p.out_stride[1] = y.stride(1);
+            p.q = at(q), p.out = y.mutable_data_ptr();
+        } else if (out) {
+            bad_value("out without q");
+        }
+        p.k = at(&k), p.v = at(&v), p.q_norm = at(qw), p.k_norm = at(kw);
+        p.slots = (const int64_t *)at(&slots), p.positions = (const int32_t *)at(positions), p.rope = (const float *)at(rope);
+        on_device(index, [&](void *stream) { return lib.kv4_append(&p, stream); });
+        if (!q) Py_RETURN_NONE;
+        return give(a[11], y);
+    });
+}
+
+// (cache, slots, bf16, k_out, v_out)
+PyObject *kv4_read(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject * {
+        count(n, 5);
+        const at::Tensor &slots = tensor(a[1], "slots");
+        const at::Tensor *k_out = maybe(a[3], "k_out"), *v_out = maybe(a[4], "v_out");
+        qmm_kv4_read_args p{};
+        int index = 0;
+        p.cache = cache4(a[0], index, true);
+        if (slots.dim() != 1) bad_value("slots must be [tokens]");
+        p.T = slots.size(0);
+        dense(slots, "slots", at::kLong, {p.T}, index);
+        const bool bf16 = truth(a[2]);
+        p.dtype = bf16 ? QMM_BF16 : QMM_F16;
+        const at::ScalarType type = bf16 ? at::kBFloat16 : at::kHalf;
+        const int64_t shape[3] = {p.T, p.cache.Hkv, p.cache.D};
+        if (k_out) rows(*k_out, "k_out", type, shape, index, p.k_out_stride);
+        if (v_out) rows(*v_out, "v_out", type, shape, index, p.v_out_stride);
+        const at::Tensor y = k_out ? *k_out : at::empty(shape, slots.options().dtype(type)), x = v_out ? *v_out : at::empty(shape, slots.options().dtype(type));
+        for (int i = 0; i < 2; ++i) p.k_out_stride[i] = y.stride(i), p.v_out_stride[i] = x.stride(i);
+        p.slots = (const int64_t *)at(&slots), p.k_out = y.mutable_data_ptr(), p.v_out = x.mutable_data_ptr();
+        on_device(index, [&](void *stream) { return lib.kv4_read(&p, stream); });
+        return pair(give(a[3], y), give(a[4], x));
+    });
+}
+
+// (q, cache, page_table, cu_q, kv_lens, max_q, max_kv, scale, window, sinks, out, lse)
+PyObject *kv4_attention(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject * {
+        count(n, 12);
+        const at::Tensor &q = tensor(a[0], "q"), &table = tensor(a[2], "page_table"), &cu = tensor(a[3], "cu_q"), &lens = tensor(a[4], "kv_lens");
+        const at::Tensor *out = maybe(a[10], "out"), *lse = maybe(a[11], "lse");
+        qmm_kv4_attention_args p{};
+        int index;
+        p.dtype = leading(q, "q", index);
+        const at::ScalarType type = q.scalar_type();
+        p.T = q.size(0), p.Hq = q.size(1);
+        const int64_t D = q.size(2);
+        rows(q, "q", type, q.sizes(), index, p.q_stride);
+        p.cache = cache4(a[1], index, false);
+        if (p.cache.D != D) bad_value("the cache has heads of " + std::to_string(p.cache.D) + ", q of " + std::to_string(D));
+        if (table.dim() != 2) bad_value("page_table must be [sequences, width]");
+        typed(table, "page_table", at::kInt);
+        same_device(table, "page_table", index);
+        p.B = table.size(0), p.width = table.size(1), p.table_stride = table.stride(0);
+        if (table.stride(1) != 1 && p.width > 1) bad_value("page_table: the ids of a sequence must stand side by side");
+        dense(cu, "cu_q", at::kInt, {p.B + 1}, index);
+        dense(lens, "kv_lens", at::kInt, {p.B}, index);
+        if (out) rows(*out, "out", type, q.sizes(), index, p.out_stride);
+        const at::Tensor y = out ? *out : at::empty({p.T, p.Hq, D}, q.options());
+        p.out_stride[0] = y.stride(0), p.out_stride[1] = y.stride(1);
+        if (lse) dense(*lse, "lse", at::kFloat, {p.T, p.Hq}, index);
+        p.max_q = integer(a[5], "max_q"), p.max_kv = integer(a[6], "max_kv"), p.window = integer(a[8], "window"), p.sinks = integer(a[9], "sinks");
+        p.scale = a[7] == Py_None ? 1.0 / std::sqrt((double)D) : number(a[7]);
+        p.q = at(&q), p.out = y.mutable_data_ptr(), p.lse = lse ? (float *)lse->mutable_data_ptr() : nullptr;
+        p.page_table = (const int32_t *)at(&table), p.cu_q = (const int32_t *)at(&cu), p.kv_lens = (const int32_t *)at(&lens);
+        at::Tensor space;
+        if ((p.workspace_bytes = lib.kv4_attention_workspace(&p)) > 0) {
+            space = scratch(p.workspace_bytes, q);
+            p.workspace = space.mutable_data_ptr();
+        }
+        on_device(index, [&](void *stream) { return lib.kv4_attention(&p, stream); });
+        return give(a[10], y);
+    });
+}
+
+// (addresses of the ten entry points, raise_status, raw_stream, get_device, set_device)
 PyObject *connect(PyObject *, PyObject *args)
 {
-    unsigned long long f[5];
+    unsigned long long f[10];
     PyObject *o[4];
-    if (!PyArg_ParseTuple(args, "KKKKKOOOO", &f[0], &f[1], &f[2], &f[3], &f[4], &o[0], &o[1], &o[2], &o[3])) return nullptr;
+    if (!PyArg_ParseTuple(args, "KKKKKKKKKKOOOO", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6], &f[7], &f[8], &f[9], &o[0], &o[1], &o[2], &o[3])) return nullptr;
     lib.linear = reinterpret_cast<decltype(lib.linear)>(f[0]);
     lib.linear_workspace = reinterpret_cast<decltype(lib.linear_workspace)>(f[1]);
     lib.kv_append = reinterpret_cast<decltype(lib.kv_append)>(f[2]);
     lib.attention = reinterpret_cast<decltype(lib.attention)>(f[3]);
     lib.attention_workspace = reinterpret_cast<decltype(lib.attention_workspace)>(f[4]);
+    lib.qk_norm = reinterpret_cast<decltype(lib.qk_norm)>(f[5]);
+    lib.kv4_append = reinterpret_cast<decltype(lib.kv4_append)>(f[6]);
+    lib.kv4_read = reinterpret_cast<decltype(lib.kv4_read)>(f[7]);
+    lib.kv4_attention = reinterpret_cast<decltype(lib.kv4_attention)>(f[8]);
+    lib.kv4_attention_workspace = reinterpret_cast<decltype(lib.kv4_attention_workspace)>(f[9]);
     for (PyObject *x : o) Py_INCREF(x);
     raise_status = o[0], raw_stream = o[1], get_device = o[2], set_device = o[3];
     Py_RETURN_NONE;
@@ -339,6 +563,10 @@ PyMethodDef methods[] = {
     {"linear", (PyCFunction)(void *)linear, METH_FASTCALL, nullptr},
     {"kv_append", (PyCFunction)(void *)kv_append, METH_FASTCALL, nullptr},
     {"paged_attention", (PyCFunction)(void *)paged_attention, METH_FASTCALL, nullptr},
+    {"qk_norm", (PyCFunction)(void *)qk_norm, METH_FASTCALL, nullptr},
+    {"kv4_append", (PyCFunction)(void *)kv4_append, METH_FASTCALL, nullptr},
+    {"kv4_read", (PyCFunction)(void *)kv4_read, METH_FASTCALL, nullptr},
+    {"kv4_attention", (PyCFunction)(void *)kv4_attention, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

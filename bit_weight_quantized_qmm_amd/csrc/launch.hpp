@@ -85,6 +85,62 @@ struct AttendArgs {
     float scale;
 };
 
+// Norms of q and k with their positions (qmm_qk_norm: k to k_out) and the append to a cache
+// of 4-bit codes (qmm_kv4_append: k and v to the codes).  Strides in elements, of codes in bytes.
+struct HeadsArgs {
+    const void *q, *k, *v;
+    void *q_out, *k_out;
+    const void *q_weight, *k_weight;      // [D] or nullptr: no norm
+    const int32_t *positions;
+    const float *rope;
+    const int64_t *slots;
+    uint8_t *k_codes, *v_codes;
+    uint16_t *k_scale, *v_scale;          // fp16 [token][D / G][s, z] of a page's head
+    int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, qo_ts, qo_hs, ko_ts, ko_hs;
+    int64_t kc_ps, kc_hs, kc_ts, vc_ps, vc_hs, vc_ts, ks_ps, ks_hs, vs_ps, vs_hs;
+    int T, Hq, Hk, Hkv, D, G, rot, page, pages, table_rows;   // Hk: heads of k that go to k_out
+    int turn_blocks;                      // workgroups that turn rows (set by the launcher)
+    float eps;
+    bool pairs;
+};
+
+// Tokens of a cache of 4-bit codes as 16-bit rows (qmm_kv4_read).  Strides as above.
+struct Read4Args {
+    const uint8_t *k_codes, *v_codes;
+    const uint16_t *k_scale, *v_scale;
+    const int64_t *slots;
+    void *k_out, *v_out;
+    int64_t kc_ps, kc_hs, kc_ts, vc_ps, vc_hs, vc_ts, ks_ps, ks_hs, vs_ps, vs_hs, ko_ts, ko_hs, vo_ts, vo_hs;
+    int T, Hkv, D, G, page, pages;
+};
+
+// Attention over a cache of 4-bit codes (qmm_kv4_attention).  Strides in bytes; a token's scales
+// stand behind the last one's.
+struct Attend4Args {
+    const void *q;
+    const uint8_t *k, *v;
+    const uint16_t *ks, *vs;
+    void *out;
+    float *lse;             // [T][Hq] or nullptr
+    const int32_t *table, *cu_q, *kv_lens;
+    float *part;            // splits > 1: outputs [T * Hq][splits][D], then log sums [T * Hq][splits]
+    int64_t q_ts, q_hs, o_ts, o_hs, k_ps, k_hs, v_ps, v_hs, ks_ps, ks_hs, vs_ps, vs_hs, table_s;
+    uint32_t k_ts, v_ts, s_ts;
+    int B, T, Hq, Hkv, g, D, lg_G, page, width, pages, max_q, max_kv, window, sinks;
+    uint32_t page_mul;      // key / page = key * page_mul >> page_sh (set by the planner)
+    int page_sh;
+    int rows;               // query rows (token, head of the group) a workgroup takes
+    int rblocks, splits, chunk;
+    int unit;               // the first tokens that stay visible take a multiple of this many places
+    float scale;
+    bool halves;            // 16 tokens in a row lie in one page, their scales at a multiple of 16 bytes
+};
+
+hipError_t launch_heads(const HeadsArgs &a, bool bf16, bool vec, bool store, hipStream_t st);
+hipError_t launch_read4(const Read4Args &a, bool bf16, bool vec, hipStream_t st);
+int64_t plan_attend4(Attend4Args &a);     // as plan_attend
+hipError_t launch_attend4(const Attend4Args &a, bool bf16, hipStream_t st);
+
 hipError_t launch_append(const AppendArgs &a, bool bf16, bool e4m3, int vec, hipStream_t st);
 // Chooses the kernel's shape from the sizes (no GPU call): fills rows, rblocks, splits and chunk.
 // Returns the bytes of workspace that the launch needs.

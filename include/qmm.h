@@ -409,6 +409,125 @@ qmm_status qmm_paged_attention(const qmm_attention_args *args, qmm_stream stream
  * valid. */
 int64_t qmm_paged_attention_workspace(const qmm_attention_args *args);
 
+/* NORMS OF HEADS, AND A CACHE IN 4 BITS.  Strides of 16-bit tensors are in
+ * elements, of codes in bytes. */
+typedef struct qmm_qk_norm_args {
+    const void *q, *k;                 /* [T][Hq][D], [T][Hkv][D]; NULL with Hq 0, Hkv 0 */
+    void *q_out, *k_out;               /* the same shapes (written); may be q and k themselves */
+    const void *q_weight, *k_weight;   /* [D] of dtype, 16-byte aligned; NULL: no norm */
+    const int32_t *positions;          /* [T]: row of the table (brought into 0 .. table_rows - 1) */
+    const float *rope;                 /* [table_rows][rot]: rot/2 cosines, then rot/2 sines; 16-byte aligned */
+    int64_t q_stride[2], k_stride[2], q_out_stride[2], k_out_stride[2];   /* token, head */
+    int64_t T, Hq, Hkv, D, rot, table_rows;
+    double eps;                        /* finite, >= 0 */
+    int32_t dtype;                     /* QMM_F16 or QMM_BF16: everything but the table */
+    int32_t pairs;                     /* 0: element i turns with i + rot/2; 1: 2i with 2i + 1 */
+} qmm_qk_norm_args;
+
+/* RMS norms of queries and keys with their rotary positions, in one pass: for
+ * every token and head
+ *     y = x / sqrt(mean(x^2) + eps) * weight,
+ * then each pair (a, b) of y's first rot elements becomes (a cos - b sin, b cos +
+ * a sin).  fp32 arithmetic (the sum of squares too), rounded once.  What it writes
+ * can go to qmm_kv_append (without a table) and qmm_paged_attention.
+ *   args   HOST struct, read during the call only
+ * rot may be 0 (positions and rope NULL).  T = 0 does nothing.
+ * Errors: QMM_ERR_INVALID_ARG for null pointers, negative sizes, rot odd or
+ * outside 0..D, a bad eps, an unknown type, weights or a table at no multiple of
+ * 16 bytes; QMM_ERR_UNSUPPORTED for D or rot no multiple of 16, D beyond 256,
+ * more than 65535 heads, a launch of 2^32 threads.  Rows at multiples of 16 bytes
+ * move fastest; q_out and k_out overlap nothing but q and k themselves. */
+qmm_status qmm_qk_norm(const qmm_qk_norm_args *args, qmm_stream stream);
+
+/* A paged cache of 4-bit codes.  The D elements of a token and head are D/2 bytes,
+ * element i at bits 4i of them (as in qmm_pack); each G of them have a scale s and a
+ * zero-point z:  x = (code - z) s. */
+typedef struct qmm_kv4_cache {
+    uint8_t *k, *v;                    /* [pages][Hkv][page][D/2] */
+    qmm_half *k_scale, *v_scale;       /* [pages][Hkv][page][D/G][2]: s and z; the last three side by side */
+    int64_t k_stride[3], v_stride[3];              /* page, head, token: bytes, multiples of 16 */
+    int64_t k_scale_stride[2], v_scale_stride[2];  /* page, head: elements, even */
+    int64_t pages, Hkv, page, D, G;    /* G 32, 64 or 128; D a multiple of it, up to 256 */
+} qmm_kv4_cache;
+
+typedef struct qmm_kv4_append_args {
+    const void *q, *k, *v;             /* [T][Hq][D], [T][Hkv][D], [T][Hkv][D] (read); q NULL with Hq 0 */
+    void *out;                         /* [T][Hq][D]: q after norm and rotation (written); may be q itself */
+    const void *q_norm, *k_norm;       /* [D] of dtype, 16-byte aligned; NULL: no norm */
+    const int64_t *slots;              /* [T]: as in qmm_kv_append */
+    const int32_t *positions;          /* as in qmm_qk_norm */
+    const float *rope;
+    qmm_kv4_cache cache;               /* written at the tokens' slots alone */
+    int64_t q_stride[2], k_stride[2], v_stride[2], out_stride[2];   /* token, head */
+    int64_t T, Hq, rot, table_rows;
+    double eps;
+    int32_t dtype, pairs;
+} qmm_kv4_append_args;
+
+/* Norm and rotation of q and k as qmm_qk_norm's, each where it is asked for, then k and
+ * v into the cache.  Over each group of G elements
+ *     lo = min(0, min x), hi = max(0, max x)
+ *     s = (hi - lo) / 15 to 7 significant bits, at least 2^-18
+ *     z = clamp(rint(-lo / s), 0, 15),  code = clamp(rint(x / s) + z, 0, 15)
+ * to nearest, ties to even: the mapping of qmm_quantize, with a scale so short that
+ * every (code - z) s is a number of fp16.  k is normed and turned in fp64 on its way,
+ * so that its codes are those of the formulas; q as in qmm_qk_norm.  Elements beyond
+ * +-57344 are stored as that; a group that holds NaN gets a scale of NaN.
+ *   args   HOST struct, read during the call only
+ * T = 0 does nothing.  A slot outside 0 .. pages * page - 1 stores nothing; two
+ * tokens of a call must not share one.
+ * Errors: as qmm_qk_norm, and for the cache QMM_ERR_INVALID_ARG for sizes < 1, D no
+ * multiple of G, codes at no multiple of 16 bytes, scales at none of 4;
+ * QMM_ERR_UNSUPPORTED for other G or D, pages * page at 2^31 and beyond, a page beyond
+ * 2^20 tokens, a token stride of the codes outside 0 .. 2^24. */
+qmm_status qmm_kv4_append(const qmm_kv4_append_args *args, qmm_stream stream);
+
+typedef struct qmm_kv4_read_args {
+    qmm_kv4_cache cache;               /* read */
+    const int64_t *slots;              /* [T] */
+    void *k_out, *v_out;               /* [T][Hkv][D] of dtype (written) */
+    int64_t k_out_stride[2], v_out_stride[2];      /* token, head */
+    int64_t T;
+    int32_t dtype;                     /* QMM_F16 or QMM_BF16 */
+} qmm_kv4_read_args;
+
+/* The keys and values at these slots: (code - z) s, in fp16 exactly what the
+ * attention multiplies by, in bf16 that rounded once.  A slot outside 0 .. pages *
+ * page - 1 gives zeros.  T = 0 does nothing.  Errors as above. */
+qmm_status qmm_kv4_read(const qmm_kv4_read_args *args, qmm_stream stream);
+
+typedef struct qmm_kv4_attention_args {
+    const void *q;                     /* [T][Hq][D] */
+    void *out;                         /* [T][Hq][D] (written) */
+    float *lse;                        /* [T][Hq] or NULL: natural log of sum_j exp(x_ij) (written) */
+    const int32_t *page_table, *cu_q, *kv_lens;    /* as in qmm_paged_attention */
+    qmm_kv4_cache cache;               /* read */
+    void *workspace;                   /* 16-byte aligned; may be NULL where none is needed */
+    int64_t workspace_bytes;
+    int64_t q_stride[2], out_stride[2];            /* token, head */
+    int64_t table_stride;              /* of a sequence's row */
+    int64_t T, B, Hq, width;
+    int64_t max_q, max_kv;             /* upper bounds of the sequences' new tokens and keys */
+    int64_t window;                    /* > 0: a row sees its last `window` keys and the sequence's first `sinks`; 0: all */
+    int64_t sinks;
+    double scale;                      /* finite, >= 0 */
+    int32_t dtype;                     /* QMM_F16 or QMM_BF16: q and out */
+} qmm_kv4_attention_args;
+
+/* qmm_paged_attention over a cache of 4-bit codes, with what it says of rows, pages,
+ * masked keys, the workspace and the same bits.  With a window, row i (at position
+ * kv_len - n + i) sees the keys j up to its own with j > its position - window or
+ * j < sinks.  Products on f16 MFMA with fp32 sums whatever q's type: keys and
+ * values are exact in f16 (with a scale of more than 7 bits off by half a step), a
+ * bf16 row of q is brought there by a power of two; softmax in fp32, probabilities
+ * rounded once to fp16.  Keys that some row of the sequence sees must have finite
+ * scales.  Errors: as qmm_paged_attention, and the cache's as in qmm_kv4_append. */
+qmm_status qmm_kv4_attention(const qmm_kv4_attention_args *args, qmm_stream stream);
+
+/* Bytes of workspace that qmm_kv4_attention takes for these arguments (from the sizes
+ * alone: no pointer is read but args), 0 if none or if they are not valid. */
+int64_t qmm_kv4_attention_workspace(const qmm_kv4_attention_args *args);
+
 /* Static text for a status code. */
 const char *qmm_status_string(qmm_status status);
 
