@@ -15,7 +15,7 @@
 // bits is lost down to 2^-28 of the row's largest, beyond that 2^-39 of it.
 //
 // The places that a block of rows looks at are numbered through: first the sinks
-// (up to a multiple of `unit`), then the keys from the block's first window on.
+// (up to a multiple of 2^lg_unit), then the keys from the block's first window on.
 #include <algorithm>
 #include <math.h>
 
@@ -27,6 +27,7 @@ typedef _Float16 f16_t;
 
 // fp16 probabilities are scaled by 2^15: in full down to 2^-29 of a row's largest.
 constexpr float A4_TOP = 15.f;
+constexpr float A4_LAZY = 4.f;         // a maximum may be exceeded by this much (base 2): p ends at 2^15
 
 struct Range4 {
     int t0, n, L;
@@ -45,12 +46,12 @@ __device__ __forceinline__ Range4 range4(const Attend4Args &a, int b, int rb)
     r.t0 = t0;
     r.n = n;
     r.L = (int)min((int64_t)max(a.kv_lens[b], 0), min((int64_t)a.width * a.page, (int64_t)a.max_kv));
-    const int first = rb * a.rows / a.g, last = (min((rb + 1) * a.rows, n * a.g) - 1) / a.g;
+    const int first = a.by_g(rb * a.rows), last = a.by_g(max(0, min((rb + 1) * a.rows, n * a.g) - 1));
     r.hi = max(0, min(r.L, r.L - n + last + 1));
     r.lo = a.window > 0 ? max(0, r.L - n + first - a.window + 1) : 0;
     r.sk = min(a.sinks, r.hi);
     r.start = r.lo & ~15;
-    r.S = (r.sk + a.unit - 1) / a.unit * a.unit;
+    r.S = (r.sk + (1 << a.lg_unit) - 1) >> a.lg_unit << a.lg_unit;
     if (r.S >= r.start) {              // they meet: one stretch
         r.S = 0;
         if (r.sk > 0) r.start = 0;
@@ -81,6 +82,13 @@ __device__ __forceinline__ int4_t code_order(int4_t q)
     }
     return r;
 }
+__device__ __forceinline__ float largest(int4_t q, f16_t)
+{
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = max(m, max((uint32_t)q[i] & 0x7fffu, (uint32_t)q[i] >> 16 & 0x7fffu));
+    return (float)as_half((uint16_t)m);
+}
 __device__ __forceinline__ float largest(int4_t q, bf16_t)
 {
     uint32_t m = 0;
@@ -88,7 +96,17 @@ __device__ __forceinline__ float largest(int4_t q, bf16_t)
     for (int i = 0; i < 4; ++i) m = max(m, max((uint32_t)q[i] << 16 & 0x7fffffffu, (uint32_t)q[i] & 0x7fff0000u));
     return __builtin_bit_cast(float, m);
 }
-__device__ __forceinline__ int4_t to_f16(int4_t q, int up)     // bf16 -> f16 times 2^up
+__device__ __forceinline__ int4_t to_f16(int4_t q, int up, f16_t)     // times 2^up
+{
+    int4_t r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const half2_t x = as_half2((uint32_t)q[i]);
+        r[i] = pack2(ldexpf((float)x[0], up), ldexpf((float)x[1], up), f16_t());
+    }
+    return r;
+}
+__device__ __forceinline__ int4_t to_f16(int4_t q, int up, bf16_t)
 {
     int4_t r;
 #pragma unroll
@@ -134,52 +152,272 @@ __device__ __forceinline__ int4_t values8(uint32_t w, const Zero &z)
     return int4_t{value2<false>(w, z), value2<true>(w, z), value2<false>(w >> 8, z), value2<true>(w >> 8, z)};
 }
 
+// The codes of a dword, in codes' order, as f16 without an exponent: c 2^-22, c 2^-18, c 2^-22, c 2^-18.
+// (The matrix instruction adds products as if such leading zeros were digits: with c 2^-24, one
+// operation less for 8 codes, 32 products were off by up to 2^-18.7 of the sum of their sizes, with c 2^-20
+// by 2^-24.1, as with numbers of full precision.)
+__device__ __forceinline__ int4_t places4(uint32_t w)
+{
+    const uint32_t low = w << 2, high = w >> 6;
+    return int4_t{(int)(low & 0x003c003cu), (int)(low & 0x03c003c0u), (int)(high & 0x003c003cu), (int)(high & 0x03c003c0u)};
+}
+
 // ---------------------------------------------------------------------------
 // Few query rows for each key head (decode, short chunks): as attend_rows_kernel, a
 // workgroup takes one (sequence, key head, block of 16 QT rows, split of the
 // places), its waves take blocks of 32 places in turn, each with its own running
 // softmax, and are joined in LDS.
-//   S^T = K Q^T   lane (g, c) holds a slice of key c's codes: with DP = 128, 32 elements from 32 g
-//                 on, 16 bytes, one group's scale; q stands in the same order.
-//   O^T = V^T P^T lane (g, c) holds 8 elements of 8 keys (4g .. 4g + 3 of either half), a dword
-//                 each; two keys' dwords are put together before the codes are taken out, so that a
-//                 pair of f16 is one element of two keys.
+//   S^T = K Q^T   lane (g, c) holds a slice of key c's codes; q stands in the same order.
+//   O^T = V^T P^T lane (g, c) holds elements of 8 keys (4g .. 4g + 3 of either half); the
+//                 dwords of two keys are put together before the codes are taken out, so
+//                 that a pair of f16 is one element of two keys.
+// What bounds it is the instructions between a byte of codes and its product, so with
+// groups of 64 or 128 (GM) nothing is computed for each code but its mask:
+//   K   c at bits 2 .. 5 of a half is the f16 c 2^-22, at bits 6 .. 9 c 2^-18, which the
+//       matrix instruction takes as they are; the rows of q, brought to 2^14 .. 2^15, have
+//       their elements there divided by 16.  A step of the contraction lies in one group:
+//           x = sum over the groups of s (sum_d q_d c_d - z sum_d q_d),
+//       on the accumulators, four keys of a lane.
+//   V   a tile of O^T lies in one group, whose s goes into the probabilities: p s / 2^e, 2^e
+//       above the largest s so far (e is kept as the maximum of the scores is, and in it),
+//       rounded to f16 as p would be; sum_j p_j s_j z_j is a product of its own, taken off at
+//       the end.  (In groups of 64 the lanes c and c ^ 1 read a dword of two keys each and change
+//       halves.)
+// Other groups (GM = 32): every code becomes (c - z) s in f16.
+// Codes and scales go from memory into LDS without a register, two blocks ahead, each wave into a
+// ring of its own; they are read once, so they leave no trace in the L2 (with the default policy the
+// loads alone took 95 us of the 4 sequences below, 84 without).
+// Pages of a multiple of 16 tokens (P16): a half of a block lies in one page; lane l looks
+// up the l-th half of the next 32 blocks, and its place goes to scalar registers
+// when its turn comes.  Other page sizes: a lane's key by its own page.
+// Measured (us): 4 sequences of up to 131071 keys, 8 key heads of 128 for 64, G 128: 100 (5.0
+// TB/s; the loads alone 84; a plain streaming read reaches 7.1); 64 of up to 8192, 32 heads: G 128 68 (4.1), G 64 80, G 32 82.  With
+// the loads in registers, one block ahead, three waves a SIMD: 105, 74, 112, 86.
 // ---------------------------------------------------------------------------
-__host__ __device__ constexpr int rows4_occupancy(int DP, int QT) { return DP <= 128 && QT == 1 ? 3 : 2; }
-
-template <typename S, int DP, bool P16, int QT, int NW>
-__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(rows4_occupancy(DP, QT), rows4_occupancy(DP, QT)))) void attend4_rows_kernel(const Attend4Args a)
+__host__ __device__ constexpr int rows4_occupancy(int DP, int GM, bool P16, int QT)
 {
-    constexpr int KJ = DP / 32;                          // steps of Q K^T
-    constexpr int KW = DP == 64 ? 2 : 4;                 // dwords of a slice
-    constexpr int KL = DP / (32 * KW);                   // slices of a lane
-    constexpr int VW = DP >= 128 ? 8 : 4;                // codes of a V row in one load
-    constexpr int VC = DP / (16 * VW);                   // loads of a V row
-    constexpr int XT = DP / 16;                          // O^T tiles
-    constexpr int LD = DP + 4;                           // row pitch of the join in LDS
+    return DP > 128 || QT > 1 ? 2 : DP == 128 && GM == 128 && !P16 ? 3 : 4;
+}
+__host__ __device__ constexpr int rows4_waves(int DP) { return DP > 128 ? 2 : 4; }      // 64 KB of ring at most
+__host__ __device__ constexpr int rows4_groups(int DP, int GM) { return GM > 32 ? DP / GM : DP / 32; }
+// bytes of a half's scales in LDS, whole loads of 64 lanes; of a block of 32 places: codes and scales of K and V
+__host__ __device__ constexpr int rows4_scales(int DP, int GM) { return rows4_groups(DP, GM) <= 4 ? 256 : 64 * rows4_groups(DP, GM); }
+__host__ __device__ constexpr int rows4_block(int DP, int GM) { return 2 * (32 * DP / 2 + 2 * rows4_scales(DP, GM)); }
+constexpr int ROWS4_IDS = 8;          // blocks whose page ids a wave keeps in LDS where pages are no multiple of 16 tokens
+__host__ __device__ constexpr int rows4_ring(int DP, int GM, bool P16) { return 2 * rows4_block(DP, GM) + (P16 ? 0 : ROWS4_IDS * 32 * 4); }
+
+// Loads of the lanes' 16 (4) bytes at p + off into LDS, from `to` on, lane by lane.  The compiler does
+// not know that they are in flight: wait_loads() before what they bring is read, and what stood there
+// must have been read.
+template <int BYTES>
+__device__ __forceinline__ void fetch(uint32_t to, __amdgpu_buffer_rsrc_t r, uint32_t off)
+{
+    if constexpr (BYTES == 16)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds" ::"s"(to), "v"(off), "s"(r) : "memory", "m0");
+    else
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen nt lds" ::"s"(to), "v"(off), "s"(r) : "memory", "m0");
+}
+template <int BYTES>
+__device__ __forceinline__ void fetch(uint32_t to, const uint8_t *p)
+{
+    if constexpr (BYTES == 16)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off nt" ::"s"(to), "v"(p) : "memory", "m0");
+    else
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off nt" ::"s"(to), "v"(p) : "memory", "m0");
+}
+template <int N> __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void wait_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+template <typename S, int DP, int GM, bool P16, int QT>
+__global__ __launch_bounds__(64 * rows4_waves(DP)) __attribute__((amdgpu_waves_per_eu(rows4_occupancy(DP, GM, P16, QT), rows4_occupancy(DP, GM, P16, QT)))) void attend4_rows_kernel(const Attend4Args a)
+{
+    constexpr int NW = rows4_waves(DP);
+    constexpr bool DEFER = GM > 32;
+    constexpr int KJ = DP / 32;                                   // steps of Q K^T
+    constexpr int KW = DEFER ? GM / 32 : DP == 64 ? 2 : 4;        // dwords of a slice
+    constexpr int KL = KJ / KW;                                   // slices of a lane: of one group each
+    constexpr int VW = GM == 128 ? 8 : GM == 64 ? 4 : DP >= 128 ? 8 : 4;   // elements of a V row that a lane has of a chunk
+    constexpr int VC = DP / (16 * VW);                            // chunks of a V row
+    constexpr int VK = GM == 64 ? 2 : 4;                          // dwords of a chunk in a half: of a key, or of two
+    constexpr int XT = DP / 16;                                   // O^T tiles
+    constexpr int NS = DEFER ? DP / GM : 1;                       // groups of a token
+    constexpr int NX = rows4_groups(DP, GM);                      // and room for them
+    constexpr int CH = DP / 32;                                   // 16-byte pieces of a token's row
+    constexpr int HALF = 16 * 16 * CH, SHALF = rows4_scales(DP, GM);      // bytes of a half's codes, scales
+    constexpr int CF = CH > 4 ? CH / 4 : 1, SF = NX > 4 ? NX / 4 : 1;   // loads of a half's codes, scales
+    constexpr int FETCHES = 2 * (CF + SF);                        // loads of a block's keys, or values
+    constexpr int BLOCK = rows4_block(DP, GM);
+    constexpr int LD = DP + 4;                                    // row pitch of the join in LDS
+    constexpr float TOP = A4_TOP - A4_LAZY;
     extern __shared__ __attribute__((aligned(16))) float att_lds[];
 
-    int id = blockIdx.x;
-    const int groups = a.B * a.Hkv, bh = id % groups;
-    id /= groups;
-    const int rb = id % a.rblocks, split = id / a.rblocks, b = bh / a.Hkv, hk = bh - b * a.Hkv;
+    // sequence and head fastest, splits slowest
+    const int id = blockIdx.x, above = a.by_groups(id), bh = id - above * a.by_groups.d;
+    const int split = a.by_rblocks(above), rb = above - split * a.rblocks, b = a.by_Hkv(bh), hk = bh - b * a.Hkv;
+
+    // Without a window a place is its key, whatever the lengths say: the first pages are looked up
+    // while those are on their way.
+    const int32_t *table = a.table + (int64_t)b * a.table_s;
+    const int lane = threadIdx.x & 63, wave = wave_id(), g = lane >> 4, c = lane & 15;
+    const int begin = split * a.chunk;
+    int first_id = 0;
+    if (P16 && a.window == 0) first_id = table[min(key_page(a, begin + 32 * (wave + NW * (lane >> 1)) + 16 * (lane & 1)), a.width - 1)];
 
     const Range4 kr = range4(a, b, rb);
     const int nrow = min(16 * QT, kr.n * a.g - rb * a.rows);     // live rows
     if (nrow <= 0) return;
-    const int begin = split * a.chunk, end = min(kr.len, begin + a.chunk);
+    const int end = min(kr.len, begin + a.chunk);
     if (begin >= end && split > 0) return;
-
-    const int lane = threadIdx.x & 63, wave = wave_id(), g = lane >> 4, c = lane & 15;
     const S tag = (S)0.f;
 
+    // ---- where a lane's pieces stand ----
+    // In LDS a half's K is [piece][key], so that each lane reads what 16 (8) bytes it needs; its V
+    // stands such that the dwords that 64 lanes read at once lie in 64 banks: pieces of 16 bytes in
+    // the order [group][e][g][c % 2][c / 8] (GM = 64), else [pieces / 4][i][g][piece % 4] (the key is 4g + i, or 4g + 2e +
+    // c % 2).
+    uint8_t *ring = reinterpret_cast<uint8_t *>(att_lds) + wave * rows4_ring(DP, GM, P16);
+    const uint32_t ring_at = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)ring);
+    int kkey[CF], vkey[CF];                 // of the piece that this lane loads: its key, where in the row
+    uint32_t kpart[CF], vpart[CF];
+#pragma unroll
+    for (int f = 0; f < CF; ++f) {
+        const int sl = 64 * f + lane;
+        int piece = sl >> 4;
+        kkey[f] = sl & 15;
+        kpart[f] = 32 * piece < a.D ? 16 * piece : 0;
+        if constexpr (GM == 64) {
+            vkey[f] = 4 * ((sl >> 2) & 3) + 2 * ((sl >> 4) & 1) + ((sl >> 1) & 1);
+            piece = 2 * (sl >> 5) + (sl & 1);
+        } else if constexpr (CH == 2) {
+            vkey[f] = 4 * ((sl >> 1) & 3) + ((sl >> 3) & 3);
+            piece = sl & 1;
+        } else {
+            vkey[f] = 4 * ((sl >> 2) & 3) + ((sl >> 4) & 3);
+            piece = 4 * (sl >> 6) + (sl & 3);
+        }
+        vpart[f] = 32 * piece < a.D ? 16 * piece : 0;
+    }
+    const int n_s = DEFER ? NS : (int)(a.s_ts >> 2);                // groups of a token
+    const uint32_t *kread = reinterpret_cast<const uint32_t *>(ring) + (KW == 4 ? 64 * g + 4 * c : 64 * (g >> 1) + 4 * c + 2 * (g & 1));
+    const uint8_t *vread = ring + 2 * HALF + (GM == 64 ? 16 * (4 * g + 2 * (c & 1) + (c >> 3)) + 4 * ((c >> 1) & 3)
+                                                       : CH == 2 ? 16 * (2 * g + (c >> 3)) + (2 * c & 15) : 16 * (4 * g + (c >> 2)) + 4 * (c & 3));
+    const uint32_t *kscale = reinterpret_cast<const uint32_t *>(ring + 4 * HALF) + (DEFER ? 4 * NS * g : c * n_s);
+    const uint32_t *vscale = reinterpret_cast<const uint32_t *>(ring + 4 * HALF + 2 * SHALF) + 4 * n_s * g;
+    int kgroup[KL], vgroup[VC];             // generic: the groups of this lane's slices and chunks
+#pragma unroll
+    for (int j = 0; j < KL; ++j) kgroup[j] = min(32 * KW * j + 8 * KW * g, a.D - 1) >> a.lg_G;
+#pragma unroll
+    for (int x = 0; x < VC; ++x) vgroup[x] = min(16 * VW * x + VW * c, a.D - 1) >> a.lg_G;
+
+    const uint8_t *kbase = a.k + (int64_t)hk * a.k_hs, *vbase = a.v + (int64_t)hk * a.v_hs;
+    const uint8_t *ksbase = (const uint8_t *)a.ks + (int64_t)hk * a.ks_hs, *vsbase = (const uint8_t *)a.vs + (int64_t)hk * a.vs_hs;
+    auto is_page = [&](int pid) { return (uint32_t)pid < (uint32_t)a.pages; };
+
+    // ---- the lookups ----
+    // P16: lane l, half l % 2 of this wave's block number 32 n + l / 2; else lane l, place l % 32 of block n,
+    // whose page ids stand in LDS for ROWS4_IDS blocks.  A place past the end or on a bad page is token
+    // 0 of page 0: in bounds, and hidden.
+    auto place_of = [&](int n) {
+        return P16 ? begin + 32 * (wave + NW * (32 * n + (lane >> 1))) + 16 * (lane & 1) : begin + 32 * (wave + NW * n) + (lane & 31);
+    };
+    auto key_of = [&](int v) { return key_at(kr, max(0, min(v, end - 1))); };
+    int64_t ko = 0, vo = 0, kso = 0, vso = 0;
+    uint64_t dead = 0;                          // lanes whose place is no key
+    auto look_up = [&](int n, int pid) {
+        const int v = place_of(n), key = key_of(v);
+        const bool ok = v < end && is_page(pid);
+        const int64_t pg = ok ? pid : 0, at = ok ? key - key_page(a, key) * a.page : 0;
+        ko = pg * a.k_ps + at * a.k_ts;
+        vo = pg * a.v_ps + at * a.v_ts;
+        kso = pg * a.ks_ps + at * a.s_ts;
+        vso = pg * a.vs_ps + at * a.s_ts;
+        dead = __ballot(!ok);
+    };
+    int32_t *ids = reinterpret_cast<int32_t *>(ring + 2 * BLOCK);
+    auto hold_ids = [&](int n) {                // of blocks n .. n + ROWS4_IDS - 1
+        int32_t x[ROWS4_IDS / 2];
+#pragma unroll
+        for (int i = 0; i < ROWS4_IDS / 2; ++i) x[i] = table[key_page(a, key_of(place_of(n + 2 * i + (lane >> 5))))];
+#pragma unroll
+        for (int i = 0; i < ROWS4_IDS / 2; ++i) ids[64 * i + lane] = x[i];
+    };
+    auto held = [&](int64_t x, int l) {         // lane l's, uniform
+        const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)x, l), hi = (uint32_t)__builtin_amdgcn_readlane((int)(x >> 32), l);
+        return (int64_t)(((uint64_t)hi << 32) | lo);
+    };
+    auto sent = [&](int64_t x, int l) {         // lane l's, each lane's own l
+        const uint32_t lo = (uint32_t)__shfl((int)(uint32_t)x, l), hi = (uint32_t)__shfl((int)(x >> 32), l);
+        return (int64_t)(((uint64_t)hi << 32) | lo);
+    };
+    // a block's keys or values on their way into its place in the ring (lanes past a half's scales load its last again)
+    uint32_t spart[SF];
+    int stok[SF];
+#pragma unroll
+    for (int f = 0; f < SF; ++f) {
+        spart[f] = min(64 * f + lane, 16 * n_s - 1);
+        stok[f] = (int)spart[f] / n_s;
+        spart[f] = P16 ? 4 * spart[f] : 4 * (spart[f] - stok[f] * n_s);
+    }
+    auto fetch_side = [&](int n, const uint8_t *base, const uint8_t *sbase, int64_t off, int64_t soff, uint32_t ts, const int (&key)[CF], const uint32_t (&part)[CF],
+                          uint32_t to, uint32_t sto) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            if constexpr (P16) {
+                const __amdgpu_buffer_rsrc_t r = make_rsrc(base + held(off, 2 * (n & 31) + t), 0x7fffffffu), rs = make_rsrc(sbase + held(soff, 2 * (n & 31) + t), 0x7fffffffu);
+#pragma unroll
+                for (int f = 0; f < CF; ++f)
+                    if (CH >= 4 || lane < 16 * CH) fetch<16>(to + t * HALF + 1024 * f, r, key[f] * ts + part[f]);
+#pragma unroll
+                for (int f = 0; f < SF; ++f) fetch<4>(sto + t * SHALF + 256 * f, rs, spart[f]);
+            } else {
+#pragma unroll
+                for (int f = 0; f < CF; ++f) {
+                    const uint8_t *p = base + sent(off, 16 * t + key[f]) + part[f];
+                    if (CH >= 4 || lane < 16 * CH) fetch<16>(to + t * HALF + 1024 * f, p);
+                }
+#pragma unroll
+                for (int f = 0; f < SF; ++f) fetch<4>(sto + t * SHALF + 256 * f, sbase + sent(soff, 16 * t + stok[f]) + spart[f]);
+            }
+        }
+    };
+    auto fetch_k = [&](int n) { fetch_side(n, kbase, ksbase, ko, kso, a.k_ts, kkey, kpart, ring_at + (n & 1) * BLOCK, ring_at + (n & 1) * BLOCK + 4 * HALF); };
+    auto fetch_v = [&](int n) {
+        fetch_side(n, vbase, vsbase, vo, vso, a.v_ts, vkey, vpart, ring_at + (n & 1) * BLOCK + 2 * HALF, ring_at + (n & 1) * BLOCK + 4 * HALF + 2 * SHALF);
+    };
+
+    const int all_blocks = (max(0, end - begin) + 31) >> 5;
+    const int blocks = all_blocks > wave ? (all_blocks - wave + NW - 1) / NW : 0;      // of this wave
+    uint64_t gone[3] = {0, 0, 0};      // places that are no keys, of blocks n, n + 1 and n + 2
+    int nid = 0;                       // P16: the next lookup's page ids
+    if (blocks > 0) {
+        if constexpr (P16) {
+            const int first = a.window == 0 ? first_id : table[key_page(a, key_of(place_of(0)))];
+            nid = table[key_page(a, key_of(place_of(1)))];
+            look_up(0, first);
+            gone[0] = dead & 3, gone[1] = dead >> 2 & 3;
+            fetch_k(0);
+            fetch_v(0);
+            fetch_k(1);
+            fetch_v(1);
+        } else {
+            hold_ids(0);
+            for (int n = 0; n < 2; ++n) {
+                look_up(n, ids[32 * n + (lane & 31)]);
+                gone[n] = dead;
+                fetch_k(n);
+                fetch_v(n);
+            }
+        }
+    }
+
+    // ---- the rows of q ----
     int4_t q[QT][KJ];
     int vhi[QT], vlo[QT];      // the row's keys: [vlo, vhi), and those below the sinks
-    float sl[QT];
+    float sl[QT], qsum[QT][NS];
 #pragma unroll
     for (int qt = 0; qt < QT; ++qt) {
         const int r = rb * a.rows + 16 * qt + c;
-        const int i = r / a.g, hq = hk * a.g + (r - i * a.g);
+        const int i = a.by_g(r), hq = hk * a.g + (r - i * a.g);
         const bool live = 16 * qt + c < nrow;
         vhi[qt] = live ? kr.L - kr.n + i + 1 : 0;
         vlo[qt] = a.window > 0 ? vhi[qt] - a.window : 0;
@@ -190,188 +428,137 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(rows4_o
             const int d = 32 * KW * (j / KW) + 8 * KW * g + 8 * (j % KW);
             q[qt][j] = *reinterpret_cast<const int4_t *>(row + (d < a.D ? 2 * d : 0));
             if (!live || d >= a.D) q[qt][j] = int4_t{0, 0, 0, 0};
-            if constexpr (!__is_same(S, f16_t)) top = fmaxf(top, largest(q[qt][j], tag));
+            top = fmaxf(top, largest(q[qt][j], tag));
         }
         sl[qt] = a.scale * ATT_LOG2E;
-        if constexpr (!__is_same(S, f16_t)) {
+        if constexpr (DEFER || !__is_same(S, f16_t)) {
             top = fmaxf(top, __shfl_xor(top, 16));
             top = fmaxf(top, __shfl_xor(top, 32));
             const int up = rise_of(top);
 #pragma unroll
-            for (int j = 0; j < KJ; ++j) q[qt][j] = to_f16(q[qt][j], up);
-            sl[qt] = ldexpf(sl[qt], -up);
+            for (int j = 0; j < KJ; ++j) q[qt][j] = to_f16(q[qt][j], up, tag);
+            sl[qt] = fminf(ldexpf(sl[qt], (DEFER ? 22 : 0) - up), 3e38f);
         }
         sl[qt] = above_zero(sl[qt]);
 #pragma unroll
         for (int j = 0; j < KJ; ++j) q[qt][j] = code_order(q[qt][j]);
+        if constexpr (DEFER) {
+#pragma unroll
+            for (int ns = 0; ns < NS; ++ns) {
+                float4_t sum = float4_t{0.f, 0.f, 0.f, 0.f};      // of a key whose codes are all 1
+#pragma unroll
+                for (int w = 0; w < KW; ++w) {
+                    int4_t &x = q[qt][KW * ns + w];
+                    const half2_t part = half2_t{(f16_t)0.0625f, (f16_t)0.0625f};
+                    x[1] = (int)as_u32(as_half2((uint32_t)x[1]) * part);
+                    x[3] = (int)as_u32(as_half2((uint32_t)x[3]) * part);
+                    sum = mfma_16(places4(0x11111111u), x, sum, f16_t());
+                }
+                qsum[qt][ns] = sum[0];
+            }
+        }
     }
     // keys that every row of the block sees: [all_lo, all_hi) (and those below the sinks)
-    const int all_hi = min(kr.hi, kr.L - kr.n + rb * a.rows / a.g + 1);
+    const int all_hi = min(kr.hi, kr.L - kr.n + a.by_g(rb * a.rows) + 1);
     const int all_lo = a.window > 0 ? kr.hi - a.window : 0;
 
-    uint32_t koff[KL], ksoff[KL], voff[VC], vsoff[VC];
-    bool kin[KL], vin[VC];
-#pragma unroll
-    for (int j = 0; j < KL; ++j) {
-        const int d = 32 * KW * j + 8 * KW * g;
-        kin[j] = d < a.D;
-        koff[j] = P16 ? (kin[j] ? (uint32_t)c * a.k_ts + d / 2 : ATT_OOB) : (kin[j] ? d / 2 : 0);
-        ksoff[j] = P16 ? (kin[j] ? (uint32_t)c * a.s_ts + 4 * (d >> a.lg_G) : ATT_OOB) : (kin[j] ? 4 * (d >> a.lg_G) : 0);
-    }
-#pragma unroll
-    for (int x = 0; x < VC; ++x) {
-        const int d = 16 * VW * x + VW * c;
-        vin[x] = d < a.D;
-        voff[x] = P16 ? (vin[x] ? 4u * g * a.v_ts + d / 2 : ATT_OOB) : (vin[x] ? d / 2 : 0);
-        vsoff[x] = P16 ? (vin[x] ? 4u * g * a.s_ts + 4 * (d >> a.lg_G) : ATT_OOB) : (vin[x] ? 4 * (d >> a.lg_G) : 0);
-    }
-
-    const uint8_t *kbase = a.k + (int64_t)hk * a.k_hs, *vbase = a.v + (int64_t)hk * a.v_hs;
-    const uint8_t *ksbase = (const uint8_t *)a.ks + (int64_t)hk * a.ks_hs, *vsbase = (const uint8_t *)a.vs + (int64_t)hk * a.vs_hs;
-    const int32_t *table = a.table + (int64_t)b * a.table_s;
-
-    // page of (each half of) block blk: P16 two uniform ids, else the id of place lane % 32
-    struct Ids {
-        int p[2];
-    };
-    auto ids_of = [&](int blk) {
-        Ids r;
-        const int v = begin + 32 * blk;
-        if constexpr (P16) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int kk = __builtin_amdgcn_readfirstlane(key_at(kr, max(0, min(v + 16 * h, end - 1))));
-                r.p[h] = table[key_page(a, kk)];
-            }
-        } else {
-            r.p[0] = table[key_page(a, key_at(kr, max(0, min(v + (lane & 31), end - 1))))];
-            r.p[1] = 0;
-        }
-        return r;
-    };
-    auto is_page = [&](int pid) { return (uint32_t)pid < (uint32_t)a.pages; };
-
-    uint32_t kd[2][KL][KW], ksd[2][KL], vd[8][VC], vsd[8][VC];
-    auto load_k = [&](int blk, const Ids &ids) {
-        const int v = begin + 32 * blk;
-        if constexpr (P16) {
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const int vv = __builtin_amdgcn_readfirstlane(v + 16 * t), pid = __builtin_amdgcn_readfirstlane(ids.p[t]);
-                const bool ok = vv < end && is_page(pid);
-                const int kk = key_at(kr, vv), at = ok ? kk - key_page(a, kk) * a.page : 0, live = min(16, end - vv);
-                const int64_t pg = ok ? pid : 0;
-                const __amdgpu_buffer_rsrc_t r = make_rsrc(kbase + pg * a.k_ps + (int64_t)at * a.k_ts, ok ? (uint32_t)(live - 1) * a.k_ts + (uint32_t)a.D / 2 : 0u);
-                const __amdgpu_buffer_rsrc_t rs = make_rsrc(ksbase + pg * a.ks_ps + (int64_t)at * a.s_ts, ok ? (uint32_t)live * a.s_ts : 0u);
-#pragma unroll
-                for (int j = 0; j < KL; ++j) {
-                    ksd[t][j] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rs, ksoff[j], 0, 0);
-                    load_dwords<LOAD_DEFAULT>(r, koff[j], kd[t][j], KW);
-                }
-            }
-        } else {
-            const bool there = v + (lane & 31) < end && is_page(ids.p[0]);
-            const int kk = key_at(kr, max(0, min(v + (lane & 31), end - 1))), at = kk - key_page(a, kk) * a.page, pg = there ? ids.p[0] : 0;
-            const int64_t off = (int64_t)pg * a.k_ps + (int64_t)at * a.k_ts, soff = (int64_t)pg * a.ks_ps + (int64_t)at * a.s_ts;
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                auto from = [&](int64_t x) {
-                    const uint32_t lo = (uint32_t)__shfl((int)(uint32_t)x, 16 * t + c), hi = (uint32_t)__shfl((int)(x >> 32), 16 * t + c);
-                    return (int64_t)(((uint64_t)hi << 32) | lo);
-                };
-                const uint8_t *row = kbase + from(off), *srow = ksbase + from(soff);
-#pragma unroll
-                for (int j = 0; j < KL; ++j) {
-                    ksd[t][j] = *reinterpret_cast<const uint32_t *>(srow + ksoff[j]);
-                    if (!kin[j]) ksd[t][j] = 0;
-                    if constexpr (KW == 4) {
-                        const int4_t w = *reinterpret_cast<const int4_t *>(row + koff[j]);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) kd[t][j][i] = (uint32_t)w[i];
-                    } else {
-                        const int2v_t w = *reinterpret_cast<const int2v_t *>(row + koff[j]);
-                        kd[t][j][0] = (uint32_t)w[0];
-                        kd[t][j][1] = (uint32_t)w[1];
-                    }
-                }
-            }
-        }
-    };
-    auto load_v = [&](int blk, const Ids &ids) {
-        const int v = begin + 32 * blk;
-        if constexpr (P16) {
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const int vv = __builtin_amdgcn_readfirstlane(v + 16 * t), pid = __builtin_amdgcn_readfirstlane(ids.p[t]);
-                const bool ok = vv < end && is_page(pid);
-                const int kk = key_at(kr, vv), at = ok ? kk - key_page(a, kk) * a.page : 0, live = min(16, end - vv);
-                const int64_t pg = ok ? pid : 0;
-                const __amdgpu_buffer_rsrc_t r = make_rsrc(vbase + pg * a.v_ps + (int64_t)at * a.v_ts, ok ? (uint32_t)(live - 1) * a.v_ts + (uint32_t)a.D / 2 : 0u);
-                const __amdgpu_buffer_rsrc_t rs = make_rsrc(vsbase + pg * a.vs_ps + (int64_t)at * a.s_ts, ok ? (uint32_t)live * a.s_ts : 0u);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int x = 0; x < VC; ++x) {
-                        const uint32_t o = voff[x] == ATT_OOB ? ATT_OOB : voff[x] + i * a.v_ts, os = vsoff[x] == ATT_OOB ? ATT_OOB : vsoff[x] + i * a.s_ts;
-                        vsd[4 * t + i][x] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rs, os, 0, 0);
-                        if constexpr (VW == 8)
-                            vd[4 * t + i][x] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, o, 0, 0);
-                        else
-                            vd[4 * t + i][x] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, o, 0, 0);
-                    }
-            }
-        } else {
-            const bool there = v + (lane & 31) < end && is_page(ids.p[0]);
-            const int kk = key_at(kr, max(0, min(v + (lane & 31), end - 1))), at = kk - key_page(a, kk) * a.page, pg = there ? ids.p[0] : 0;
-            const int64_t off = (int64_t)pg * a.v_ps + (int64_t)at * a.v_ts, soff = (int64_t)pg * a.vs_ps + (int64_t)at * a.s_ts;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int src = 16 * (e >> 2) + 4 * g + (e & 3);
-                auto from = [&](int64_t x) {
-                    const uint32_t lo = (uint32_t)__shfl((int)(uint32_t)x, src), hi = (uint32_t)__shfl((int)(x >> 32), src);
-                    return (int64_t)(((uint64_t)hi << 32) | lo);
-                };
-                const uint8_t *row = vbase + from(off), *srow = vsbase + from(soff);
-#pragma unroll
-                for (int x = 0; x < VC; ++x) {
-                    vsd[e][x] = *reinterpret_cast<const uint32_t *>(srow + vsoff[x]);
-                    if (!vin[x]) vsd[e][x] = 0;
-                    if constexpr (VW == 8)
-                        vd[e][x] = *reinterpret_cast<const uint32_t *>(row + voff[x]);
-                    else
-                        vd[e][x] = *reinterpret_cast<const uint16_t *>(row + voff[x]);
-                }
-            }
-        }
-    };
-
-    float m[QT], l[QT];
-    float4_t o[QT][XT];
+    // m: the running maximum, DEFER: with the exponent `rise` of the largest scale so far added
+    float m[QT], l[QT], rise = -24.f, most = 0x1p-24f;
+    float4_t o[QT][XT], oz[QT][NS];      // oz: sum of p s z, alike in all four
 #pragma unroll
     for (int qt = 0; qt < QT; ++qt) {
         m[qt] = -INFINITY;
         l[qt] = 0.f;
 #pragma unroll
         for (int x = 0; x < XT; ++x) o[qt][x] = float4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int x = 0; x < NS; ++x) oz[qt][x] = float4_t{0.f, 0.f, 0.f, 0.f};
     }
 
-    const int blocks = (max(0, end - begin) + 31) >> 5;
-    if (wave < blocks) {
-        Ids cur = ids_of(wave), nxt = ids_of(wave + NW);
-        load_k(wave, cur);
-        load_v(wave, cur);
-        for (int blk = wave; blk < blocks; blk += NW) {
-            const int v0 = begin + 32 * blk;
-            float4_t s[QT][2];
+    for (int n = 0; n < blocks; ++n) {
+        const int v0 = begin + 32 * (wave + NW * n);
+        const int in_ring = (n & 1) * BLOCK;
+        // loads of V n, K n + 1 and V n + 1 stay on their way
+        wait_loads<3 * FETCHES>();
+        uint32_t kd[2][KL][KW], ksd[2][DEFER ? 4 : KL][NS];
 #pragma unroll
-            for (int qt = 0; qt < QT; ++qt)
+        for (int t = 0; t < 2; ++t) {
+            const uint32_t *p = kread + (in_ring + t * HALF) / 4, *ps = kscale + (in_ring + t * SHALF) / 4;
 #pragma unroll
-                for (int t = 0; t < 2; ++t) s[qt][t] = float4_t{0.f, 0.f, 0.f, 0.f};
+            for (int j = 0; j < KL; ++j) {
+                if constexpr (KW == 4) {
+                    const int4_t w = *reinterpret_cast<const int4_t *>(p + 256 * j);
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+                    for (int i = 0; i < 4; ++i) kd[t][j][i] = (uint32_t)w[i];
+                } else {
+                    const int2v_t w = *reinterpret_cast<const int2v_t *>(p + 128 * j);
+                    kd[t][j][0] = (uint32_t)w[0];
+                    kd[t][j][1] = (uint32_t)w[1];
+                }
+            }
+            if constexpr (DEFER) {
+#pragma unroll
+                for (int i = 0; i < NS; ++i) {
+                    const int4_t w = *reinterpret_cast<const int4_t *>(ps + 4 * i);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) (&ksd[t][0][0])[4 * i + e] = (uint32_t)w[e];
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < KL; ++j) {
+                    ksd[t][j][0] = ps[kgroup[j]];
+                    if (32 * KW * j + 8 * KW * g >= a.D) ksd[t][j][0] = 0;
+                }
+            }
+        }
+        // the block after the next: its lookups, its keys in this one's place
+        if constexpr (P16) {
+            if (((n + 2) & 31) == 0) {
+                look_up((n + 2) >> 5, nid);
+                nid = table[key_page(a, key_of(place_of(((n + 2) >> 5) + 1)))];
+            }
+            gone[2] = dead >> (2 * ((n + 2) & 31)) & 3;
+        } else {
+            if ((n + 2) % ROWS4_IDS == 0) hold_ids(n + 2);
+            look_up(n + 2, ids[32 * ((n + 2) % ROWS4_IDS) + (lane & 31)]);
+            gone[2] = dead;
+        }
+        wait_reads();
+        fetch_k(n + 2);
+
+        float4_t s[QT][2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            if constexpr (DEFER) {
+                float4_t acc[QT][NS];
+#pragma unroll
+                for (int ns = 0; ns < NS; ++ns) {
+#pragma unroll
+                    for (int qt = 0; qt < QT; ++qt) acc[qt][ns] = float4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int w = 0; w < KW; ++w) {
+                        const int4_t kf = places4(kd[t][ns][w]);
+#pragma unroll
+                        for (int qt = 0; qt < QT; ++qt) acc[qt][ns] = mfma_16(kf, q[qt][KW * ns + w], acc[qt][ns], f16_t());
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int ns = 0; ns < NS; ++ns) {
+                        const half2_t sz = as_half2(ksd[t][i][ns]);
+#pragma unroll
+                        for (int qt = 0; qt < QT; ++qt) {
+                            const float d = fmaf(-(float)sz[1], qsum[qt][ns], acc[qt][ns][i]);
+                            s[qt][t][i] = fmaf(d, (float)sz[0], ns == 0 ? 0.f : s[qt][t][i]);      // (one instruction from fp16)
+                        }
+                    }
+            } else {
+#pragma unroll
+                for (int qt = 0; qt < QT; ++qt) s[qt][t] = float4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int jl = 0; jl < KL; ++jl) {
-                    const Zero z = zero_of(ksd[t][jl], ksd[t][jl]);
+                    const Zero z = zero_of(ksd[t][jl][0], ksd[t][jl][0]);
 #pragma unroll
                     for (int w = 0; w < KW; ++w) {
                         const int4_t kf = values8(kd[t][jl][w], z);
@@ -379,93 +566,204 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(rows4_o
                         for (int qt = 0; qt < QT; ++qt) s[qt][t] = mfma_16(kf, q[qt][KW * jl + w], s[qt][t], f16_t());
                     }
                 }
-            // the next block's keys load under this block's softmax and second product
-            load_k(blk + NW, nxt);
+            }
+        }
 
-            // a half needs a look at its keys where not every row sees all of them
-            int key0[2];
-            bool masked = v0 + 32 > end;
+        // loads of K n + 1, V n + 1 and K n + 2 stay on their way
+        wait_loads<3 * FETCHES>();
+        uint32_t vd[2][VC][VK], vsd[2][4][DEFER ? NS : VC];
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                key0[t] = key_at(kr, v0 + 16 * t);
-                masked = masked || key0[t] + 16 > all_hi || (key0[t] < all_lo && key0[t] + 16 > a.sinks);
-                if constexpr (P16) masked = masked || !is_page(cur.p[t]);
-            }
-            if constexpr (!P16) masked = masked || __any(!is_page(cur.p[0]));
-            if (masked) {
+        for (int t = 0; t < 2; ++t) {
+            const uint8_t *p = vread + in_ring + t * HALF;
+            const uint32_t *ps = vscale + (in_ring + t * SHALF) / 4;
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+            for (int x = 0; x < VC; ++x)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int key = key0[t] + 4 * g + i;
-                        const int pid = P16 ? cur.p[t] : __shfl(cur.p[0], 16 * t + 4 * g + i);     // (by all lanes)
-                        const bool off = v0 + 16 * t + 4 * g + i >= end || !is_page(pid);
-#pragma unroll
-                        for (int qt = 0; qt < QT; ++qt)
-                            if (off || key >= vhi[qt] || (key < vlo[qt] && key >= a.sinks)) s[qt][t][i] = -INFINITY;
-                        // values that no row sees may hold anything: they meet p = 0 as zeros
-                        if (off || key >= kr.hi || (key < kr.lo && key >= a.sinks)) {
-#pragma unroll
-                            for (int x = 0; x < VC; ++x) vsd[4 * t + i][x] = 0;
-                        }
-                    }
-            }
-            int4_t p[QT];
-#pragma unroll
-            for (int qt = 0; qt < QT; ++qt) {
-                float x[8], mx = -INFINITY;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    x[e] = s[qt][e >> 2][e & 3] * sl[qt];
-                    mx = fmaxf(mx, x[e]);
+                for (int e = 0; e < VK; ++e) {
+                    if constexpr (GM == 64)
+                        vd[t][x][e] = *reinterpret_cast<const uint32_t *>(p + 256 * (2 * x + e));
+                    else if constexpr (CH == 2)
+                        vd[t][x][e] = *reinterpret_cast<const uint16_t *>(p + 128 * e);
+                    else
+                        vd[t][x][e] = *reinterpret_cast<const uint32_t *>(p + 1024 * x + 256 * e);
                 }
+            if constexpr (DEFER) {
+#pragma unroll
+                for (int i = 0; i < NS; ++i) {
+                    const int4_t w = *reinterpret_cast<const int4_t *>(ps + 4 * i);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) (&vsd[t][0][0])[4 * i + e] = (uint32_t)w[e];
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int x = 0; x < VC; ++x) vsd[t][i][x] = ps[i * n_s + vgroup[x]];
+            }
+        }
+        wait_reads();
+        fetch_v(n + 2);
+
+        // a half needs a look at its keys where not every row sees all of them
+        int key0[2];
+        bool masked = gone[0] != 0 || v0 + 32 > end;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            key0[t] = key_at(kr, v0 + 16 * t);
+            masked = masked || key0[t] + 16 > all_hi || (key0[t] < all_lo && key0[t] + 16 > a.sinks);
+        }
+        if (masked) {
+            // (the comparisons stay in here)
+            asm volatile("" : "+s"(key0[0]), "+s"(key0[1]));
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int key = key0[t] + 4 * g + i;
+                    const bool off = v0 + 16 * t + 4 * g + i >= end || (gone[0] >> (P16 ? t : 16 * t + 4 * g + i) & 1);
+#pragma unroll
+                    for (int qt = 0; qt < QT; ++qt)
+                        if (off || key >= vhi[qt] || (key < vlo[qt] && key >= a.sinks)) s[qt][t][i] = -INFINITY;
+                    // values that no row sees may hold anything: they meet p = 0 as zeros
+                    if (off || key >= kr.hi || (key < kr.lo && key >= a.sinks)) {
+#pragma unroll
+                        for (int x = 0; x < (DEFER ? NS : VC); ++x) vsd[t][i][x] = 0;
+                    }
+                }
+        }
+        gone[0] = gone[1];
+        gone[1] = gone[2];
+        if constexpr (DEFER) {      // the largest scale so far, up to a power of two
+            half2_t top = as_half2(vsd[0][0][0]);
+#pragma unroll
+            for (int e = 1; e < 8 * NS; ++e) top = __builtin_elementwise_max(top, as_half2(vsd[e / (4 * NS)][e / NS % 4][e % NS]));
+            float mine = (float)top[0];
+            if (__any(mine > most)) {
+#pragma unroll
+                for (int x = 1; x < 64; x <<= 1) mine = fmaxf(mine, __shfl_xor(mine, x));
+                const float to = (float)__builtin_amdgcn_frexp_expf(mine), f = __builtin_amdgcn_exp2f(rise - to);
+#pragma unroll
+                for (int qt = 0; qt < QT; ++qt) {
+                    m[qt] += to - rise;
+                    l[qt] *= f;
+#pragma unroll
+                    for (int x = 0; x < XT; ++x) o[qt][x] *= f;
+#pragma unroll
+                    for (int x = 0; x < NS; ++x) oz[qt][x] *= f;
+                }
+                rise = to;
+                most = __builtin_amdgcn_exp2f(to);
+            }
+        }
+        float x[QT][8];
+        int4_t p[QT];
+#pragma unroll
+        for (int qt = 0; qt < QT; ++qt) {
+            float mx = s[qt][0][0];
+#pragma unroll
+            for (int e = 1; e < 8; ++e) mx = fmaxf(mx, s[qt][e >> 2][e & 3]);
+            mx *= sl[qt];
+            if constexpr (DEFER) mx += rise;
+            if (__any(mx > m[qt] + A4_LAZY)) {         // also the first finite maximum: m is -inf
                 mx = fmaxf(mx, __shfl_xor(mx, 16));
                 mx = fmaxf(mx, __shfl_xor(mx, 32));
-                const float mn = fmaxf(m[qt], mx), ms = mn == -INFINITY ? 0.f : mn;
-                if (__any(mn > m[qt])) {
-                    const float al = __builtin_amdgcn_exp2f(m[qt] - ms);
-                    l[qt] *= al;
+                const float mn = fmaxf(m[qt], mx), al = __builtin_amdgcn_exp2f(m[qt] - (mn == -INFINITY ? 0.f : mn));
+                l[qt] *= al;
 #pragma unroll
-                    for (int xx = 0; xx < XT; ++xx) o[qt][xx] *= al;
-                    m[qt] = mn;
-                }
-                const float base = ms - A4_TOP;
-                float sum = 0.f;
+                for (int xx = 0; xx < XT; ++xx) o[qt][xx] *= al;
+                if constexpr (DEFER) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    x[e] = __builtin_amdgcn_exp2f(x[e] - base);
-                    sum += x[e];
+                    for (int xx = 0; xx < NS; ++xx) oz[qt][xx] *= al;
                 }
-                l[qt] += sum;
-                p[qt] = int4_t{pack2(x[0], x[1], f16_t()), pack2(x[2], x[3], f16_t()), pack2(x[4], x[5], f16_t()), pack2(x[6], x[7], f16_t())};
+                m[qt] = mn;
             }
+            const float base = (m[qt] == -INFINITY ? 0.f : m[qt]) - TOP;
+            float sum = 0.f;
 #pragma unroll
-            for (int x = 0; x < VC; ++x) {
-                Zero z[4];
+            for (int e = 0; e < 8; ++e) {
+                x[qt][e] = __builtin_amdgcn_exp2f(fmaf(s[qt][e >> 2][e & 3], sl[qt], -base));
+                sum += x[qt][e];
+            }
+            l[qt] += sum;
+            if constexpr (!DEFER)
+                p[qt] = int4_t{pack2(x[qt][0], x[qt][1], f16_t()), pack2(x[qt][2], x[qt][3], f16_t()), pack2(x[qt][4], x[qt][5], f16_t()),
+                               pack2(x[qt][6], x[qt][7], f16_t())};
+        }
+        if constexpr (DEFER) {
 #pragma unroll
-                for (int y = 0; y < 4; ++y) z[y] = zero_of(vsd[2 * y][x], vsd[2 * y + 1][x]);
+            for (int ns = 0; ns < NS; ++ns) {
+                int4_t zf;
 #pragma unroll
-                for (int h = 0; h < VW / 4; ++h) {
-                    // four elements of two keys a dword
-                    uint32_t w[4];
+                for (int y = 0; y < 4; ++y) {
+                    const uint32_t s0 = vsd[y >> 1][2 * y & 3][ns], s1 = vsd[y >> 1][(2 * y & 3) + 1][ns];
+                    zf[y] = (int)__builtin_amdgcn_perm(s1, s0, 0x07060302u);
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) w[y] = __builtin_amdgcn_perm(vd[2 * y + 1][x], vd[2 * y][x], h ? 0x07060302u : 0x05040100u);
+                    for (int qt = 0; qt < QT; ++qt)
+                        p[qt][y] = pack2(fmaf(x[qt][2 * y], (float)as_half2(s0)[0], 0.f), fmaf(x[qt][2 * y + 1], (float)as_half2(s1)[0], 0.f), f16_t());
+                }
 #pragma unroll
-                    for (int n = 0; n < 4; ++n) {
+                for (int qt = 0; qt < QT; ++qt) oz[qt][ns] = mfma_16(zf, p[qt], oz[qt][ns], f16_t());
+                // w[h][y]: elements 4h .. 4h + 3 of keys 2y and 2y + 1
+                uint32_t w[VW / 4][4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    if constexpr (GM == 64) {
+                        const uint32_t mine = vd[y >> 1][ns][y & 1], other = (uint32_t)__builtin_amdgcn_mov_dpp((int)mine, 0xb1, 0xf, 0xf, true);   // lane c ^ 1's
+                        w[0][y] = __builtin_amdgcn_perm(mine, other, c & 1 ? 0x07060302u : 0x01000504u);
+                    } else {
+                        const uint32_t d0 = vd[y >> 1][ns][2 * y & 3], d1 = vd[y >> 1][ns][(2 * y & 3) + 1];
+                        w[0][y] = __builtin_amdgcn_perm(d1, d0, 0x05040100u);
+                        w[VW / 4 - 1][y] = __builtin_amdgcn_perm(d1, d0, 0x07060302u);
+                    }
+                }
+#pragma unroll
+                for (int h = 0; h < VW / 4; ++h)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
                         int4_t vf;
 #pragma unroll
-                        for (int y = 0; y < 4; ++y) vf[y] = n & 1 ? value2<true>(w[y] >> (n & 2 ? 8 : 0), z[y]) : value2<false>(w[y] >> (n & 2 ? 8 : 0), z[y]);
+                        for (int y = 0; y < 4; ++y) vf[y] = places4(w[h][y])[e];
 #pragma unroll
-                        for (int qt = 0; qt < QT; ++qt) o[qt][VW * x + 4 * h + n] = mfma_16(vf, p[qt], o[qt][VW * x + 4 * h + n], f16_t());
+                        for (int qt = 0; qt < QT; ++qt) o[qt][VW * ns + 4 * h + e] = mfma_16(vf, p[qt], o[qt][VW * ns + 4 * h + e], f16_t());
+                    }
+            }
+        } else {
+#pragma unroll
+            for (int xc = 0; xc < VC; ++xc) {
+                Zero z[4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) z[y] = zero_of(vsd[y >> 1][2 * y & 3][xc], vsd[y >> 1][(2 * y & 3) + 1][xc]);
+#pragma unroll
+                for (int h = 0; h < VW / 4; ++h) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) w[y] = __builtin_amdgcn_perm(vd[y >> 1][xc][(2 * y & 3) + 1], vd[y >> 1][xc][2 * y & 3], h ? 0x07060302u : 0x05040100u);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        int4_t vf;
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) vf[y] = e & 1 ? value2<true>(e & 2 ? w[y] >> 8 : w[y], z[y]) : value2<false>(e & 2 ? w[y] >> 8 : w[y], z[y]);
+#pragma unroll
+                        for (int qt = 0; qt < QT; ++qt) o[qt][VW * xc + 4 * h + e] = mfma_16(vf, p[qt], o[qt][VW * xc + 4 * h + e], f16_t());
                     }
                 }
             }
-            load_v(blk + NW, nxt);
-            cur = nxt;
-            nxt = ids_of(blk + 2 * NW);
         }
     }
+    if constexpr (DEFER) {      // the codes' places, scales and zero-points
+#pragma unroll
+        for (int qt = 0; qt < QT; ++qt)
+#pragma unroll
+            for (int x = 0; x < XT; ++x) {
+                const float f = (x & 1 ? 0x1p18f : 0x1p22f);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[qt][x][i] = fmaf(o[qt][x][i], f, -oz[qt][x / VW][0]);
+            }
+    }
 
+    // the ring is done with: nothing is on its way into LDS any more, from no wave
+    wait_loads<0>();
+    __syncthreads();
     // join the waves
     float *ml = att_lds + NW * nrow * LD;      // [wave][row][m, l]
 #pragma unroll
@@ -503,14 +801,14 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(rows4_o
             tot += f * ml[(w * nrow + row) * 2 + 1];
             sum += f * *reinterpret_cast<const float4_t *>(att_lds + (w * nrow + row) * LD + d);
         }
-        const int r = rb * a.rows + row, i = r / a.g, hq = hk * a.g + (r - i * a.g);
+        const int r = rb * a.rows + row, i = a.by_g(r), hq = hk * a.g + (r - i * a.g);
         const int64_t t = kr.t0 + i;
         // no sum: no key, or scores of -inf by overflow (of a split: the join looks)
         const bool none = tot == 0.f && (a.splits > 1 || !row_sees(a, b, kr, i));
         const float inv = 1.f / (tot > 0.f ? tot : NAN);
 #pragma unroll
         for (int e = 0; e < 4; ++e) sum[e] = none ? 0.f : sum[e] * inv;
-        const float lse2 = none ? -INFINITY : mm - A4_TOP + __builtin_amdgcn_logf(tot > 0.f ? tot : NAN);
+        const float lse2 = none ? -INFINITY : mm - TOP + __builtin_amdgcn_logf(tot > 0.f ? tot : NAN);
         if (a.splits == 1) {
             *reinterpret_cast<int2v_t *>((char *)a.out + t * a.o_ts + (int64_t)hq * a.o_hs + 2 * d) =
                 int2v_t{pack2(sum[0], sum[1], tag), pack2(sum[2], sum[3], tag)};
@@ -533,7 +831,6 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(rows4_o
 // ---------------------------------------------------------------------------
 __host__ __device__ constexpr int tiles4_keys(int D) { return D <= 128 ? 64 : 32; }
 __host__ __device__ constexpr int tiles4_waves(int D) { return D <= 128 ? 8 : 4; }
-constexpr float A4_LAZY = 4.f;         // a maximum may be exceeded by this much (base 2)
 
 // 8 codes of a dword as f16, in their own order: byte b's two codes stand at bits 0 and 20
 __device__ __forceinline__ int4_t values8_in_order(uint32_t w, uint32_t sc)
@@ -564,12 +861,9 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DC <= 1
     extern __shared__ __attribute__((aligned(16))) uint8_t att_tiles[];   // K [2][TILE], V [2][TILE]
     typedef __attribute__((address_space(3))) short4v_t lds4_t;
 
-    int id = blockIdx.x;
-    const int groups = a.B * a.Hkv;
-    const int bh = id % groups;                          // sequence and head fastest: one head's blocks share an L2
-    id /= groups;
-    const int split = id % a.splits, rb = a.rblocks - 1 - id / a.splits;   // the longest blocks first
-    const int b = bh / a.Hkv, hk = bh - b * a.Hkv;
+    const int above = a.by_groups(blockIdx.x), bh = blockIdx.x - above * a.by_groups.d;     // sequence and head fastest: one head's blocks share an L2
+    const int top = above / a.splits, split = above - top * a.splits, rb = a.rblocks - 1 - top;   // the longest blocks first
+    const int b = a.by_Hkv(bh), hk = bh - b * a.Hkv;
 
     const Range4 kr = range4(a, b, rb);
     const int nrow = min(32 * NW, kr.n * a.g - rb * a.rows);
@@ -581,7 +875,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DC <= 1
     const S tag = (S)0.f;
 
     // this lane's row
-    const int r = rb * a.rows + 32 * wave + c, i = r / a.g, hq = hk * a.g + (r - i * a.g);
+    const int r = rb * a.rows + 32 * wave + c, i = a.by_g(r), hq = hk * a.g + (r - i * a.g);
     const bool live = 32 * wave + c < nrow;
     const int vhi = live ? kr.L - kr.n + i + 1 : 0, vlo = a.window > 0 ? vhi - a.window : 0;
     int4_t q[QJ];
@@ -599,7 +893,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DC <= 1
         if constexpr (!__is_same(S, f16_t)) {
             const int up = rise_of(fmaxf(top, __shfl_xor(top, 32)));
 #pragma unroll
-            for (int j = 0; j < QJ; ++j) q[j] = to_f16(q[j], up);
+            for (int j = 0; j < QJ; ++j) q[j] = to_f16(q[j], up, tag);
             sl = ldexpf(sl, -up);
         }
         sl = above_zero(sl);
@@ -609,7 +903,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DC <= 1
     // keys that some row of the wave sees, and keys that all of them see
     const int wr0 = rb * a.rows + 32 * wave, wr1 = min(wr0 + 31, rb * a.rows + nrow - 1);
     const bool wlive = 32 * wave < nrow;
-    const int whi = wlive ? kr.L - kr.n + wr1 / a.g + 1 : 0, wall_hi = wlive ? kr.L - kr.n + wr0 / a.g + 1 : 0;
+    const int whi = wlive ? kr.L - kr.n + a.by_g(wr1) + 1 : 0, wall_hi = wlive ? kr.L - kr.n + a.by_g(wr0) + 1 : 0;
     const int wlo = a.window > 0 ? wall_hi - a.window : 0, wall_lo = a.window > 0 ? whi - a.window : 0;
 
     const uint8_t *kbase = a.k + (int64_t)hk * a.k_hs, *vbase = a.v + (int64_t)hk * a.v_hs;
@@ -848,7 +1142,7 @@ __global__ __launch_bounds__(256) void attend4_join_kernel(const Attend4Args a)
     const int per = (int)(((int64_t)a.max_q * a.Hq + RG - 1) / RG);
     const int b = blockIdx.x / per, wave = wave_id(), part_wave = wave % JW, lane = threadIdx.x & 63;
     const int r = (blockIdx.x - b * per) * RG + wave / JW, i = r / a.Hq, hq = r - i * a.Hq;
-    const int rb = (min(i, a.max_q - 1) * a.g + hq % a.g) / a.rows;
+    const int rb = (min(i, a.max_q - 1) * a.g + hq - a.by_g(hq) * a.g) / a.rows;
     const Range4 kr = range4(a, b, rb);
     const bool live = i < a.max_q && i < kr.n;
     if (JW == 4 && !live) return;                    // the whole workgroup
@@ -900,35 +1194,41 @@ __global__ __launch_bounds__(256) void attend4_join_kernel(const Attend4Args a)
     if (a.lse && lane == 0) a.lse[row] = none ? -INFINITY : (mm + __builtin_amdgcn_logf(tot)) * ATT_LN2;
 }
 
-constexpr int ROWS4_NW = 4;     // waves of a rows workgroup
-
 int64_t plan_attend4(Attend4Args &a)
 {
-    int lg = 0;                // key / page by one multiplication, as in plan_attend
-    while ((int64_t(1) << lg) < a.page) ++lg;
-    a.page_mul = (uint32_t)((uint64_t(1) << (31 + lg)) / (uint64_t)a.page + 1);
-    a.page_sh = 31 + lg;
+    Divisor by_page;
+    by_page.set(a.page);
+    a.page_mul = by_page.mul, a.page_sh = by_page.sh;
 
     const int64_t rows = (int64_t)a.max_q * a.g;
     const bool tiles = rows > 32;
     a.rows = tiles ? 32 * tiles4_waves(a.D) : rows <= 16 || a.D > 128 ? 16 : 32;
     a.rblocks = (int)((rows + a.rows - 1) / a.rows);
-    a.unit = tiles ? tiles4_keys(a.D) : 16;
+    a.lg_unit = !tiles ? 4 : tiles4_keys(a.D) == 64 ? 6 : 5;
     int64_t span = a.max_kv;
     if (a.window > 0)
-        span = std::min(span, (int64_t)a.window + (a.rows + a.g - 1) / a.g + (std::min<int64_t>(a.sinks, a.max_kv) + a.unit - 1) / a.unit * a.unit);
+        span = std::min(span, (int64_t)a.window + (a.rows + a.g - 1) / a.g + (((std::min(a.sinks, a.max_kv) - 1) >> a.lg_unit) + 1 << a.lg_unit));
     span += 15;
-    const int64_t groups = (int64_t)a.B * a.Hkv * a.rblocks;
+    const int64_t heads = (int64_t)a.B * a.Hkv, groups = heads * a.rblocks;
+    if (heads < (int64_t(1) << 31)) a.by_groups.set(heads);        // (more are refused)
+    a.by_Hkv.set(a.Hkv);
+    a.by_rblocks.set(a.rblocks);
+    a.by_g.set(a.g);
     int64_t splits, unit;
     if (tiles) {
         unit = 128;
         splits = std::max(std::min(256 / groups, span / 320), std::min((512 + groups - 1) / groups, span / 2048));
     } else {
-        unit = 32 * ROWS4_NW;
+        // The GPU holds 1024 workgroups at once; with at least 64 KB of codes and scales each, or 16 KB
+        // where there are few (4 sequences of up to 131071 keys, 8 heads, us: 100 in 24 shares, 100 in 32, 104
+        // in 64; one of 4000: 18.8 in 4, 13.8 in 16, 12.5 in 32).  Many sequences are hardly ever alike in
+        // length: shares of 160 KB let the GPU even them out (64 of up to 8192: 68 in 4, 83 in 2; D 64: 55 in 3, 69 in 2).  One
+        // launch without a join is enough where the keys are few.
+        unit = 32 * rows4_waves(a.D);
         const int64_t bytes = (span - 15) * (a.D + 8 * (a.D >> a.lg_G)), kb = 1024;
-        splits = std::max(std::min(256 / groups, (bytes + 32 * kb - 1) / (32 * kb)),
-                          std::max<int64_t>(1, std::min((768 + groups - 1) / groups, (bytes + 64 * kb - 1) / (64 * kb))));
-        splits *= (std::max<int64_t>(1, bytes / splits) + 1152 * kb - 1) / (1152 * kb);
+        splits = std::max(std::min(256 / groups, (bytes + 16 * kb - 1) / (16 * kb)),
+                          std::max<int64_t>(1, std::min((1024 + groups - 1) / groups, (bytes + 64 * kb - 1) / (64 * kb))));
+        if (groups >= 128) splits = std::max(splits, std::min((2048 + groups - 1) / groups, bytes / (160 * kb)));
         if (bytes <= std::max<int64_t>(112, std::min<int64_t>(512, 2 * groups)) * kb) splits = 1;
     }
     splits = std::max<int64_t>(1, splits);
@@ -955,25 +1255,35 @@ static hipError_t tiles4_go(const Attend4Args &a, hipStream_t st)
     return hipGetLastError();
 }
 
-template <typename S, int DP, bool P16, int QT>
+template <typename S, int DP, int GM, bool P16, int QT>
 static hipError_t rows4_go(const Attend4Args &a, hipStream_t st)
 {
-    constexpr int NW = ROWS4_NW;
+    constexpr int NW = rows4_waves(DP);
     const int nrow = (int)std::min<int64_t>(16 * QT, (int64_t)a.max_q * a.g);
-    const size_t lds = (size_t)NW * nrow * (DP + 6) * 4;
-    const hipError_t e = allow_lds(&attend4_rows_kernel<S, DP, P16, QT, NW>, lds);
+    const size_t lds = std::max<size_t>((size_t)NW * nrow * (DP + 6) * 4, NW * rows4_ring(DP, GM, P16));   // join, ring
+    const hipError_t e = allow_lds(&attend4_rows_kernel<S, DP, GM, P16, QT>, lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((attend4_rows_kernel<S, DP, P16, QT, NW>), dim3((unsigned)((int64_t)a.B * a.rblocks * a.Hkv * a.splits)), dim3(64 * NW), lds, st, a);
+    hipLaunchKernelGGL((attend4_rows_kernel<S, DP, GM, P16, QT>), dim3((unsigned)((int64_t)a.B * a.rblocks * a.Hkv * a.splits)), dim3(64 * NW), lds, st, a);
     return hipGetLastError();
 }
 
-template <typename S, int DP, bool P16>
+template <typename S, int DP, int GM, bool P16>
 static hipError_t rows4_pick(const Attend4Args &a, hipStream_t st)
 {
     if constexpr (DP <= 128) {
-        if (a.rows == 32) return rows4_go<S, DP, P16, 2>(a, st);
+        if (a.rows == 32) return rows4_go<S, DP, GM, P16, 2>(a, st);
     }
-    return rows4_go<S, DP, P16, 1>(a, st);
+    return rows4_go<S, DP, GM, P16, 1>(a, st);
+}
+// Groups that leave the codes as they are where they pay: of 64 in rows of 64, of 128 in rows of 128 and
+// 256 (64 users of up to 8192 keys, us: D 64, G 64: 56, as (c - z) s 64; D 128, G 128: 68 and 80).  Groups of 64
+// in rows of 128 take the registers of a wave and gain nothing (81 and 80).
+template <typename S, int DP, bool P16>
+static hipError_t rows4_by_group(const Attend4Args &a, hipStream_t st)
+{
+    constexpr int GM = DP == 64 ? 64 : 128;
+    if (a.D == DP && (1 << a.lg_G) == GM) return rows4_pick<S, DP, GM, P16>(a, st);
+    return rows4_pick<S, DP, 32, P16>(a, st);
 }
 
 // A wave a row where the splits are few, the workgroup's four where a single wave would
@@ -1002,11 +1312,11 @@ static hipError_t attend4_type(const Attend4Args &a, hipStream_t st)
     if (a.rows > 32)
         e = a.D <= 64 ? tiles4_go<S, 64>(a, st) : a.D <= 96 ? tiles4_go<S, 96>(a, st) : a.D <= 128 ? tiles4_go<S, 128>(a, st) : tiles4_go<S, 256>(a, st);
     else if (a.D <= 64)
-        e = a.halves ? rows4_pick<S, 64, true>(a, st) : rows4_pick<S, 64, false>(a, st);
+        e = a.halves ? rows4_by_group<S, 64, true>(a, st) : rows4_by_group<S, 64, false>(a, st);
     else if (a.D <= 128)
-        e = a.halves ? rows4_pick<S, 128, true>(a, st) : rows4_pick<S, 128, false>(a, st);
+        e = a.halves ? rows4_by_group<S, 128, true>(a, st) : rows4_by_group<S, 128, false>(a, st);
     else
-        e = a.halves ? rows4_pick<S, 256, true>(a, st) : rows4_pick<S, 256, false>(a, st);
+        e = a.halves ? rows4_by_group<S, 256, true>(a, st) : rows4_by_group<S, 256, false>(a, st);
     if (e != hipSuccess || a.splits == 1) return e;
     if (a.D <= 64) return join4_go<S, 64>(a, st);
     if (a.D <= 128) return join4_go<S, 128>(a, st);
@@ -1018,7 +1328,7 @@ static hipError_t attend4_type(const Attend4Args &a, hipStream_t st)
 static bool attend4_fits(const Attend4Args &a)
 {
     const int64_t most = (int64_t(1) << 32) - 1, groups = (int64_t)a.B * a.Hkv;
-    const int64_t threads = 64 * (a.rows > 32 ? tiles4_waves(a.D) : ROWS4_NW);
+    const int64_t threads = 64 * (a.rows > 32 ? tiles4_waves(a.D) : rows4_waves(a.D));
     if (groups > most || a.rblocks * groups > most / threads / a.splits) return false;
     return a.splits == 1 || join4_blocks(a) <= most / 256 / a.B;
 }

@@ -114,6 +114,20 @@ struct Read4Args {
     int T, Hkv, D, G, page, pages;
 };
 
+// Division of 0 <= x < 2^31 by d > 0 with one product: with l = ceil(log2 d), mul = floor(2^(31+l) / d) + 1
+// is exact (mul d - 2^(31+l) <= d <= 2^l).
+struct Divisor {
+    uint32_t mul;
+    int sh, d;
+    void set(int64_t by)
+    {
+        int l = 0;
+        while ((int64_t(1) << l) < by) ++l;
+        mul = (uint32_t)((uint64_t(1) << (31 + l)) / (uint64_t)by + 1), sh = 31 + l, d = (int)by;
+    }
+    __host__ __device__ int operator()(int x) const { return (int)(((uint64_t)(uint32_t)x * mul) >> sh); }
+};
+
 // Attention over a cache of 4-bit codes (qmm_kv4_attention).  Strides in bytes; a token's scales
 // stand behind the last one's.
 struct Attend4Args {
@@ -127,11 +141,12 @@ struct Attend4Args {
     int64_t q_ts, q_hs, o_ts, o_hs, k_ps, k_hs, v_ps, v_hs, ks_ps, ks_hs, vs_ps, vs_hs, table_s;
     uint32_t k_ts, v_ts, s_ts;
     int B, T, Hq, Hkv, g, D, lg_G, page, width, pages, max_q, max_kv, window, sinks;
-    uint32_t page_mul;      // key / page = key * page_mul >> page_sh (set by the planner)
+    uint32_t page_mul;      // key / page = key * page_mul >> page_sh (from here on set by the planner)
     int page_sh;
     int rows;               // query rows (token, head of the group) a workgroup takes
     int rblocks, splits, chunk;
-    int unit;               // the first tokens that stay visible take a multiple of this many places
+    int lg_unit;            // the first tokens that stay visible take a multiple of 2^lg_unit places
+    Divisor by_groups, by_Hkv, by_rblocks, by_g;   // B * Hkv, Hkv, rblocks, g
     float scale;
     bool halves;            // 16 tokens in a row lie in one page, their scales at a multiple of 16 bytes
 };
