@@ -480,7 +480,8 @@ qmm_status qmm_kv4_read(const qmm_kv4_read_args *p, qmm_stream stream)
     a.kc_ps = c.k_stride[0], a.kc_hs = c.k_stride[1], a.kc_ts = c.k_stride[2], a.vc_ps = c.v_stride[0], a.vc_hs = c.v_stride[1], a.vc_ts = c.v_stride[2];
     a.ks_ps = c.k_scale_stride[0], a.ks_hs = c.k_scale_stride[1], a.vs_ps = c.v_scale_stride[0], a.vs_hs = c.v_scale_stride[1];
     a.ko_ts = p->k_out_stride[0], a.ko_hs = p->k_out_stride[1], a.vo_ts = p->v_out_stride[0], a.vo_hs = p->v_out_stride[1];
-    a.T = (int)p->T, a.Hkv = (int)c.Hkv, a.D = (int)c.D, a.G = (int)c.G, a.page = (int)c.page, a.pages = (int)c.pages;
+    a.T = (int)p->T, a.Hkv = (int)c.Hkv, a.D = (int)c.D, a.lg_G = c.G == 32 ? 5 : c.G == 64 ? 6 : 7, a.page = (int)c.page, a.pages = (int)c.pages;
+    a.by_page.set(c.page);
     return hip_status(qmm::launch_read4(a, p->dtype == QMM_BF16, even_rows({{p->k_out, p->k_out_stride}, {p->v_out, p->v_out_stride}}), (hipStream_t)stream), fn);
 }
 

@@ -85,6 +85,20 @@ struct AttendArgs {
     float scale;
 };
 
+// Division of 0 <= x < 2^31 by d > 0 with one product: with l = ceil(log2 d), mul = floor(2^(31+l) / d) + 1
+// is exact (mul d - 2^(31+l) <= d <= 2^l).
+struct Divisor {
+    uint32_t mul;
+    int sh, d;
+    void set(int64_t by)
+    {
+        int l = 0;
+        while ((int64_t(1) << l) < by) ++l;
+        mul = (uint32_t)((uint64_t(1) << (31 + l)) / (uint64_t)by + 1), sh = 31 + l, d = (int)by;
+    }
+    __host__ __device__ int operator()(int x) const { return (int)(((uint64_t)(uint32_t)x * mul) >> sh); }
+};
+
 // Norms of q and k with their positions (qmm_qk_norm: k to k_out) and the append to a cache
 // of 4-bit codes (qmm_kv4_append: k and v to the codes).  Strides in elements, of codes in bytes.
 struct HeadsArgs {
@@ -99,7 +113,8 @@ struct HeadsArgs {
     int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, qo_ts, qo_hs, ko_ts, ko_hs;
     int64_t kc_ps, kc_hs, kc_ts, vc_ps, vc_hs, vc_ts, ks_ps, ks_hs, vs_ps, vs_hs;
     int T, Hq, Hk, Hkv, D, G, rot, page, pages, table_rows;   // Hk: heads of k that go to k_out
-    int turn_blocks;                      // workgroups that turn rows (set by the launcher)
+    int put_blocks;                       // workgroups that store k and v; one in by_period.d is one (set by the launcher)
+    Divisor by_period, by_page, by_G;
     float eps;
     bool pairs;
 };
@@ -111,21 +126,8 @@ struct Read4Args {
     const int64_t *slots;
     void *k_out, *v_out;
     int64_t kc_ps, kc_hs, kc_ts, vc_ps, vc_hs, vc_ts, ks_ps, ks_hs, vs_ps, vs_hs, ko_ts, ko_hs, vo_ts, vo_hs;
-    int T, Hkv, D, G, page, pages;
-};
-
-// Division of 0 <= x < 2^31 by d > 0 with one product: with l = ceil(log2 d), mul = floor(2^(31+l) / d) + 1
-// is exact (mul d - 2^(31+l) <= d <= 2^l).
-struct Divisor {
-    uint32_t mul;
-    int sh, d;
-    void set(int64_t by)
-    {
-        int l = 0;
-        while ((int64_t(1) << l) < by) ++l;
-        mul = (uint32_t)((uint64_t(1) << (31 + l)) / (uint64_t)by + 1), sh = 31 + l, d = (int)by;
-    }
-    __host__ __device__ int operator()(int x) const { return (int)(((uint64_t)(uint32_t)x * mul) >> sh); }
+    int T, Hkv, D, lg_G, page, pages;
+    Divisor by_page;
 };
 
 // Attention over a cache of 4-bit codes (qmm_kv4_attention).  Strides in bytes; a token's scales
