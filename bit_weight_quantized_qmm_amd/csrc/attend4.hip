@@ -1216,8 +1216,22 @@ int64_t plan_attend4(Attend4Args &a)
     a.by_g.set(a.g);
     int64_t splits, unit;
     if (tiles) {
+        // One workgroup a CU, 256 at once: what counts is in how many rounds the blocks of rows go, and what
+        // shares of their keys cost, fp32 sums for each output written and read.  A share takes about
+        // (12 + D / 5) ns a key and 5 us; of the shares that fill r rounds the largest number is the
+        // quickest.  (us: 3 x up to 600 tokens, 8 heads of 4, a window of 4096: 159 whole, 191 in two
+        // shares; one chunk of 600 on 32768 keys: 1035 whole, 379 in three, 562 in four; 50 tokens on
+        // 48752 keys, one head of 2: 25 in 152, 70 in 19; 15 x 124 tokens on up to 3078 keys, 4 heads: 79
+        // whole, 40 in four; 4 x 512 on 2048: 77 and 128 in two.)
         unit = 128;
-        splits = std::max(std::min(256 / groups, span / 320), std::min((512 + groups - 1) / groups, span / 2048));
+        const int64_t live = std::min(groups, a.Hkv * (((int64_t)a.T * a.g + a.rows - 1) / a.rows + a.B / 2));     // blocks with rows
+        const double key = (12.0 + a.D / 5.0) * 1e-3, share = 8.0 * a.T * a.Hq * (a.D + 1) / 4.5e6;
+        auto cost = [&](int64_t s) { return (double)((live * s + 255) / 256) * ((double)span / s * key + 5.0) + (s > 1 ? 5.0 + share * s : 0.0); };
+        splits = 1;
+        for (int64_t round = 1; round <= 4; ++round) {
+            const int64_t s = std::min(256 * round / std::max<int64_t>(1, live), span / unit);
+            if (s > 1 && cost(s) < cost(splits)) splits = s;
+        }
     } else {
         // The GPU holds 1024 workgroups at once; with at least 64 KB of codes and scales each, or 16 KB
         // where there are few (4 sequences of up to 131071 keys, 8 heads, us: 100 in 24 shares, 100 in 32, 104
