@@ -82,39 +82,44 @@ __device__ __forceinline__ int4_t code_order(int4_t q)
     }
     return r;
 }
-__device__ __forceinline__ float largest(int4_t q, f16_t)
+// The largest of the sizes of a dword's two elements and of `so_far`'s, as they stand (f16 and bf16 order
+// like whole numbers); a half of that as a number.
+typedef uint16_t ushort2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t larger2(uint32_t so_far, int4_t q)
 {
-    uint32_t m = 0;
+    ushort2_t m = __builtin_bit_cast(ushort2_t, so_far);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) m = max(m, max((uint32_t)q[i] & 0x7fffu, (uint32_t)q[i] >> 16 & 0x7fffu));
-    return (float)as_half((uint16_t)m);
+    for (int i = 0; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(ushort2_t, (uint32_t)q[i] & 0x7fff7fffu));
+    return __builtin_bit_cast(uint32_t, m);
 }
-__device__ __forceinline__ float largest(int4_t q, bf16_t)
+__device__ __forceinline__ float size_of(uint32_t bits, f16_t) { return (float)as_half((uint16_t)bits); }
+__device__ __forceinline__ float size_of(uint32_t bits, bf16_t) { return __builtin_bit_cast(float, bits << 16); }
+// N steps of a row in codes' order as f16 times 2^up; PART: the elements whose codes stand higher by 16 less
+template <bool PART, int N>
+__device__ __forceinline__ void scale_row(int4_t (&q)[N], int up, f16_t)
 {
-    uint32_t m = 0;
+    int low = up, high = PART ? up - 4 : up;
+    do {                                    // 2^15 at a time: once but for rows below 1
+        const f16_t fl = (f16_t)ldexpf(1.f, min(low, 15)), fh = (f16_t)ldexpf(1.f, min(high, 15));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) m = max(m, max((uint32_t)q[i] << 16 & 0x7fffffffu, (uint32_t)q[i] & 0x7fff0000u));
-    return __builtin_bit_cast(float, m);
+        for (int j = 0; j < N; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) q[j][i] = (int)as_u32(as_half2((uint32_t)q[j][i]) * (i & 1 ? half2_t{fh, fh} : half2_t{fl, fl}));
+        low = max(low - 15, 0);
+        high = max(high - 15, 0);
+    } while (__any(low > 0));
 }
-__device__ __forceinline__ int4_t to_f16(int4_t q, int up, f16_t)     // times 2^up
+template <bool PART, int N>
+__device__ __forceinline__ void scale_row(int4_t (&q)[N], int up, bf16_t)
 {
-    int4_t r;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const half2_t x = as_half2((uint32_t)q[i]);
-        r[i] = pack2(ldexpf((float)x[0], up), ldexpf((float)x[1], up), f16_t());
-    }
-    return r;
-}
-__device__ __forceinline__ int4_t to_f16(int4_t q, int up, bf16_t)
-{
-    int4_t r;
+    for (int j = 0; j < N; ++j)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float x = __builtin_bit_cast(float, (uint32_t)q[i] << 16), y = __builtin_bit_cast(float, (uint32_t)q[i] & 0xffff0000u);
-        r[i] = pack2(ldexpf(x, up), ldexpf(y, up), f16_t());
-    }
-    return r;
+        for (int i = 0; i < 4; ++i) {
+            const int by = PART && (i & 1) ? up - 4 : up;
+            const float x = __builtin_bit_cast(float, (uint32_t)q[j][i] << 16), y = __builtin_bit_cast(float, (uint32_t)q[j][i] & 0xffff0000u);
+            q[j][i] = pack2(ldexpf(x, by), ldexpf(y, by), f16_t());
+        }
 }
 // the power that brings a row whose largest is m below 2^15
 __device__ __forceinline__ int rise_of(float m)
@@ -422,38 +427,32 @@ __global__ __launch_bounds__(64 * rows4_waves(DP)) __attribute__((amdgpu_waves_p
         vhi[qt] = live ? kr.L - kr.n + i + 1 : 0;
         vlo[qt] = a.window > 0 ? vhi[qt] - a.window : 0;
         const char *row = (const char *)a.q + (int64_t)(kr.t0 + (live ? i : 0)) * a.q_ts + (int64_t)(live ? hq : 0) * a.q_hs;
-        float top = 0.f;
+        uint32_t bits = 0;
 #pragma unroll
         for (int j = 0; j < KJ; ++j) {
             const int d = 32 * KW * (j / KW) + 8 * KW * g + 8 * (j % KW);
             q[qt][j] = *reinterpret_cast<const int4_t *>(row + (d < a.D ? 2 * d : 0));
             if (!live || d >= a.D) q[qt][j] = int4_t{0, 0, 0, 0};
-            top = fmaxf(top, largest(q[qt][j], tag));
+            bits = larger2(bits, q[qt][j]);
         }
         sl[qt] = a.scale * ATT_LOG2E;
+#pragma unroll
+        for (int j = 0; j < KJ; ++j) q[qt][j] = code_order(q[qt][j]);
         if constexpr (DEFER || !__is_same(S, f16_t)) {
+            float top = size_of(max(bits & 0xffffu, bits >> 16), tag);
             top = fmaxf(top, __shfl_xor(top, 16));
             top = fmaxf(top, __shfl_xor(top, 32));
             const int up = rise_of(top);
-#pragma unroll
-            for (int j = 0; j < KJ; ++j) q[qt][j] = to_f16(q[qt][j], up, tag);
+            scale_row<DEFER, KJ>(q[qt], up, tag);
             sl[qt] = fminf(ldexpf(sl[qt], (DEFER ? 22 : 0) - up), 3e38f);
         }
         sl[qt] = above_zero(sl[qt]);
-#pragma unroll
-        for (int j = 0; j < KJ; ++j) q[qt][j] = code_order(q[qt][j]);
         if constexpr (DEFER) {
 #pragma unroll
             for (int ns = 0; ns < NS; ++ns) {
                 float4_t sum = float4_t{0.f, 0.f, 0.f, 0.f};      // of a key whose codes are all 1
 #pragma unroll
-                for (int w = 0; w < KW; ++w) {
-                    int4_t &x = q[qt][KW * ns + w];
-                    const half2_t part = half2_t{(f16_t)0.0625f, (f16_t)0.0625f};
-                    x[1] = (int)as_u32(as_half2((uint32_t)x[1]) * part);
-                    x[3] = (int)as_u32(as_half2((uint32_t)x[3]) * part);
-                    sum = mfma_16(places4(0x11111111u), x, sum, f16_t());
-                }
+                for (int w = 0; w < KW; ++w) sum = mfma_16(places4(0x11111111u), q[qt][KW * ns + w], sum, f16_t());
                 qsum[qt][ns] = sum[0];
             }
         }
@@ -615,21 +614,30 @@ __global__ __launch_bounds__(64 * rows4_waves(DP)) __attribute__((amdgpu_waves_p
         if (masked) {
             // (the comparisons stay in here)
             asm volatile("" : "+s"(key0[0]), "+s"(key0[1]));
+            auto below = [](int n) { return (1 << min(max(n, 0), 4)) - 1; };       // bits of this lane's keys before the n-th
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < 2; ++t) {
+                const int key = key0[t] + 4 * g;
+                const int dead4 = P16 ? (gone[0] >> t & 1 ? 15 : 0) : (int)(gone[0] >> (16 * t + 4 * g)) & 15;
+                const int open = below(end - v0 - 16 * t - 4 * g) & ~dead4, sinks = below(a.sinks - key);
+                const int some = open & below(kr.hi - key) & (~below(kr.lo - key) | sinks);
+                int mine[QT];
+#pragma unroll
+                for (int qt = 0; qt < QT; ++qt) mine[qt] = open & below(vhi[qt] - key) & (~below(vlo[qt] - key) | sinks);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int key = key0[t] + 4 * g + i;
-                    const bool off = v0 + 16 * t + 4 * g + i >= end || (gone[0] >> (P16 ? t : 16 * t + 4 * g + i) & 1);
 #pragma unroll
-                    for (int qt = 0; qt < QT; ++qt)
-                        if (off || key >= vhi[qt] || (key < vlo[qt] && key >= a.sinks)) s[qt][t][i] = -INFINITY;
-                    // values that no row sees may hold anything: they meet p = 0 as zeros
-                    if (off || key >= kr.hi || (key < kr.lo && key >= a.sinks)) {
-#pragma unroll
-                        for (int x = 0; x < (DEFER ? NS : VC); ++x) vsd[t][i][x] = 0;
+                    for (int qt = 0; qt < QT; ++qt) {
+                        const float was = s[qt][t][i];       // (a copy: bit_cast of a vector's element takes its first)
+                        const int m = (mine[qt] << (31 - i)) >> 31;
+                        s[qt][t][i] = __builtin_bit_cast(float, (__builtin_bit_cast(int, was) & m) | ((int)0xff800000u & ~m));
                     }
+                    // values that no row sees may hold anything: they meet p = 0 as zeros
+                    const uint32_t m = (uint32_t)((some << (31 - i)) >> 31);
+#pragma unroll
+                    for (int x = 0; x < (DEFER ? NS : VC); ++x) vsd[t][i][x] &= m;
                 }
+            }
         }
         gone[0] = gone[1];
         gone[1] = gone[2];
@@ -882,23 +890,23 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DC <= 1
     float sl = a.scale * ATT_LOG2E;
     {
         const char *row = (const char *)a.q + (int64_t)(kr.t0 + (live ? i : 0)) * a.q_ts + (int64_t)(live ? hq : 0) * a.q_hs;
-        float top = 0.f;
+        uint32_t bits = 0;
 #pragma unroll
         for (int j = 0; j < QJ; ++j) {
             const int d = 16 * j + 8 * h;
             q[j] = *reinterpret_cast<const int4_t *>(row + (d < a.D ? 2 * d : 0));
             if (!live || d >= a.D) q[j] = int4_t{0, 0, 0, 0};
-            if constexpr (!__is_same(S, f16_t)) top = fmaxf(top, largest(q[j], tag));
+            if constexpr (!__is_same(S, f16_t)) bits = larger2(bits, q[j]);
         }
-        if constexpr (!__is_same(S, f16_t)) {
-            const int up = rise_of(fmaxf(top, __shfl_xor(top, 32)));
-#pragma unroll
-            for (int j = 0; j < QJ; ++j) q[j] = to_f16(q[j], up, tag);
-            sl = ldexpf(sl, -up);
-        }
-        sl = above_zero(sl);
 #pragma unroll
         for (int j = 0; j < QJ; ++j) q[j] = code_order(q[j]);
+        if constexpr (!__is_same(S, f16_t)) {
+            const float top = size_of(max(bits & 0xffffu, bits >> 16), tag);
+            const int up = rise_of(fmaxf(top, __shfl_xor(top, 32)));
+            scale_row<false, QJ>(q, up, tag);
+            sl = fminf(ldexpf(sl, -up), 3e38f);
+        }
+        sl = above_zero(sl);
     }
     // keys that some row of the wave sees, and keys that all of them see
     const int wr0 = rb * a.rows + 32 * wave, wr1 = min(wr0 + 31, rb * a.rows + nrow - 1);
