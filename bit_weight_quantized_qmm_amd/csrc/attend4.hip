@@ -653,6 +653,7 @@ __global__ __launch_bounds__(64 * rows4_waves(DP)) __attribute__((amdgpu_waves_p
 #pragma unroll
                 for (int qt = 0; qt < QT; ++qt) {
                     m[qt] += to - rise;
+                    if (n == 0) continue;          // (nothing but zeros yet)
                     l[qt] *= f;
 #pragma unroll
                     for (int x = 0; x < XT; ++x) o[qt][x] *= f;
@@ -676,14 +677,16 @@ __global__ __launch_bounds__(64 * rows4_waves(DP)) __attribute__((amdgpu_waves_p
                 mx = fmaxf(mx, __shfl_xor(mx, 16));
                 mx = fmaxf(mx, __shfl_xor(mx, 32));
                 const float mn = fmaxf(m[qt], mx), al = __builtin_amdgcn_exp2f(m[qt] - (mn == -INFINITY ? 0.f : mn));
-                l[qt] *= al;
-#pragma unroll
-                for (int xx = 0; xx < XT; ++xx) o[qt][xx] *= al;
-                if constexpr (DEFER) {
-#pragma unroll
-                    for (int xx = 0; xx < NS; ++xx) oz[qt][xx] *= al;
-                }
                 m[qt] = mn;
+                if (n > 0) {
+                    l[qt] *= al;
+#pragma unroll
+                    for (int xx = 0; xx < XT; ++xx) o[qt][xx] *= al;
+                    if constexpr (DEFER) {
+#pragma unroll
+                        for (int xx = 0; xx < NS; ++xx) oz[qt][xx] *= al;
+                    }
+                }
             }
             const float base = (m[qt] == -INFINITY ? 0.f : m[qt]) - TOP;
             float sum = 0.f;
@@ -1157,17 +1160,35 @@ __global__ __launch_bounds__(256) void attend4_join_kernel(const Attend4Args a)
     const int splits = live ? max(1, (kr.len + a.chunk - 1) / a.chunk) : 0;
     const int64_t row = live ? (int64_t)(kr.t0 + i) * a.Hq + hq : 0;
     const float *lses = a.part + (int64_t)a.T * a.Hq * a.splits * a.D + row * a.splits;
+    const int d = 4 * (lane % LN);
+    const float *part = a.part + row * a.splits * a.D + (d < a.D ? d : 0);
+    // the first four of a lane's splits are on their way before the maximum is known
+    constexpr int AHEAD = 4, STEP = JW * SW;
+    const int s0 = part_wave * SW + lane / LN;
+    float4_t o[AHEAD];
+    float lse[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+        const int s = max(0, min(s0 + k * STEP, splits - 1));
+        lse[k] = lses[s];
+        o[k] = *reinterpret_cast<const float4_t *>(part + (int64_t)s * a.D);
+    }
     float mm = -INFINITY;
     for (int s = lane; s < splits; s += 64) mm = fmaxf(mm, lses[s]);
 #pragma unroll
     for (int x = 1; x < 64; x <<= 1) mm = fmaxf(mm, __shfl_xor(mm, x));
     const float ms = mm == -INFINITY ? 0.f : mm;
-    const int d = 4 * (lane % LN);
-    const float *part = a.part + row * a.splits * a.D + (d < a.D ? d : 0);
     float4_t sum = float4_t{0.f, 0.f, 0.f, 0.f};
     float tot = 0.f;
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+        if (s0 + k * STEP < splits) {
+            const float f = __builtin_amdgcn_exp2f(lse[k] - ms);
+            tot += f;
+            sum += f * o[k];
+        }
 #pragma unroll 4
-    for (int s = part_wave * SW + lane / LN; s < splits; s += JW * SW) {
+    for (int s = s0 + AHEAD * STEP; s < splits; s += STEP) {
         const float f = __builtin_amdgcn_exp2f(lses[s] - ms);
         tot += f;
         sum += f * *reinterpret_cast<const float4_t *>(part + (int64_t)s * a.D);
