@@ -319,11 +319,11 @@ __global__ __launch_bounds__(64 * rows4_waves(DP)) __attribute__((amdgpu_waves_p
     auto is_page = [&](int pid) { return (uint32_t)pid < (uint32_t)a.pages; };
 
     // ---- the lookups ----
-    // P16: lane l, half l % 2 of this wave's block number 32 n + l / 2; else lane l, place l % 32 of block n,
-    // whose page ids stand in LDS for ROWS4_IDS blocks.  A place past the end or on a bad page is token
+    // P16: lane l, half l % 2 of this wave's block number 32 n + l / 2; else lane l, place l % 32 of block
+    // 2 n + l / 32, the page ids in LDS for ROWS4_IDS blocks.  A place past the end or on a bad page is token
     // 0 of page 0: in bounds, and hidden.
     auto place_of = [&](int n) {
-        return P16 ? begin + 32 * (wave + NW * (32 * n + (lane >> 1))) + 16 * (lane & 1) : begin + 32 * (wave + NW * n) + (lane & 31);
+        return P16 ? begin + 32 * (wave + NW * (32 * n + (lane >> 1))) + 16 * (lane & 1) : begin + 32 * (wave + NW * (2 * n + (lane >> 5))) + (lane & 31);
     };
     auto key_of = [&](int v) { return key_at(kr, max(0, min(v, end - 1))); };
     int64_t ko = 0, vo = 0, kso = 0, vso = 0;
@@ -339,10 +339,10 @@ __global__ __launch_bounds__(64 * rows4_waves(DP)) __attribute__((amdgpu_waves_p
         dead = __ballot(!ok);
     };
     int32_t *ids = reinterpret_cast<int32_t *>(ring + 2 * BLOCK);
-    auto hold_ids = [&](int n) {                // of blocks n .. n + ROWS4_IDS - 1
+    auto hold_ids = [&](int n) {                // of blocks n .. n + ROWS4_IDS - 1, n even
         int32_t x[ROWS4_IDS / 2];
 #pragma unroll
-        for (int i = 0; i < ROWS4_IDS / 2; ++i) x[i] = table[key_page(a, key_of(place_of(n + 2 * i + (lane >> 5))))];
+        for (int i = 0; i < ROWS4_IDS / 2; ++i) x[i] = table[key_page(a, key_of(place_of(n / 2 + i)))];
 #pragma unroll
         for (int i = 0; i < ROWS4_IDS / 2; ++i) ids[64 * i + lane] = x[i];
     };
@@ -377,11 +377,11 @@ __global__ __launch_bounds__(64 * rows4_waves(DP)) __attribute__((amdgpu_waves_p
             } else {
 #pragma unroll
                 for (int f = 0; f < CF; ++f) {
-                    const uint8_t *p = base + sent(off, 16 * t + key[f]) + part[f];
+                    const uint8_t *p = base + sent(off, 32 * (n & 1) + 16 * t + key[f]) + part[f];
                     if (CH >= 4 || lane < 16 * CH) fetch<16>(to + t * HALF + 1024 * f, p);
                 }
 #pragma unroll
-                for (int f = 0; f < SF; ++f) fetch<4>(sto + t * SHALF + 256 * f, sbase + sent(soff, 16 * t + stok[f]) + spart[f]);
+                for (int f = 0; f < SF; ++f) fetch<4>(sto + t * SHALF + 256 * f, sbase + sent(soff, 32 * (n & 1) + 16 * t + stok[f]) + spart[f]);
             }
         }
     };
@@ -406,9 +406,9 @@ __global__ __launch_bounds__(64 * rows4_waves(DP)) __attribute__((amdgpu_waves_p
             fetch_v(1);
         } else {
             hold_ids(0);
+            look_up(0, ids[lane]);
             for (int n = 0; n < 2; ++n) {
-                look_up(n, ids[32 * n + (lane & 31)]);
-                gone[n] = dead;
+                gone[n] = dead >> (32 * n) & 0xffffffffu;
                 fetch_k(n);
                 fetch_v(n);
             }
@@ -519,8 +519,8 @@ __global__ __launch_bounds__(64 * rows4_waves(DP)) __attribute__((amdgpu_waves_p
             gone[2] = dead >> (2 * ((n + 2) & 31)) & 3;
         } else {
             if ((n + 2) % ROWS4_IDS == 0) hold_ids(n + 2);
-            look_up(n + 2, ids[32 * ((n + 2) % ROWS4_IDS) + (lane & 31)]);
-            gone[2] = dead;
+            if (n % 2 == 0) look_up((n + 2) / 2, ids[32 * ((n + 2) % ROWS4_IDS) + lane]);
+            gone[2] = dead >> (32 * (n & 1)) & 0xffffffffu;
         }
         wait_reads();
         fetch_k(n + 2);
