@@ -218,6 +218,7 @@ template <typename S> struct Row4 {
     S own[8], other[8];         // this lane's elements; those that turn with them (halves)
     S w_own[8], w_other[8];
     float cs[8], sn[8];         // pairs: four of each
+    float turn;                 // the largest of them, at least 1
     bool norm, turns, pairs, low;
 };
 
@@ -235,11 +236,13 @@ __device__ __forceinline__ float round_lanes(float x, int span, F f)
 }
 
 // The row's elements after norm and rotation in fp32.  Returns a bound of what its roundings move any of
-// this lane's 8 by: a dozen of 2^-24, and half of the sum of squares' D 2^-24.
+// this lane's 8 by: a dozen of 2^-24, and half of the sum of squares' D 2^-24; infinity where that sum
+// leaves fp32's range.
 template <int LN, typename S>
 __device__ __forceinline__ float turned8(const HeadsArgs &a, const Row4<S> &r, float (&x)[8])
 {
     float root = 1.f, size = 0.f, y[8];
+    bool in_range = true;
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = to_f32(r.own[i]);
     if (r.norm) {
@@ -247,7 +250,9 @@ __device__ __forceinline__ float turned8(const HeadsArgs &a, const Row4<S> &r, f
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum = fmaf(x[i], x[i], sum);
         sum = round_lanes(sum, LN, [](float p, float q) { return p + q; });
-        root = 1.f / sqrtf(sum / (float)a.D + a.eps);
+        const float mean = sum / (float)a.D + a.eps;
+        in_range = mean > 0x1p-100f && mean < 0x1p112f;
+        root = 1.f / sqrtf(mean);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {        // (products of two 16-bit numbers are exact)
             x[i] *= to_f32(r.w_own[i]);
@@ -278,7 +283,7 @@ __device__ __forceinline__ float turned8(const HeadsArgs &a, const Row4<S> &r, f
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] *= root;
     }
-    return 0x1p-20f * size * root;
+    return in_range ? 0x1p-20f * size * root * r.turn : INFINITY;
 }
 // The same in fp64.
 template <int LN, typename S>
@@ -389,6 +394,7 @@ __device__ __forceinline__ void put_rows(const HeadsArgs &a, int block, int h0)
     r.turns = d < a.rot;
     r.pairs = PAIRS;
     r.low = d < a.rot / 2;
+    r.turn = 1.f;
     const int other = PAIRS || !r.turns ? from : r.low ? d + a.rot / 2 : d - a.rot / 2;
     const int pos = a.rot > 0 ? min(max(a.positions[t], 0), a.table_rows - 1) : 0;
     S k[HP][8], k_other[HP][8], v[HP][8];
@@ -412,6 +418,8 @@ __device__ __forceinline__ void put_rows(const HeadsArgs &a, int block, int h0)
             load_line<4>(line + 4, reinterpret_cast<float(&)[4]>(r.cs[4]));
             load_line<4>(line + a.rot / 2 + 4, reinterpret_cast<float(&)[4]>(r.sn[4]));
         }
+#pragma unroll
+        for (int i = 0; i < (PAIRS ? 4 : 8); ++i) r.turn = fmaxf(r.turn, fmaxf(fabsf(r.cs[i]), fabsf(r.sn[i])));
     }
 
     const int span = a.G / 8;
@@ -445,6 +453,9 @@ __device__ __forceinline__ void put_rows(const HeadsArgs &a, int block, int h0)
             if (side == 0 && __any(!sure)) {
                 double y[8];
                 turned8<LN>(a, r, y);
+                nan = false;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) nan = nan || y[e] != y[e];
                 map8(y, span, s, z, word);
             }
             nan = (__ballot(nan) & of_group) != 0;

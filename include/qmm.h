@@ -441,7 +441,8 @@ qmm_status qmm_qk_norm(const qmm_qk_norm_args *args, qmm_stream stream);
 
 /* A paged cache of 4-bit codes.  The D elements of a token and head are D/2 bytes,
  * element i at bits 4i of them (as in qmm_pack); each G of them have a scale s and a
- * zero-point z:  x = (code - z) s. */
+ * zero-point z:  x = (code - z) s.  What is read must have s finite and >= 0, z a whole
+ * number of 0 .. 15, |x| below 65520: qmm_kv4_append writes nothing else but for NaN. */
 typedef struct qmm_kv4_cache {
     uint8_t *k, *v;                    /* [pages][Hkv][page][D/2] */
     qmm_half *k_scale, *v_scale;       /* [pages][Hkv][page][D/G][2]: s and z; the last three side by side */
@@ -470,8 +471,9 @@ typedef struct qmm_kv4_append_args {
  *     s = (hi - lo) / 15 to 7 significant bits, at least 2^-18
  *     z = clamp(rint(-lo / s), 0, 15),  code = clamp(rint(x / s) + z, 0, 15)
  * to nearest, ties to even: the mapping of qmm_quantize, with a scale so short that
- * every (code - z) s is a number of fp16.  k is normed and turned in fp64 on its way,
- * so that its codes are those of the formulas; q as in qmm_qk_norm.  Elements beyond
+ * every (code - z) s is a number of fp16.  k is normed and turned in fp32, and where
+ * that leaves a doubt in fp64, so that its codes are those of the formulas; q as in
+ * qmm_qk_norm.  Elements beyond
  * +-57344 are stored as that; a group that holds NaN gets a scale of NaN.
  *   args   HOST struct, read during the call only
  * T = 0 does nothing.  A slot outside 0 .. pages * page - 1 stores nothing; two

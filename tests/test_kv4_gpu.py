@@ -3,7 +3,7 @@ qmm_kv4_attention), against their formulas in 64 bits, on an MI355X.
 
 Tolerances count roundings.  u is half a step of the output's type (2^-11 for fp16, 2^-8 for bf16); fp32
 sums of n terms are off by at most n 2^-24 of the sum of magnitudes.  Codes, scales and zero-points are
-exact: the kernel decides them in fp64 (a value within 2^-40 of a border would be another matter; none of the
+exact: what fp32 leaves in doubt the kernel decides in fp64 (a value within 2^-40 of a border would be another matter; none of the
 inputs is, exact ties apart).
 """
 import importlib.util
@@ -234,6 +234,23 @@ def test_append(q, T, Hq, Hkv, D, G, rot, page, pairs, norm, dtype):
         want, size = turned(xq, wq, 1e-5, pos, table, pairs)
         close(out, want, norm_bound(want, size, D, dtype))
         check_stored(c, before, turned(k, wk, 1e-5, pos, table, pairs)[0], v.double(), slots, G)
+
+
+@pytest.mark.parametrize("pairs", [False, True], ids=["halves", "pairs"])
+@pytest.mark.parametrize("size,eps,turn", [(1e20, 1e-5, 1), (3e37, 1e-5, 1), (1e-25, 0.0, 1), (1e-37, 0.0, 1), (1.0, 1e-5, 300), (2e-3, 0.0, 1e-3), (1e18, 1e-5, 50)])
+def test_append_keys_of_any_size(q, size, eps, turn, pairs):
+    """Squares beyond fp32's range, tables beyond 1: the codes are the formulas' all the same."""
+    g = gen(41)
+    _, k, v = heads(40, 0, 3, 128, BF16, g, size=size)
+    k[0, 0] = 0
+    v = torch.zeros_like(v)
+    w, table, pos = (1 + 0.3 * torch.randn(128, generator=g, device=DEV)).to(BF16), rope_table(100, 128) * turn, torch.arange(40, device=DEV, dtype=torch.int32)
+    c = q.kv4_cache(6, 3, 16, 128, 64)
+    before, slots = q.KV4Cache(*(t.clone() for t in c)), place(40, 6, 16, g)
+    q.kv4_append(None, k, v, c, slots, pos, table, pairs, k_norm=w, eps=eps)
+    want = turned(k, w, eps, pos, table, pairs)[0]
+    assert eps == 0 or torch.isfinite(want).all()
+    check_stored(c, before, want, v.double(), slots, 64)
 
 
 def test_append_in_place_and_keys_alone(q):
