@@ -207,7 +207,7 @@ __device__ __forceinline__ void turn_rows(const HeadsArgs &a, int block, int gro
 // heads, k and v of each, LN lanes a token's row; range and zero-point go round the G / 8
 // lanes of a group.  A workgroup's 256 / LN tokens stand side by side in a page's head.  Its
 // waves wait for memory (one row a wave: 31 us for 8192 tokens of 2 x 8 heads, k and v of two
-// heads 26), so they run between q's, which is bound by memory: 72 us for both, 54 for q.
+// heads 26; few tokens: see heads_pick), so they run between q's, which is bound by memory: 72 us for both, 54 for q.
 //
 // k is normed, turned and mapped in fp32 first, with a bound of what its roundings may have
 // moved its elements by; where that leaves a scale, a zero-point or a code in doubt
@@ -472,13 +472,12 @@ __device__ __forceinline__ void put_rows(const HeadsArgs &a, int block, int h0)
     }
 }
 
-constexpr int KP = 2;      // heads of k and v that a lane takes
-
-template <typename S, bool PAIRS, bool VEC, int U, int HP, bool STORE>
+// KP: heads of k and v that a lane takes (0: no cache)
+template <typename S, bool PAIRS, bool VEC, int U, int HP, int KP>
 __global__ __launch_bounds__(256) void heads_kernel(const HeadsArgs a)
 {
     const int groups = (a.Hq + a.Hk + HP - 1) / HP, id = (int)blockIdx.x;
-    if constexpr (!STORE) {
+    if constexpr (KP == 0) {
         turn_rows<S, PAIRS, VEC, U, HP>(a, id, groups);
     } else {
         // every by_period.d-th workgroup takes k or v: computing and moving run side by side
@@ -492,27 +491,40 @@ __global__ __launch_bounds__(256) void heads_kernel(const HeadsArgs a)
     }
 }
 
-template <typename S, bool PAIRS, bool VEC, int U, bool STORE>
+template <typename S, bool PAIRS, bool VEC, int U, int KP>
 static hipError_t heads_go(HeadsArgs a, hipStream_t st)
 {
     constexpr int HP = 2;
     const int64_t turned = ((int64_t)a.T + 256 / U - 1) / (256 / U) * ((a.Hq + a.Hk + HP - 1) / HP);
-    const int64_t put = STORE ? ((int64_t)a.T + 128 / U - 1) / (128 / U) * ((a.Hkv + KP - 1) / KP) : 0;
+    int64_t put = 0;
+    if constexpr (KP > 0) put = ((int64_t)a.T + 128 / U - 1) / (128 / U) * ((a.Hkv + KP - 1) / KP);
     if ((turned + put) * 256 >= (int64_t(1) << 32)) return hipErrorNotSupported;   // threads of a launch
     if (turned + put == 0) return hipSuccess;
-    if (STORE) {
+    if (KP > 0) {
         a.put_blocks = (int)put;
         a.by_period.set((turned + put) / put);
         a.by_page.set(a.page);
         a.by_G.set(a.G);
     }
-    hipLaunchKernelGGL((heads_kernel<S, PAIRS, VEC, U, HP, STORE>), dim3((unsigned)(turned + put)), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((heads_kernel<S, PAIRS, VEC, U, HP, KP>), dim3((unsigned)(turned + put)), dim3(256), 0, st, a);
     return hipGetLastError();
+}
+template <typename S, bool PAIRS, bool VEC, int U, bool STORE>
+static hipError_t heads_pick(const HeadsArgs &a, hipStream_t st)
+{
+    if constexpr (!STORE) {
+        return heads_go<S, PAIRS, VEC, U, 0>(a, st);
+    } else {
+        // One head a lane is soonest done where all workgroups run at once, two move more where they go in rounds
+        // (32 + 2 x 8 heads of 128, us, one and two: 1 token 4.3 and 6.1, 256: 6.1 and 8.0, 2048: 16.2 and 17.0,
+        // 4096 with 64 heads of q: 37.1 and 36.6, 8192: 67 and 64).
+        return (int64_t)a.T * a.Hkv * 2 * U <= 1024 * 256 ? heads_go<S, PAIRS, VEC, U, 1>(a, st) : heads_go<S, PAIRS, VEC, U, 2>(a, st);
+    }
 }
 template <typename S, bool PAIRS, bool VEC, bool STORE>
 static hipError_t heads_width(const HeadsArgs &a, hipStream_t st)
 {
-    return a.D <= 64 ? heads_go<S, PAIRS, VEC, 4, STORE>(a, st) : a.D <= 128 ? heads_go<S, PAIRS, VEC, 8, STORE>(a, st) : heads_go<S, PAIRS, VEC, 16, STORE>(a, st);
+    return a.D <= 64 ? heads_pick<S, PAIRS, VEC, 4, STORE>(a, st) : a.D <= 128 ? heads_pick<S, PAIRS, VEC, 8, STORE>(a, st) : heads_pick<S, PAIRS, VEC, 16, STORE>(a, st);
 }
 template <typename S, bool STORE>
 static hipError_t heads_type(const HeadsArgs &a, bool vec, hipStream_t st)
