@@ -201,7 +201,7 @@ __device__ __forceinline__ int4_t places4(uint32_t w)
 // ---------------------------------------------------------------------------
 __host__ __device__ constexpr int rows4_occupancy(int DP, int GM, bool P16, int QT)
 {
-    return DP > 128 || QT > 1 ? 2 : DP == 128 && GM == 128 && !P16 ? 3 : 4;
+    return DP > 128 || QT > 1 ? 2 : DP == 128 && (GM == 64 || (GM == 128 && !P16)) ? 3 : 4;
 }
 __host__ __device__ constexpr int rows4_waves(int DP) { return DP > 128 ? 2 : 4; }      // 64 KB of ring at most
 __host__ __device__ constexpr int rows4_groups(int DP, int GM) { return GM > 32 ? DP / GM : DP / 32; }
@@ -1318,14 +1318,17 @@ static hipError_t rows4_pick(const Attend4Args &a, hipStream_t st)
     }
     return rows4_go<S, DP, GM, P16, 1>(a, st);
 }
-// Groups that leave the codes as they are where they pay: of 64 in rows of 64, of 128 in rows of 128 and
-// 256 (64 users of up to 8192 keys, us: D 64, G 64: 56, as (c - z) s 64; D 128, G 128: 68 and 80).  Groups of 64
-// in rows of 128 take the registers of a wave and gain nothing (81 and 80).
+// Groups that leave the codes as they are where they pay: of 64 in rows of 64 and 128, of 128 in rows of 128
+// and 256 (64 users of up to 8192 keys, us, so and as (c - z) s: D 64, G 64: 52 and 59; D 128, G 128: 65 and 75; D 128, G 64: 76 and
+// 80, pages of 100 tokens 78 and 85).  Two tiles of rows with groups of 64 in rows of 128 have not the registers for it (105 and 102).
 template <typename S, int DP, bool P16>
 static hipError_t rows4_by_group(const Attend4Args &a, hipStream_t st)
 {
     constexpr int GM = DP == 64 ? 64 : 128;
     if (a.D == DP && (1 << a.lg_G) == GM) return rows4_pick<S, DP, GM, P16>(a, st);
+    if constexpr (DP == 128) {
+        if (a.D == DP && a.lg_G == 6 && a.rows == 16) return rows4_go<S, DP, 64, P16, 1>(a, st);
+    }
     return rows4_pick<S, DP, 32, P16>(a, st);
 }
 
