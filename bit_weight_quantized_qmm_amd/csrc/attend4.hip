@@ -192,16 +192,18 @@ __device__ __forceinline__ int4_t places4(uint32_t w)
 // Codes and scales go from memory into LDS without a register, two blocks ahead, each wave into a
 // ring of its own; they are read once, so they leave no trace in the L2 (with the default policy the
 // loads alone took 95 us of the 4 sequences below, 84 without).
-// Pages of a multiple of 16 tokens (P16): a half of a block lies in one page; lane l looks
+// Pages of a multiple of 16 tokens (HALVES): a half of a block lies in one page; lane l looks
 // up the l-th half of the next 32 blocks, and its place goes to scalar registers
-// when its turn comes.  Other page sizes: a lane's key by its own page.
-// Measured (us): 4 sequences of up to 131071 keys, 8 key heads of 128 for 64, G 128: 100 (5.0
-// TB/s; the loads alone 84; a plain streaming read reaches 7.1); 64 of up to 8192, 32 heads: G 128 68 (4.1), G 64 80, G 32 82.  With
-// the loads in registers, one block ahead, three waves a SIMD: 105, 74, 112, 86.
+// when its turn comes.  Other page sizes: a lane's key by its own page, two blocks a lookup; where
+// a page holds a cache line or less of a head (SHARED), a sequence's heads run on one L2, whose lines they share.
+// Measured (us): 4 sequences of up to 131071 keys, 8 key heads of 128 for 64, G 128: 96 (5.2
+// TB/s; the loads alone 85; a plain streaming read reaches 7.1); 64 of up to 8192, 32 heads: G 128 65 (4.4; the loads alone
+// 57), G 64 74 (57), G 32 77 (63); one of 513 keys 9.5 (7.4).
 // ---------------------------------------------------------------------------
-__host__ __device__ constexpr int rows4_occupancy(int DP, int GM, bool P16, int QT)
+enum { HALVES, ANY, SHARED };         // PAGES
+__host__ __device__ constexpr int rows4_occupancy(int DP, int GM, int PAGES, int QT)
 {
-    return DP > 128 || QT > 1 ? 2 : DP == 128 && (GM == 64 || (GM == 128 && !P16)) ? 3 : 4;
+    return DP > 128 || QT > 1 ? 2 : DP == 128 && (GM == 64 || (GM == 128 && PAGES != HALVES)) ? 3 : 4;
 }
 __host__ __device__ constexpr int rows4_waves(int DP) { return DP > 128 ? 2 : 4; }      // 64 KB of ring at most
 __host__ __device__ constexpr int rows4_groups(int DP, int GM) { return GM > 32 ? DP / GM : DP / 32; }
@@ -209,7 +211,7 @@ __host__ __device__ constexpr int rows4_groups(int DP, int GM) { return GM > 32 
 __host__ __device__ constexpr int rows4_scales(int DP, int GM) { return rows4_groups(DP, GM) <= 4 ? 256 : 64 * rows4_groups(DP, GM); }
 __host__ __device__ constexpr int rows4_block(int DP, int GM) { return 2 * (32 * DP / 2 + 2 * rows4_scales(DP, GM)); }
 constexpr int ROWS4_IDS = 8;          // blocks whose page ids a wave keeps in LDS where pages are no multiple of 16 tokens
-__host__ __device__ constexpr int rows4_ring(int DP, int GM, bool P16) { return 2 * rows4_block(DP, GM) + (P16 ? 0 : ROWS4_IDS * 32 * 4); }
+__host__ __device__ constexpr int rows4_ring(int DP, int GM, int PAGES) { return 2 * rows4_block(DP, GM) + (PAGES == HALVES ? 0 : ROWS4_IDS * 32 * 4); }
 
 // Loads of the lanes' 16 (4) bytes at p + off into LDS, from `to` on, lane by lane.  The compiler does
 // not know that they are in flight: wait_loads() before what they bring is read, and what stood there
@@ -222,21 +224,26 @@ __device__ __forceinline__ void fetch(uint32_t to, __amdgpu_buffer_rsrc_t r, uin
     else
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen nt lds" ::"s"(to), "v"(off), "s"(r) : "memory", "m0");
 }
-template <int BYTES>
+template <int BYTES, bool KEEP>
 __device__ __forceinline__ void fetch(uint32_t to, const uint8_t *p)
 {
-    if constexpr (BYTES == 16)
+    if constexpr (BYTES == 16 && KEEP)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(p) : "memory", "m0");
+    else if constexpr (BYTES == 16)
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off nt" ::"s"(to), "v"(p) : "memory", "m0");
+    else if constexpr (KEEP)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(to), "v"(p) : "memory", "m0");
     else
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off nt" ::"s"(to), "v"(p) : "memory", "m0");
 }
 template <int N> __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
 __device__ __forceinline__ void wait_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
-template <typename S, int DP, int GM, bool P16, int QT>
-__global__ __launch_bounds__(64 * rows4_waves(DP)) __attribute__((amdgpu_waves_per_eu(rows4_occupancy(DP, GM, P16, QT), rows4_occupancy(DP, GM, P16, QT)))) void attend4_rows_kernel(const Attend4Args a)
+template <typename S, int DP, int GM, int PAGES, int QT>
+__global__ __launch_bounds__(64 * rows4_waves(DP)) __attribute__((amdgpu_waves_per_eu(rows4_occupancy(DP, GM, PAGES, QT), rows4_occupancy(DP, GM, PAGES, QT)))) void attend4_rows_kernel(const Attend4Args a)
 {
     constexpr int NW = rows4_waves(DP);
+    constexpr bool P16 = PAGES == HALVES, NEAR = PAGES == SHARED;
     constexpr bool DEFER = GM > 32;
     constexpr int KJ = DP / 32;                                   // steps of Q K^T
     constexpr int KW = DEFER ? GM / 32 : DP == 64 ? 2 : 4;        // dwords of a slice
@@ -256,9 +263,13 @@ __global__ __launch_bounds__(64 * rows4_waves(DP)) __attribute__((amdgpu_waves_p
     constexpr float TOP = A4_TOP - A4_LAZY;
     extern __shared__ __attribute__((aligned(16))) float att_lds[];
 
-    // sequence and head fastest, splits slowest
-    const int id = blockIdx.x, above = a.by_groups(id), bh = id - above * a.by_groups.d;
-    const int split = a.by_rblocks(above), rb = above - split * a.rblocks, b = a.by_Hkv(bh), hk = bh - b * a.Hkv;
+    // head and sequence fastest, splits slowest; SHARED: eight sequences take turns (workgroups go round the
+    // eight L2s), so that a sequence's heads share one
+    const int id = blockIdx.x, eight = NEAR ? a.by_Hkv(id >> 3) : 0;
+    const bool turns = NEAR && (eight + 1) * 8 * a.Hkv <= (int)gridDim.x;
+    const int rest = turns ? 8 * eight + (id & 7) : a.by_Hkv(id), hk = turns ? (id >> 3) - eight * a.Hkv : id - rest * a.Hkv;
+    const int above = a.by_groups(rest * a.Hkv), b = rest - above * a.B;
+    const int split = a.by_rblocks(above), rb = above - split * a.rblocks;
 
     // Without a window a place is its key, whatever the lengths say: the first pages are looked up
     // while those are on their way.
@@ -280,7 +291,7 @@ __global__ __launch_bounds__(64 * rows4_waves(DP)) __attribute__((amdgpu_waves_p
     // stands such that the dwords that 64 lanes read at once lie in 64 banks: pieces of 16 bytes in
     // the order [group][e][g][c % 2][c / 8] (GM = 64), else [pieces / 4][i][g][piece % 4] (the key is 4g + i, or 4g + 2e +
     // c % 2).
-    uint8_t *ring = reinterpret_cast<uint8_t *>(att_lds) + wave * rows4_ring(DP, GM, P16);
+    uint8_t *ring = reinterpret_cast<uint8_t *>(att_lds) + wave * rows4_ring(DP, GM, PAGES);
     const uint32_t ring_at = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)ring);
     int kkey[CF], vkey[CF];                 // of the piece that this lane loads: its key, where in the row
     uint32_t kpart[CF], vpart[CF];
@@ -378,10 +389,10 @@ __global__ __launch_bounds__(64 * rows4_waves(DP)) __attribute__((amdgpu_waves_p
 #pragma unroll
                 for (int f = 0; f < CF; ++f) {
                     const uint8_t *p = base + sent(off, 32 * (n & 1) + 16 * t + key[f]) + part[f];
-                    if (CH >= 4 || lane < 16 * CH) fetch<16>(to + t * HALF + 1024 * f, p);
+                    if (CH >= 4 || lane < 16 * CH) fetch<16, NEAR>(to + t * HALF + 1024 * f, p);
                 }
 #pragma unroll
-                for (int f = 0; f < SF; ++f) fetch<4>(sto + t * SHALF + 256 * f, sbase + sent(soff, 32 * (n & 1) + 16 * t + stok[f]) + spart[f]);
+                for (int f = 0; f < SF; ++f) fetch<4, NEAR>(sto + t * SHALF + 256 * f, sbase + sent(soff, 32 * (n & 1) + 16 * t + stok[f]) + spart[f]);
             }
         }
     };
@@ -1263,9 +1274,9 @@ int64_t plan_attend4(Attend4Args &a)
         }
     } else {
         // The GPU holds 1024 workgroups at once; with at least 64 KB of codes and scales each, or 16 KB
-        // where there are few (4 sequences of up to 131071 keys, 8 heads, us: 100 in 24 shares, 100 in 32, 104
-        // in 64; one of 4000: 18.8 in 4, 13.8 in 16, 12.5 in 32).  Many sequences are hardly ever alike in
-        // length: shares of 160 KB let the GPU even them out (64 of up to 8192: 68 in 4, 83 in 2; D 64: 55 in 3, 69 in 2).  One
+        // where there are few (4 sequences of up to 131071 keys, 8 heads, us: 96 in 24 shares, 97 in 32, 98
+        // in 48; one of 5000, G 64: 19.5 in 4, 13.8 in 16, 12.8 in 32).  Many sequences are hardly ever alike in
+        // length: shares of 160 KB let the GPU even them out (64 of up to 8192, G 128: 65 in 4, 77 in 2).  One
         // launch without a join is enough where the keys are few.
         unit = 32 * rows4_waves(a.D);
         const int64_t bytes = (span - 15) * (a.D + 8 * (a.D >> a.lg_G)), kb = 1024;
@@ -1298,38 +1309,48 @@ static hipError_t tiles4_go(const Attend4Args &a, hipStream_t st)
     return hipGetLastError();
 }
 
-template <typename S, int DP, int GM, bool P16, int QT>
+template <typename S, int DP, int GM, int PAGES, int QT>
 static hipError_t rows4_go(const Attend4Args &a, hipStream_t st)
 {
     constexpr int NW = rows4_waves(DP);
     const int nrow = (int)std::min<int64_t>(16 * QT, (int64_t)a.max_q * a.g);
-    const size_t lds = std::max<size_t>((size_t)NW * nrow * (DP + 6) * 4, NW * rows4_ring(DP, GM, P16));   // join, ring
-    const hipError_t e = allow_lds(&attend4_rows_kernel<S, DP, GM, P16, QT>, lds);
+    const size_t lds = std::max<size_t>((size_t)NW * nrow * (DP + 6) * 4, NW * rows4_ring(DP, GM, PAGES));   // join, ring
+    const hipError_t e = allow_lds(&attend4_rows_kernel<S, DP, GM, PAGES, QT>, lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((attend4_rows_kernel<S, DP, GM, P16, QT>), dim3((unsigned)((int64_t)a.B * a.rblocks * a.Hkv * a.splits)), dim3(64 * NW), lds, st, a);
+    hipLaunchKernelGGL((attend4_rows_kernel<S, DP, GM, PAGES, QT>), dim3((unsigned)((int64_t)a.B * a.rblocks * a.Hkv * a.splits)), dim3(64 * NW), lds, st, a);
     return hipGetLastError();
 }
 
-template <typename S, int DP, int GM, bool P16>
+template <typename S, int DP, int GM, int PAGES>
 static hipError_t rows4_pick(const Attend4Args &a, hipStream_t st)
 {
     if constexpr (DP <= 128) {
-        if (a.rows == 32) return rows4_go<S, DP, GM, P16, 2>(a, st);
+        if (a.rows == 32) return rows4_go<S, DP, GM, PAGES, 2>(a, st);
     }
-    return rows4_go<S, DP, GM, P16, 1>(a, st);
+    return rows4_go<S, DP, GM, PAGES, 1>(a, st);
 }
 // Groups that leave the codes as they are where they pay: of 64 in rows of 64 and 128, of 128 in rows of 128
 // and 256 (64 users of up to 8192 keys, us, so and as (c - z) s: D 64, G 64: 52 and 59; D 128, G 128: 65 and 75; D 128, G 64: 76 and
 // 80, pages of 100 tokens 78 and 85).  Two tiles of rows with groups of 64 in rows of 128 have not the registers for it (105 and 102).
-template <typename S, int DP, bool P16>
+template <typename S, int DP, int PAGES>
 static hipError_t rows4_by_group(const Attend4Args &a, hipStream_t st)
 {
     constexpr int GM = DP == 64 ? 64 : 128;
-    if (a.D == DP && (1 << a.lg_G) == GM) return rows4_pick<S, DP, GM, P16>(a, st);
+    if (a.D == DP && (1 << a.lg_G) == GM) return rows4_pick<S, DP, GM, PAGES>(a, st);
     if constexpr (DP == 128) {
-        if (a.D == DP && a.lg_G == 6 && a.rows == 16) return rows4_go<S, DP, 64, P16, 1>(a, st);
+        if (a.D == DP && a.lg_G == 6 && a.rows == 16) return rows4_go<S, DP, 64, PAGES, 1>(a, st);
     }
-    return rows4_pick<S, DP, 32, P16>(a, st);
+    return rows4_pick<S, DP, 32, PAGES>(a, st);
+}
+
+// SHARED: what a page holds of a head is a cache line at most, and neighbouring heads read the same lines (64 users
+// of up to 8192 keys, us, so and as any page: D 128, pages of 1 token 125 and 188, of 2 96 and 110, of 4 89 and 86;
+// D 32, of 1 96 and 208, of 8 95 and 97; D 256, up to 4096, of 1 126 and 147, of 2 122 and 117).
+template <typename S, int DP>
+static hipError_t rows4_by_pages(const Attend4Args &a, hipStream_t st)
+{
+    if (a.halves) return rows4_by_group<S, DP, HALVES>(a, st);
+    return a.page * a.D / 2 <= 128 ? rows4_by_group<S, DP, SHARED>(a, st) : rows4_by_group<S, DP, ANY>(a, st);
 }
 
 // A wave a row where the splits are few, the workgroup's four where a single wave would
@@ -1358,11 +1379,11 @@ static hipError_t attend4_type(const Attend4Args &a, hipStream_t st)
     if (a.rows > 32)
         e = a.D <= 64 ? tiles4_go<S, 64>(a, st) : a.D <= 96 ? tiles4_go<S, 96>(a, st) : a.D <= 128 ? tiles4_go<S, 128>(a, st) : tiles4_go<S, 256>(a, st);
     else if (a.D <= 64)
-        e = a.halves ? rows4_by_group<S, 64, true>(a, st) : rows4_by_group<S, 64, false>(a, st);
+        e = rows4_by_pages<S, 64>(a, st);
     else if (a.D <= 128)
-        e = a.halves ? rows4_by_group<S, 128, true>(a, st) : rows4_by_group<S, 128, false>(a, st);
+        e = rows4_by_pages<S, 128>(a, st);
     else
-        e = a.halves ? rows4_by_group<S, 256, true>(a, st) : rows4_by_group<S, 256, false>(a, st);
+        e = rows4_by_pages<S, 256>(a, st);
     if (e != hipSuccess || a.splits == 1) return e;
     if (a.D <= 64) return join4_go<S, 64>(a, st);
     if (a.D <= 128) return join4_go<S, 128>(a, st);

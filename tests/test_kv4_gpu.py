@@ -477,7 +477,7 @@ SEQS = {
 @pytest.mark.parametrize("seqs", list(SEQS))
 @pytest.mark.parametrize("Hq,Hkv,D,G,page", [(8, 2, 128, 128, 16), (5, 5, 64, 64, 1), (6, 2, 96, 32, 32), (16, 1, 32, 32, 7), (8, 1, 256, 64, 64), (24, 1, 128, 32, 256),
                                              (3, 1, 192, 64, 48), (4, 4, 128, 64, 1), (8, 2, 64, 32, 16), (4, 2, 256, 128, 5), (2, 2, 224, 32, 16),
-                                             (8, 1, 128, 128, 7), (16, 2, 128, 64, 16), (24, 1, 128, 64, 3), (32, 1, 128, 128, 5), (20, 1, 64, 64, 16)])
+                                             (8, 1, 128, 128, 7), (9, 3, 64, 32, 2), (16, 2, 128, 64, 16), (24, 1, 128, 64, 3), (32, 1, 128, 128, 5), (20, 1, 64, 64, 16)])
 def test_attention(q, dtype, seqs, Hq, Hkv, D, G, page):
     c = Paged(q, SEQS[seqs], Hq, Hkv, D, G, page, dtype, seed=D + page)
     c.check(*c.run(q))
