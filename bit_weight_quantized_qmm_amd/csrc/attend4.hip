@@ -850,6 +850,10 @@ __global__ __launch_bounds__(64 * rows4_waves(DP)) __attribute__((amdgpu_waves_p
 // that stage them make out of the codes: once for all rows.
 // Keys stand in LDS in codes' order within each 8 elements (q's rows do too), values in
 // their own.
+// The matrix instructions and the softmax between them bound it, which share a SIMD's issue: 2 prompts of 4096
+// tokens, 32 heads of 128: 327 to 340 us, 840 to 810 TFLOP/s of a large product's 1216, matrix instructions in 37 % of the
+// cycles and vector ones in 57 %.  Taking the codes out costs what reading rows of 16 bits does (those: 335
+// us).  D = 256 has one wave a SIMD (2 chunks of 300 on up to 8192 keys, 16 heads: 238 us, 270 TFLOP/s).
 // ---------------------------------------------------------------------------
 __host__ __device__ constexpr int tiles4_keys(int D) { return D <= 128 ? 64 : 32; }
 __host__ __device__ constexpr int tiles4_waves(int D) { return D <= 128 ? 8 : 4; }
