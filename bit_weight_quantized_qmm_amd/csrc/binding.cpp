@@ -359,8 +359,9 @@ qmm_kv4_cache cache4(PyObject *o, int &index, bool leads)
     qmm_kv4_cache c{};
     c.k = (uint8_t *)k.mutable_data_ptr(), c.v = (uint8_t *)v.mutable_data_ptr();
     c.k_scale = (qmm_half *)ks.mutable_data_ptr(), c.v_scale = (qmm_half *)vs.mutable_data_ptr();
-    for (int i = 0; i < 3; ++i) c.k_stride[i] = k.stride(i), c.v_stride[i] = v.stride(i);
-    for (int i = 0; i < 2; ++i) c.k_scale_stride[i] = ks.stride(i), c.v_scale_stride[i] = vs.stride(i);
+    auto step = [](const at::Tensor &t, int i) { return t.size(i) > 1 ? t.stride(i) : 0; };      // (of one page, head or token it says nothing)
+    for (int i = 0; i < 3; ++i) c.k_stride[i] = step(k, i), c.v_stride[i] = step(v, i);
+    for (int i = 0; i < 2; ++i) c.k_scale_stride[i] = step(ks, i), c.v_scale_stride[i] = step(vs, i);
     c.pages = k.size(0), c.Hkv = k.size(1), c.page = k.size(2), c.D = D, c.G = D / groups;
     return c;
 }

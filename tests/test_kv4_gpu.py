@@ -558,6 +558,24 @@ def test_attention_layouts(q):
     assert same(wide[:, :, 1], out) and (wide[:, :, 0] == 7).all() and (wide[:, :, 2] == 7).all()
 
 
+def test_strides_of_single_sizes_say_nothing(q):
+    """One page, one head, pages of one token: torch leaves any stride there."""
+    for pages, heads_, page in ((20, 3, 1), (20, 1, 16), (1, 3, 16), (1, 1, 1)):
+        g = gen(pages + heads_)
+        T = min(pages * page, 20)
+        _, k, v = heads(T, 0, heads_, 64, F16, g)
+        slots = place(T, pages, page, g)
+        a, b = (q.kv4_cache(pages, heads_, page, 64, 32) for _ in range(2))
+        odd = q.KV4Cache(*(t.as_strided(t.shape, [7 if n == 1 else s for n, s in zip(t.shape[:3], t.stride()[:3])] + list(t.stride()[3:])) for t in b))
+        q.kv4_append(None, k, v, a, slots)
+        q.kv4_append(None, k, v, odd, slots)
+        assert all(same(x, y) for x, y in zip(a, b))
+        assert all(same(x, y) for x, y in zip(q.kv4_read(a, slots), q.kv4_read(odd, slots)))
+        table, cu, lens = torch.arange(pages, device=DEV, dtype=torch.int32)[None], torch.tensor([0, 1], device=DEV, dtype=torch.int32), torch.tensor([T], device=DEV, dtype=torch.int32)
+        x = torch.randn(1, 2 * heads_, 64, generator=g, device=DEV).half()
+        assert same(q.kv4_attention(x, a, table, cu, lens, 1, T), q.kv4_attention(x, odd, table, cu, lens, 1, T))
+
+
 def test_attention_nothing(q):
     c = Paged(q, [(1, 0), (3, 0)], 4, 1, 64, 32, 16, F16)
     out, lse = c.run(q)
