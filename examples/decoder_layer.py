@@ -1,11 +1,11 @@
 """A decoder layer on 4-bit weights, served from a paged cache.
 
-    python examples/decoder_layer.py [--steps 50] [--users 16] [--prompt 700]
+    python examples/decoder_layer.py [--steps 50] [--users 16] [--prompt 700] [--cache-bits 16]
 
 Each user's prompt runs through the layer in one call (chunks of different lengths side by side),
 then all users decode a token at a time, the step captured in a graph.  Projections are
 `linear` calls with their epilogues, positions and the cache `kv_append`, attention
-`paged_attention`; only the norm is torch's.  Weights are random, quantised by `quantize`.
+`paged_attention` (with `--cache-bits 4` `kv4_append` and `kv4_attention`); only the norm is torch's.  Weights are random, quantised by `quantize`.
 The last step's outputs are compared with the same layer in fp32 on the dequantised weights.
 """
 import argparse
@@ -55,8 +55,12 @@ class Layer:
 
     def __call__(self, x, cache, slots, positions, rope, table, cu_q, kv_lens, max_q, max_kv):
         q, k, v = self.split(self.qkv(norm(x)))
-        q = qmm.kv_append(q, k, v, cache[0], cache[1], slots, positions, rope)
-        a = qmm.paged_attention(q, cache[0], cache[1], table, cu_q, kv_lens, max_q, max_kv)
+        if isinstance(cache, qmm.KV4Cache):
+            q = qmm.kv4_append(q, k, v, cache, slots, positions, rope)
+            a = qmm.kv4_attention(q, cache, table, cu_q, kv_lens, max_q, max_kv)
+        else:
+            q = qmm.kv_append(q, k, v, cache[0], cache[1], slots, positions, rope)
+            a = qmm.paged_attention(q, cache[0], cache[1], table, cu_q, kv_lens, max_q, max_kv)
         x = self.o(a.flatten(1), residual=x)
         h = norm(x)
         return self.down(self.gate(h, act="silu", mul=self.up(h)), residual=x)
@@ -77,7 +81,7 @@ class Layer:
         return x + (g * torch.sigmoid(g) * (h @ self.up.dense())) @ self.down.dense()
 
 
-def run(hidden=4096, heads=32, kv_heads=8, head_dim=128, inner=14336, users=16, prompt=700, steps=50, page=16, seed=0):
+def run(hidden=4096, heads=32, kv_heads=8, head_dim=128, inner=14336, users=16, prompt=700, steps=50, page=16, seed=0, cache_bits=16):
     """Prompts, then `steps` decode steps; returns (us a decode step, relative error of a user's last output)."""
     dev, gen = "cuda", torch.Generator(device="cuda")
     gen.manual_seed(seed)
@@ -85,7 +89,10 @@ def run(hidden=4096, heads=32, kv_heads=8, head_dim=128, inner=14336, users=16, 
     lens = [max(1, prompt - 37 * u % prompt) for u in range(users)]
     most = max(lens) + steps
     width = -(-most // page)
-    cache = tuple(torch.zeros(users * width, kv_heads, page, head_dim, device=dev, dtype=torch.float16) for _ in range(2))
+    if cache_bits == 4:
+        cache = qmm.kv4_cache(users * width, kv_heads, page, head_dim)
+    else:
+        cache = tuple(torch.zeros(users * width, kv_heads, page, head_dim, device=dev, dtype=torch.float16) for _ in range(2))
     table = torch.randperm(users * width, generator=gen, device=dev).to(torch.int32).view(users, width)
     angle = torch.arange(most, device=dev, dtype=torch.float64)[:, None] * 10000.0 ** (-torch.arange(head_dim // 2, device=dev, dtype=torch.float64) * 2 / head_dim)
     rope = torch.cat((angle.cos(), angle.sin()), 1).float()
@@ -139,6 +146,7 @@ if __name__ == "__main__":
     ap = argparse.ArgumentParser()
     for name, value in (("steps", 50), ("users", 16), ("prompt", 700)):
         ap.add_argument(f"--{name}", type=int, default=value)
+    ap.add_argument("--cache-bits", type=int, choices=(4, 16), default=16)
     a = ap.parse_args()
-    us, error = run(users=a.users, prompt=a.prompt, steps=a.steps)
-    print(f"decode step of one layer, {a.users} users, prompts up to {a.prompt}: {us:.1f} us; relative error of the last output {error:.1e}")
+    us, error = run(users=a.users, prompt=a.prompt, steps=a.steps, cache_bits=a.cache_bits)
+    print(f"decode step of one layer, {a.users} users, prompts up to {a.prompt}, cache of {a.cache_bits} bits: {us:.1f} us; relative error of the last output {error:.1e}")

@@ -710,6 +710,16 @@ def test_layer_step_in_a_graph(q):
 
 
 # -------------------------------------------------------------- refusals --
+def test_decoder_layer_example(q):
+    """The example runs on a cache of 4 bits."""
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "decoder_layer.py")
+    spec = importlib.util.spec_from_file_location("decoder_layer_4", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    us, error = example.run(hidden=512, heads=8, kv_heads=2, head_dim=64, inner=1024, users=3, prompt=50, steps=4, cache_bits=4)
+    assert us > 0 and math.isfinite(error)
+
+
 def test_refusals_on_the_gpu(q):
     """Shapes, types and devices that do not fit, named in the error; nothing is written."""
     c = Paged(q, [(1, 20)], 4, 2, 64, 32, 16, F16)
