@@ -851,9 +851,10 @@ __global__ __launch_bounds__(64 * rows4_waves(DP)) __attribute__((amdgpu_waves_p
 // Keys stand in LDS in codes' order within each 8 elements (q's rows do too), values in
 // their own.
 // The matrix instructions and the softmax between them bound it, which share a SIMD's issue: 2 prompts of 4096
-// tokens, 32 heads of 128: 327 to 340 us, 840 to 810 TFLOP/s of a large product's 1216, matrix instructions in 37 % of the
+// tokens, 32 heads of 128: 326 us, 842 TFLOP/s of a large product's 1216, matrix instructions in 37 % of the
 // cycles and vector ones in 57 %.  Taking the codes out costs what reading rows of 16 bits does (those: 335
-// us).  D = 256 has one wave a SIMD (2 chunks of 300 on up to 8192 keys, 16 heads: 238 us, 270 TFLOP/s).
+// us).  Masks as a bit a key (compared key by key: 337; 16 chunks of up to 256 tokens 37.6, now 34.0).  D = 256 has one
+// wave a SIMD (2 chunks of 300 on up to 8192 keys, 16 heads: 230 us, 280 TFLOP/s).
 // ---------------------------------------------------------------------------
 __host__ __device__ constexpr int tiles4_keys(int D) { return D <= 128 ? 64 : 32; }
 __host__ __device__ constexpr int tiles4_waves(int D) { return D <= 128 ? 8 : 4; }
@@ -968,16 +969,17 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DC <= 1
         return ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane(hi) << 32) | (uint32_t)__builtin_amdgcn_readfirstlane(lo);
     };
     auto off64 = [](int lo, int hi) { return (int64_t)(((uint64_t)(uint32_t)hi << 32) | (uint32_t)lo); };
+    const uint8_t *kb = kbase + in_row, *vb = vbase + in_row, *ksb = ksbase + in_scales, *vsb = vsbase + in_scales;
     auto load_tile = [&](int tile) {
         const int slot = tile % SLOTS;
         const int4_t mk = masks[slot];
 #pragma unroll
         for (int n = 0; n < LN; ++n) {
             const int4_t at = places[2 * (slot * KB + srow + SSTEP * n)], as = places[2 * (slot * KB + srow + SSTEP * n) + 1];
-            kst[n] = *reinterpret_cast<const uint32_t *>(kbase + off64(at[0], at[1]) + in_row);
-            vst[n] = *reinterpret_cast<const uint32_t *>(vbase + off64(at[2], at[3]) + in_row);
-            kss[n] = *reinterpret_cast<const uint32_t *>(ksbase + off64(as[0], as[1]) + in_scales);
-            vss[n] = *reinterpret_cast<const uint32_t *>(vsbase + off64(as[2], as[3]) + in_scales);
+            kst[n] = *reinterpret_cast<const uint32_t *>(kb + off64(at[0], at[1]));
+            vst[n] = *reinterpret_cast<const uint32_t *>(vb + off64(at[2], at[3]));
+            kss[n] = *reinterpret_cast<const uint32_t *>(ksb + off64(as[0], as[1]));
+            vss[n] = *reinterpret_cast<const uint32_t *>(vsb + off64(as[2], as[3]));
         }
         vlive = uniform64(mk[0], mk[1]);
         hidden = uniform64(mk[2], mk[3]);
@@ -1077,16 +1079,18 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DC <= 1
             }
             __builtin_amdgcn_sched_barrier(0);
             if (v0 + KB > end || key0 + KB > wall_hi || (key0 < wall_lo && key0 + KB > kr.sk) || bad) {
-                // element e of tile t is key key0 + 4 h + kt, kt a constant (v0 + KB > end with the last places alone: key >= vhi there)
+                // element e of tile t is key key0 + 4 h + 32 t + e % 4 + 8 (e / 4) (v0 + KB > end with the last places alone: key >= vhi there)
                 const int to = min(vhi, key0 + end - v0) - key0 - 4 * h, from = vlo - key0 - 4 * h, sinks = kr.sk - key0 - 4 * h;
-                const uint64_t hide = bad >> (4 * h);
+                auto below = [](int n) { return n >= 64 ? ~uint64_t(0) : (uint64_t(1) << max(n, 0)) - 1; };      // keys before the n-th
+                const uint64_t mine = below(to) & (~below(from) | below(sinks)) & ~(bad >> (4 * h));
+                const int word[2] = {(int)(uint32_t)mine, (int)(uint32_t)(mine >> 32)};
 #pragma unroll
                 for (int t = 0; t < KT; ++t)
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const int kt = 32 * t + (e & 3) + 8 * (e >> 2);
-                        const bool off = kt >= to || (kt < from && kt >= sinks) || ((uint32_t)(hide >> (32 * t)) & (1u << (kt & 31)));
-                        s[t][e] = off ? -INFINITY : s[t][e];
+                        const int m = (word[t] << (31 - (e & 3) - 8 * (e >> 2))) >> 31;
+                        const float was = s[t][e];       // (a copy: bit_cast of a vector's element takes its first)
+                        s[t][e] = __builtin_bit_cast(float, (__builtin_bit_cast(int, was) & m) | ((int)0xff800000u & ~m));
                     }
             }
             float mx = s[0][0];

@@ -105,7 +105,7 @@ __device__ __forceinline__ double quotient(double x, double s, double inv)
 // once.  As in append.hip a lane owns two vectors of 8 elements that turn
 // together (past rot two that stay), of HP heads of one token, so that cos and
 // sin are read once for them; U lanes own a row, and the sum of its squares goes
-// round them.
+// round them.  8192 tokens of 64 + 8 heads of 128, bf16: 59 us, 5.2 TB/s (a large copy the same); 1 token 4.2, the call.
 // ---------------------------------------------------------------------------
 template <typename S, bool PAIRS, bool VEC, int U, int HP>
 __device__ __forceinline__ void turn_rows(const HeadsArgs &a, int block, int groups)
@@ -207,7 +207,7 @@ __device__ __forceinline__ void turn_rows(const HeadsArgs &a, int block, int gro
 // heads, k and v of each, LN lanes a token's row; range and zero-point go round the G / 8
 // lanes of a group.  A workgroup's 256 / LN tokens stand side by side in a page's head.  Its
 // waves wait for memory (one row a wave: 31 us for 8192 tokens of 2 x 8 heads, k and v of two
-// heads 26; few tokens: see heads_pick), so they run between q's, which is bound by memory: 72 us for both, 54 for q.
+// heads 26; few tokens: see heads_pick), so they run between q's, which is bound by memory: 72 to 78 us for both (cards differ), 54 for q.
 //
 // k is normed, turned and mapped in fp32 first, with a bound of what its roundings may have
 // moved its elements by; where that leaves a scale, a zero-point or a code in doubt
@@ -544,7 +544,8 @@ hipError_t launch_heads(const HeadsArgs &a, bool bf16, bool vec, bool store, hip
 // Tokens of the cache as 16-bit rows: bound by what it writes.  A lane takes 8
 // elements of a token, of HP heads and both sides; U lanes a row.  A workgroup's
 // tokens stand side by side in a page's head, its heads side by side in a
-// token's output.
+// token's output.  131072 tokens of 2 x 8 heads of 128, G 64: 128 to 136 us, 5.1 to 5.4 TB/s, four fifths of it written;
+// 1001 of 2 x 4 heads of 96: 5.6, the call.
 // ---------------------------------------------------------------------------
 template <typename S, bool VEC, int U, int HP>
 __global__ __launch_bounds__(256) void read4_kernel(const Read4Args a)
