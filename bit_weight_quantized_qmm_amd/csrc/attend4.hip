@@ -851,8 +851,8 @@ __global__ __launch_bounds__(64 * rows4_waves(DP)) __attribute__((amdgpu_waves_p
 // Keys stand in LDS in codes' order within each 8 elements (q's rows do too), values in
 // their own.
 // The matrix instructions and the softmax between them bound it, which share a SIMD's issue: 2 prompts of 4096
-// tokens, 32 heads of 128: 326 us, 842 TFLOP/s of a large product's 1216, matrix instructions in 37 % of the
-// cycles and vector ones in 57 %.  Taking the codes out costs what reading rows of 16 bits does (those: 335
+// tokens, 32 heads of 128: 326 us, 842 TFLOP/s of a large product's 1216, matrix instructions in 39 % of the
+// cycles and vector ones in 54 %.  Taking the codes out costs what reading rows of 16 bits does (those: 335
 // us).  Masks as a bit a key (compared key by key: 337; 16 chunks of up to 256 tokens 37.6, now 34.0).  D = 256 has one
 // wave a SIMD (2 chunks of 300 on up to 8192 keys, 16 heads: 230 us, 280 TFLOP/s).
 // ---------------------------------------------------------------------------
