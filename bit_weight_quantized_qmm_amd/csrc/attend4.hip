@@ -28,6 +28,7 @@ typedef _Float16 f16_t;
 // fp16 probabilities are scaled by 2^15: in full down to 2^-29 of a row's largest.
 constexpr float A4_TOP = 15.f;
 constexpr float A4_LAZY = 4.f;         // a maximum may be exceeded by this much (base 2): p ends at 2^15
+constexpr float A4_LIFT = 24.f;        // of weights p s: brings the least s of fp16 to 1
 
 struct Range4 {
     int t0, n, L;
@@ -183,11 +184,12 @@ __device__ __forceinline__ int4_t places4(uint32_t w)
 //       their elements there divided by 16.  A step of the contraction lies in one group:
 //           x = sum over the groups of s (sum_d q_d c_d - z sum_d q_d),
 //       on the accumulators, four keys of a lane.
-//   V   a tile of O^T lies in one group, whose s goes into the probabilities: p s / 2^e, 2^e
-//       above the largest s so far (e is kept as the maximum of the scores is, and in it),
+//   V   a tile of O^T lies in one group, whose s goes into the probabilities: p s 2^lift,
 //       rounded to f16 as p would be; sum_j p_j s_j z_j is a product of its own, taken off at
-//       the end.  (In groups of 64 the lanes c and c ^ 1 read a dword of two keys each and change
-//       halves.)
+//       the end.  Each row has a lift for each group, such that its largest p s there stands at
+//       2^11 to 2^15: other groups' scales, and those of keys that get no weight, take none of
+//       its bits.  The first group's is in the exponent of p already.  (In groups of 64 the lanes
+//       c and c ^ 1 read a dword of two keys each and change halves.)
 // Other groups (GM = 32): every code becomes (c - z) s in f16.
 // Codes and scales go from memory into LDS without a register, two blocks ahead, each wave into a
 // ring of its own; they are read once, so they leave no trace in the L2 (with the default policy the
@@ -472,18 +474,29 @@ __global__ __launch_bounds__(64 * rows4_waves(DP)) __attribute__((amdgpu_waves_p
     const int all_hi = min(kr.hi, kr.L - kr.n + a.by_g(rb * a.rows) + 1);
     const int all_lo = a.window > 0 ? kr.hi - a.window : 0;
 
-    // m: the running maximum, DEFER: with the exponent `rise` of the largest scale so far added
-    float m[QT], l[QT], rise = -24.f, most = 0x1p-24f;
+    // m: the running maximum.  DEFER: rounded down to a whole number, as the lifts are, so that what stands is
+    // multiplied by powers of two alone; l and group 0 are in units of 2^(lift[0] - m), group ns' in 2^(lift[ns] - m),
+    // `more` times as large (two groups at most)
+    float m[QT], l[QT], lift[QT][NS], more[QT];
     float4_t o[QT][XT], oz[QT][NS];      // oz: sum of p s z, alike in all four
 #pragma unroll
     for (int qt = 0; qt < QT; ++qt) {
         m[qt] = -INFINITY;
         l[qt] = 0.f;
+        more[qt] = 1.f;
 #pragma unroll
         for (int x = 0; x < XT; ++x) o[qt][x] = float4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int x = 0; x < NS; ++x) oz[qt][x] = float4_t{0.f, 0.f, 0.f, 0.f};
+        for (int x = 0; x < NS; ++x) {
+            oz[qt][x] = float4_t{0.f, 0.f, 0.f, 0.f};
+            lift[qt][x] = A4_LIFT;
+        }
     }
+    auto scale_group = [&](int qt, int ns, float f) {
+#pragma unroll
+        for (int x = 0; x < XT / NS; ++x) o[qt][XT / NS * ns + x] *= f;
+        oz[qt][ns] *= f;
+    };
 
     for (int n = 0; n < blocks; ++n) {
         const int v0 = begin + 32 * (wave + NW * n);
@@ -652,29 +665,6 @@ __global__ __launch_bounds__(64 * rows4_waves(DP)) __attribute__((amdgpu_waves_p
         }
         gone[0] = gone[1];
         gone[1] = gone[2];
-        if constexpr (DEFER) {      // the largest scale so far, up to a power of two
-            half2_t top = as_half2(vsd[0][0][0]);
-#pragma unroll
-            for (int e = 1; e < 8 * NS; ++e) top = __builtin_elementwise_max(top, as_half2(vsd[e / (4 * NS)][e / NS % 4][e % NS]));
-            float mine = (float)top[0];
-            if (__any(mine > most)) {
-#pragma unroll
-                for (int x = 1; x < 64; x <<= 1) mine = fmaxf(mine, __shfl_xor(mine, x));
-                const float to = (float)__builtin_amdgcn_frexp_expf(mine), f = __builtin_amdgcn_exp2f(rise - to);
-#pragma unroll
-                for (int qt = 0; qt < QT; ++qt) {
-                    m[qt] += to - rise;
-                    if (n == 0) continue;          // (nothing but zeros yet)
-                    l[qt] *= f;
-#pragma unroll
-                    for (int x = 0; x < XT; ++x) o[qt][x] *= f;
-#pragma unroll
-                    for (int x = 0; x < NS; ++x) oz[qt][x] *= f;
-                }
-                rise = to;
-                most = __builtin_amdgcn_exp2f(to);
-            }
-        }
         float x[QT][8];
         int4_t p[QT];
 #pragma unroll
@@ -683,23 +673,31 @@ __global__ __launch_bounds__(64 * rows4_waves(DP)) __attribute__((amdgpu_waves_p
 #pragma unroll
             for (int e = 1; e < 8; ++e) mx = fmaxf(mx, s[qt][e >> 2][e & 3]);
             mx *= sl[qt];
-            if constexpr (DEFER) mx += rise;
             if (__any(mx > m[qt] + A4_LAZY)) {         // also the first finite maximum: m is -inf
                 mx = fmaxf(mx, __shfl_xor(mx, 16));
                 mx = fmaxf(mx, __shfl_xor(mx, 32));
-                const float mn = fmaxf(m[qt], mx), al = __builtin_amdgcn_exp2f(m[qt] - (mn == -INFINITY ? 0.f : mn));
-                m[qt] = mn;
-                if (n > 0) {
+                float mn = fmaxf(m[qt], mx);
+                if constexpr (DEFER) {
+                    // the weights so far keep their places (and only their places: f is 1) up to the largest lift
+                    mn = __builtin_floorf(mn);
+#pragma unroll
+                    for (int ns = 0; ns < NS; ++ns) {
+                        const float was = lift[qt][ns];
+                        lift[qt][ns] = fminf(was + (mn - m[qt]), A4_LIFT);      // (nothing seen: NaN, then the largest)
+                        const float f = __builtin_amdgcn_exp2f(m[qt] - (mn == -INFINITY ? 0.f : mn) + (lift[qt][ns] - was));
+                        if (n > 0) scale_group(qt, ns, f);
+                        if (ns == 0) l[qt] *= f;
+                    }
+                    more[qt] = __builtin_amdgcn_exp2f(lift[qt][NS - 1] - lift[qt][0]);
+                } else if (n > 0) {
+                    const float al = __builtin_amdgcn_exp2f(m[qt] - (mn == -INFINITY ? 0.f : mn));
                     l[qt] *= al;
 #pragma unroll
                     for (int xx = 0; xx < XT; ++xx) o[qt][xx] *= al;
-                    if constexpr (DEFER) {
-#pragma unroll
-                        for (int xx = 0; xx < NS; ++xx) oz[qt][xx] *= al;
-                    }
                 }
+                m[qt] = mn;
             }
-            const float base = (m[qt] == -INFINITY ? 0.f : m[qt]) - TOP;
+            const float base = (m[qt] == -INFINITY ? 0.f : m[qt]) - (DEFER ? TOP + lift[qt][0] : TOP);
             float sum = 0.f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -716,12 +714,34 @@ __global__ __launch_bounds__(64 * rows4_waves(DP)) __attribute__((amdgpu_waves_p
             for (int ns = 0; ns < NS; ++ns) {
                 int4_t zf;
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const uint32_t s0 = vsd[y >> 1][2 * y & 3][ns], s1 = vsd[y >> 1][(2 * y & 3) + 1][ns];
-                    zf[y] = (int)__builtin_amdgcn_perm(s1, s0, 0x07060302u);
+                for (int y = 0; y < 4; ++y) zf[y] = (int)__builtin_amdgcn_perm(vsd[y >> 1][(2 * y & 3) + 1][ns], vsd[y >> 1][2 * y & 3][ns], 0x07060302u);
+                auto weight = [&](int qt, int e) { return fmaf(ns == 0 ? x[qt][e] : x[qt][e] * more[qt], (float)as_half2(vsd[e >> 2][e & 3][ns])[0], 0.f); };
 #pragma unroll
-                    for (int qt = 0; qt < QT; ++qt)
-                        p[qt][y] = pack2(fmaf(x[qt][2 * y], (float)as_half2(s0)[0], 0.f), fmaf(x[qt][2 * y + 1], (float)as_half2(s1)[0], 0.f), f16_t());
+                for (int qt = 0; qt < QT; ++qt) {
+                    half2_t top = half2_t{(f16_t)0.f, (f16_t)0.f};
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        p[qt][y] = pack2(weight(qt, 2 * y), weight(qt, 2 * y + 1), f16_t());
+                        top = __builtin_elementwise_max(top, as_half2((uint32_t)p[qt][y]));
+                    }
+                    if (__any((float)__builtin_elementwise_max(top[0], top[1]) > 0x1p15f)) {      // (the first block's always)
+                        float mine = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) mine = fmaxf(mine, weight(qt, e));
+                        mine = fmaxf(mine, __shfl_xor(mine, 16));
+                        mine = fmaxf(mine, __shfl_xor(mine, 32));
+                        const float by = fminf(TOP + 1.f - (float)__builtin_amdgcn_frexp_expf(mine), 0.f), f = __builtin_amdgcn_exp2f(by);
+                        lift[qt][ns] += by;
+                        if (n > 0) scale_group(qt, ns, f);
+                        if (ns == 0) {
+                            l[qt] *= f;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) x[qt][e] *= f;
+                        }
+                        more[qt] = __builtin_amdgcn_exp2f(lift[qt][NS - 1] - lift[qt][0]);
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) p[qt][y] = pack2(weight(qt, 2 * y), weight(qt, 2 * y + 1), f16_t());
+                    }
                 }
 #pragma unroll
                 for (int qt = 0; qt < QT; ++qt) oz[qt][ns] = mfma_16(zf, p[qt], oz[qt][ns], f16_t());
@@ -779,8 +799,13 @@ __global__ __launch_bounds__(64 * rows4_waves(DP)) __attribute__((amdgpu_waves_p
             for (int x = 0; x < XT; ++x) {
                 const float f = (x & 1 ? 0x1p18f : 0x1p22f);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) o[qt][x][i] = fmaf(o[qt][x][i], f, -oz[qt][x / VW][0]);
+                for (int i = 0; i < 4; ++i) {
+                    o[qt][x][i] = fmaf(o[qt][x][i], f, -oz[qt][x / VW][0]);
+                    if (x / VW > 0) o[qt][x][i] *= 1.f / more[qt];      // (a power of two)
+                }
             }
+#pragma unroll
+        for (int qt = 0; qt < QT; ++qt) m[qt] -= lift[qt][0];
     }
 
     // the ring is done with: nothing is on its way into LDS any more, from no wave

@@ -521,8 +521,12 @@ typedef struct qmm_kv4_attention_args {
  * kv_len - n + i) sees the keys j up to its own with j > its position - window or
  * j < sinks.  Products on f16 MFMA with fp32 sums whatever q's type: keys and
  * values are exact in f16 (with a scale of more than 7 bits off by half a step), a
- * bf16 row of q is brought there by a power of two; softmax in fp32, probabilities
- * rounded once to fp16.  Keys that some row of the sequence sees must have finite
+ * bf16 row of q is brought there by a power of two; softmax in fp32, probabilities p
+ * rounded once to fp16, by half a step or 2^-36 of the row's largest.  With up to 32
+ * rows a key head (of G = 64 and D = 128: 16) and D = G = 64, D = 128 with G 64 or 128,
+ * or D = 256 with G 128, it is p s that is rounded so, of the largest in the row and
+ * group, and codes and zero-points are summed apart: roundings of fp32 are then those of
+ * sum p s (code + z).  Keys that some row of the sequence sees must have finite
  * scales.  Errors: as qmm_paged_attention, and the cache's as in qmm_kv4_append. */
 qmm_status qmm_kv4_attention(const qmm_kv4_attention_args *args, qmm_stream stream);
 

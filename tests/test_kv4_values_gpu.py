@@ -1,0 +1,124 @@
+"""Values at which the calls around a cache of 4-bit codes can go wrong without a fault: keys and values of very
+different sizes side by side, sums that cancel.  On an MI355X.
+
+Tolerances count roundings, as in test_kv4_gpu.py.
+"""
+import math
+
+import pytest
+import torch
+
+from test_kv4_gpu import BF16, DEV, F16, SEQS, U, Paged, _announce, close, decoded, encoded, gen, q  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------ attention: sizes far apart --
+def refill(c, k=None, v=None):
+    """k and v, [L, Hkv, D] for each sequence, into the pages of c; keeps their codes, scales and zero-points."""
+    c.parts = []
+    for b, (_, L) in enumerate(c.seqs):
+        sides = []
+        for x, codes, scale, now in ((k, c.cache.k, c.cache.k_scale, c.k), (v, c.cache.v, c.cache.v_scale, c.v)):
+            G = c.D // scale.shape[3]
+            n, s, z = encoded(now[b] if x is None else x[b].double(), G)
+            packed, sz = (n[..., 0::2] | n[..., 1::2] << 4).to(torch.uint8), torch.stack((s, z), -1).half()
+            for p in range(-(-L // c.page)):
+                at, lo, hi = int(c.table[b, p]), p * c.page, min(L, (p + 1) * c.page)
+                if at >= 0:
+                    codes[at, :, :hi - lo] = packed[lo:hi].transpose(0, 1)
+                    scale[at, :, :hi - lo] = sz[lo:hi].transpose(0, 1)
+            now[b] = decoded(packed, sz)
+            sides.append((n.double().unflatten(-1, (-1, G)), sz[..., 0].double(), sz[..., 1].double()))      # s and z as they are held
+        c.parts.append(sides)
+
+
+def check(c, out, lse, fed):
+    """fed: the codes meet the products as they are, scales and zero-points apart; else as (code - z) s."""
+    t = 0
+    for b, (n, L) in enumerate(c.seqs):
+        if n == 0 or L == 0:
+            t += n
+            continue
+        qs = c.q[t:t + n].double().unflatten(1, (c.Hkv, c.g))
+        got, gl = out[t:t + n].double().unflatten(1, (c.Hkv, c.g)), lse[t:t + n].double().unflatten(1, (c.Hkv, c.g))
+        t += n
+        pos, key = torch.arange(L - n, L, device=DEV)[:, None], torch.arange(L, device=DEV)
+        mask = (key <= pos).repeat_interleave(c.g, 0)
+        (kn, ks, kz), (vn, vs, vz) = c.parts[b]
+        G = kn.shape[-1]
+        for h in range(c.Hkv):
+            qh, k, v = qs[:, h].reshape(n * c.g, c.D), c.k[b][:, h], c.v[b][:, h]
+            x = torch.where(mask, qh @ k.T * c.scale, -math.inf)
+            l = torch.logsumexp(x, 1)
+            p = torch.exp(x - l[:, None])
+            # a score: sums of q c and of q, q on a grid of 6 bits, are exact where they meet so; times s, added, times the
+            # scale and in the exponent some ten roundings.  Else D products (code - z) s q summed in fp32.
+            size = ((kn[:, h] + kz[:, h, :, None]) * ks[:, h, :, None]).flatten(1)
+            dx = ((12 if fed else c.D + 8) * 2.0 ** -24 * c.scale * torch.where(mask, qh.abs() @ size.T, 0.0)).amax(1, keepdim=True)
+            rel = 2 * dx + (L + 64) * 2.0 ** -24 + 2.0 ** -20
+            o, each = p @ v, p @ v.abs()
+            bound = (U[F16] + rel) * each + U[c.dtype] * o.abs() + (2.0 ** -25 if c.dtype == F16 else 0.0)
+            if fed:
+                # weights p s in fp16: half a step, or 2^-36 of the row's largest in the group, times up to 15 steps;
+                # sums of codes and of zero-points in fp32, each for itself
+                w = p[:, :, None] * vs[:, h]                                       # [rows, keys, groups]
+                tiny = 2.0 ** -36 * 15 * mask.sum(1)[:, None] * w.amax(1)
+                step = torch.einsum("rjg,jge->rge", w, vn[:, h] + vz[:, h, :, None])
+                bound = bound + ((L + 64) * 2.0 ** -24 * step + tiny[..., None]).flatten(1)
+            else:
+                bound = bound + 2.0 ** -36 * p.amax(1, keepdim=True) * (mask.double() @ v.abs())
+            close(got[:, h].reshape(n * c.g, c.D), o, bound)
+            close(gl[:, h].reshape(-1), l, rel[:, 0] + 2.0 ** -21 * l.abs())
+
+
+def sizes(kind, L, Hkv, D, G, g):
+    """(values' exponents [L, Hkv, D / G], what is added to the keys' first 16 elements [L])."""
+    e, up = torch.zeros(L, Hkv, D // G, device=DEV), torch.zeros(L, device=DEV)
+    at = torch.arange(L, device=DEV)
+    if kind == "keys":           # any size beside any other
+        e = torch.randint(-11, 14, e.shape, generator=g, device=DEV).float()
+    elif kind == "groups":       # one group small, the next large
+        e[..., 0::2], e[..., 1::2] = -11, 13
+    elif kind == "groups_down":
+        e[..., 0::2], e[..., 1::2] = 13, -11
+    elif kind == "rare":         # a key in 61 is large, and gets next to no weight
+        e -= 11
+        e[at % 61 == 17], up[at % 61 == 17] = 13, -4.5
+    elif kind == "early":        # large values first, then keys that take all weight from them
+        e -= 11
+        e[:L // 3], up[L // 3:] = 13, 5.0
+    elif kind == "late":
+        e -= 11
+        e[L // 2:], up[L // 2:] = 13, -5.0
+    elif kind == "block":        # in one wave's block alone
+        e -= 11
+        e[(at >= 32) & (at < 64)] = 13
+    return e, up
+
+
+FED = [(128, 128), (128, 64), (64, 64), (256, 128)]
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("kind", ["keys", "groups", "groups_down", "rare", "early", "late", "block"])
+@pytest.mark.parametrize("D,G", FED + [(128, 32), (192, 64), (256, 64)])
+def test_attention_of_values_of_very_different_sizes(q, D, G, kind, dtype):
+    """Scales of values some 2^24 apart, between keys, groups, blocks, waves and shares: a small value keeps its bits
+    wherever no large one has weight beside it in its group."""
+    for seqs, Hq, Hkv, page in (([(1, 700), (1, 33), (2, 130)], 4, 2, 16), ([(3, 400), (1, 90)], 8, 1, 3), ([(1, 500), (2, 64)], 4, 2, 1),
+                                ([(70, 300), (1, 200)], 4, 2, 16), ([(1, 9000)], 4, 2, 16)):
+        c = Paged(q, seqs, Hq, Hkv, D, G, page, dtype, seed=D + G)
+        g = gen(D + page)
+        c.q.copy_((c.q.clamp(-3.9, 3.9) * 4).round() / 4)
+        c.q[..., :16] += 4.0
+        k, v = [], []
+        for b, (_, L) in enumerate(seqs):
+            e, up = sizes(kind, L, Hkv, D, G, g)
+            k.append(c.k[b].clone())
+            k[b][..., :16] += up[:, None, None]
+            v.append(c.v[b] * torch.exp2(e.double()).repeat_interleave(G, 2))
+        refill(c, k, v)
+        out, lse = c.run(q)
+        rows = max(n for n, _ in seqs) * Hq // Hkv
+        check(c, out, lse, (D, G) in FED and rows <= (16 if (D, G) == (128, 64) else 32))
