@@ -159,9 +159,14 @@ __device__ __forceinline__ int4_t values8(uint32_t w, const Zero &z)
 }
 
 // The codes of a dword, in codes' order, as f16 without an exponent: c 2^-22, c 2^-18, c 2^-22, c 2^-18.
-// (The matrix instruction adds products as if such leading zeros were digits: with c 2^-24, one
-// operation less for 8 codes, 32 products were off by up to 2^-18.7 of the sum of their sizes, with c 2^-20
-// by 2^-24.1, as with numbers of full precision.)
+// The matrix instruction aligns products as if such leading zeros were digits, so its sums lose bits with them.  Worst
+// and root mean square of 32 products, as parts of the sum of their sizes, for codes of any size and codes of 1:
+//     c 2^-24           2^-18.5  2^-21.3      2^-15.7  2^-18.6
+//     c 2^-22, 2^-18    2^-21.6  2^-24.8      2^-18.4  2^-21.8
+//     c 2^-20           2^-22.6  2^-26.0      2^-21.2  2^-24.6
+//     c                 2^-23.4  2^-26.0      2^-24.8  2^-29.7
+// 32 roundings of fp32 in a row are 2^-19 at most.  The first takes one operation less for 8 codes, the third one more
+// (64 users of up to 8192 keys, G 64: 71.5 us, the third's 74; 4 of up to 131071, G 128: 97.2 and 98.7).
 __device__ __forceinline__ int4_t places4(uint32_t w)
 {
     const uint32_t low = w << 2, high = w >> 6;
@@ -463,10 +468,12 @@ __global__ __launch_bounds__(64 * rows4_waves(DP)) __attribute__((amdgpu_waves_p
         if constexpr (DEFER) {
 #pragma unroll
             for (int ns = 0; ns < NS; ++ns) {
-                float4_t sum = float4_t{0.f, 0.f, 0.f, 0.f};      // of a key whose codes are all 1
+                // of a key whose codes are all 1; as 1 and 16, which keep all bits (z times it is taken off)
+                float4_t sum = float4_t{0.f, 0.f, 0.f, 0.f};
+                const int4_t ones = int4_t{0x3c003c00, 0x4c004c00, 0x3c003c00, 0x4c004c00};
 #pragma unroll
-                for (int w = 0; w < KW; ++w) sum = mfma_16(places4(0x11111111u), q[qt][KW * ns + w], sum, f16_t());
-                qsum[qt][ns] = sum[0];
+                for (int w = 0; w < KW; ++w) sum = mfma_16(ones, q[qt][KW * ns + w], sum, f16_t());
+                qsum[qt][ns] = sum[0] * 0x1p-22f;
             }
         }
     }

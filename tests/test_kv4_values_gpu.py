@@ -122,3 +122,40 @@ def test_attention_of_values_of_very_different_sizes(q, D, G, kind, dtype):
         out, lse = c.run(q)
         rows = max(n for n, _ in seqs) * Hq // Hkv
         check(c, out, lse, (D, G) in FED and rows <= (16 if (D, G) == (128, 64) else 32))
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("kind", ["ones", "minus", "mixed", "any"])
+@pytest.mark.parametrize("D,G,g", [(64, 64, 16), (64, 64, 32), (128, 64, 16), (128, 128, 16), (128, 128, 32), (256, 128, 16), (128, 32, 16), (96, 32, 32), (256, 64, 8)])
+def test_scores_are_sums_of_fp32(q, D, G, g, kind, dtype):
+    """One key a sequence: its log sum is its score.  Codes of 1 beside one of 15 in their group, and zero-points of 15, where sums of
+    s c, and of z, are far larger than what they differ by.
+
+    32 products of codes of 1 may be off by 2^-18.4 of the sum of their sizes (49 of 2^-24; root mean square 2^-21.6), their sums add a
+    rounding each, twelve more are s, z, the scale, the exponent and the logarithm, with 36 at most in the exponent (half a step
+    there 2^-19).  Taken together the errors are root mean squares: of the products 2^-21.6, and of twelve roundings in any
+    direction 2^-23."""
+    B, Hkv = 200, 2
+    c = Paged(q, [(1, 1)] * B, g * Hkv, Hkv, D, G, 16, dtype, seed=D + G + g)
+    r = gen(g)
+    k = torch.ones(B, 1, Hkv, D, device=DEV)
+    if kind == "mixed":
+        k = torch.randint(-1, 2, k.shape, generator=r, device=DEV).float()
+    elif kind == "any":
+        k = torch.randint(0, 16, k.shape, generator=r, device=DEV).float()
+    k.unflatten(-1, (-1, G))[..., 5] = 15.0
+    if kind == "minus":
+        k = -k
+    refill(c, list(k))
+    _, lse = c.run(q)
+    square = 0.0
+    for b in range(B):
+        kn, ks, kz = (x[0] for x in c.parts[b][0])
+        qs = c.q[b].double().unflatten(0, (Hkv, g))
+        size = ((kn + kz[..., None]) * ks[..., None]).flatten(1)
+        want = torch.einsum("hgd,hd->hg", qs, c.k[b][0]) * c.scale
+        most = torch.einsum("hgd,hd->hg", qs.abs(), size) * c.scale
+        got = lse[b].unflatten(0, (Hkv, g))
+        close(got, want, (49 + D // 32 + 12) * 2.0 ** -24 * most + 2.0 ** -19)
+        square += float(((got.double() - want) / (most + 0.25)).square().mean()) / B
+    assert math.sqrt(square) < 2.0 ** -21
