@@ -105,7 +105,8 @@ __device__ __forceinline__ double quotient(double x, double s, double inv)
 // once.  As in append.hip a lane owns two vectors of 8 elements that turn
 // together (past rot two that stay), of HP heads of one token, so that cos and
 // sin are read once for them; U lanes own a row, and the sum of its squares goes
-// round them.  8192 tokens of 64 + 8 heads of 128, bf16: 59 us, 5.2 TB/s (a large copy the same); 1 token 4.2, the call.
+// round them (in fp64 where a row of bf16 has squares beyond fp32).  8192 tokens of 64 + 8
+// heads of 128, bf16: 59 us, 5.2 TB/s (a large copy the same); 1 token 4.2, the call.
 // ---------------------------------------------------------------------------
 template <typename S, bool PAIRS, bool VEC, int U, int HP>
 __device__ __forceinline__ void turn_rows(const HeadsArgs &a, int block, int groups)
@@ -161,7 +162,24 @@ __device__ __forceinline__ void turn_rows(const HeadsArgs &a, int block, int gro
             for (int e = 0; e < 8; ++e) sum += x[0][e] * x[0][e] + x[1][e] * x[1][e];
 #pragma unroll
             for (int m = 1; m < U; m <<= 1) sum += __shfl_xor(sum, m);
-            const float r = 1.f / sqrtf(sum / (float)a.D + a.eps);
+            const float mean = sum / (float)a.D + a.eps;
+            float r = 1.f / sqrtf(mean);
+            if constexpr (__is_same(S, bf16_t)) {
+                if (__any(!(mean > 0x1p-100f && mean < 0x1p112f))) {      // squares outside fp32's range, or rows of zeros
+                    double far = 0.0;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) far += (double)x[0][e] * (double)x[0][e] + (double)x[1][e] * (double)x[1][e];
+#pragma unroll
+                    for (int m = 1; m < U; m <<= 1) far += __shfl_xor(far, m);
+                    far = 1.0 / sqrt(far / (double)a.D + (double)a.eps);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        x[0][e] = (float)((double)x[0][e] * far);
+                        x[1][e] = (float)((double)x[1][e] * far);
+                    }
+                    r = 1.f;
+                }
+            }
             if (live) {
                 S wa[8], wb[8];
                 load_weights(w + first, wa);

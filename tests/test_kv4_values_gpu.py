@@ -8,7 +8,7 @@ import math
 import pytest
 import torch
 
-from test_kv4_gpu import BF16, DEV, F16, SEQS, U, Paged, _announce, close, decoded, encoded, gen, q  # noqa: F401
+from test_kv4_gpu import BF16, DEV, F16, U, Paged, _announce, close, decoded, encoded, gen, heads, norm_bound, place, q, rope_table, same, turned  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -159,3 +159,26 @@ def test_scores_are_sums_of_fp32(q, D, G, g, kind, dtype):
         close(got, want, (49 + D // 32 + 12) * 2.0 ** -24 * most + 2.0 ** -19)
         square += float(((got.double() - want) / (most + 0.25)).square().mean()) / B
     assert math.sqrt(square) < 2.0 ** -21
+
+
+# ------------------------------------------------------------------- norms --
+@pytest.mark.parametrize("pairs", [False, True], ids=["halves", "pairs"])
+@pytest.mark.parametrize("D,rot", [(128, 128), (80, 48), (256, 0)])
+@pytest.mark.parametrize("size,eps", [(1e20, 1e-5), (1e20, 0.0), (3e37, 1e-5), (1e-25, 0.0), (1e-37, 0.0), (1e18, 1e-5), (1e-3, 1e-5)])
+def test_norms_of_rows_of_any_size(q, size, eps, D, rot, pairs):
+    """Squares beyond fp32 on either side: the norm is the formula's all the same, here and where k goes to a cache; rows
+    of other sizes and of zeros beside them."""
+    g = gen(D)
+    xq, xk, v = heads(70, 5, 2, D, BF16, g, size=size)
+    xq[3], xk[11] = torch.randn(5, D, generator=g, device=DEV).to(BF16), torch.randn(2, D, generator=g, device=DEV).to(BF16)
+    if eps:
+        xq[4, 2] = 0
+    w, u = ((1 + 0.3 * torch.randn(D, generator=g, device=DEV)).to(BF16) for _ in range(2))
+    table, pos = (rope_table(100, rot), torch.arange(70, device=DEV, dtype=torch.int32)) if rot else (None, None)
+    yq, yk = q.qk_norm(xq, xk, w, u, eps, pos, table, pairs)
+    for x, weight, y in ((xq, w, yq), (xk, u, yk)):
+        want, most = turned(x, weight, eps, pos, table, pairs)
+        close(y, want, norm_bound(want, most, D, BF16))
+    if D % 32 == 0:
+        c = q.kv4_cache(8, 2, 16, D)
+        assert same(q.kv4_append(xq, xk, v, c, place(70, 8, 16, g), pos, table, pairs, w, u, eps), yq)
