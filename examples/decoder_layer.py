@@ -6,7 +6,8 @@ Each user's prompt runs through the layer in one call (chunks of different lengt
 then all users decode a token at a time, the step captured in a graph.  Projections are
 `linear` calls with their epilogues, positions and the cache `kv_append`, attention
 `paged_attention` (with `--cache-bits 4` `kv4_append` and `kv4_attention`); only the norm is torch's.  Weights are random, quantised by `quantize`.
-The last step's outputs are compared with the same layer in fp32 on the dequantised weights.
+The last step's outputs are compared with the same layer in fp32 on the dequantised weights, with a cache
+of 4 bits on the keys and values that it stands for.
 """
 import argparse
 import os
@@ -65,14 +66,14 @@ class Layer:
         h = norm(x)
         return self.down(self.gate(h, act="silu", mul=self.up(h)), residual=x)
 
-    def reference(self, x, rope):
-        """One user's whole sequence in fp32."""
+    def reference(self, x, rope, cached=None):
+        """One user's whole sequence in fp32; `cached`: keys and values to take instead of its own."""
         L, rot = x.shape[0], rope.shape[1]
         x = x.float()
         q, k, v = self.split(norm(x).float() @ self.qkv.dense())
         c, s = rope[:L, None, :rot // 2], rope[:L, None, rot // 2:]
         q, k = (torch.cat((t[..., :rot // 2] * c - t[..., rot // 2:] * s, t[..., rot // 2:] * c + t[..., :rot // 2] * s), -1) for t in (q, k))
-        k, v = (t.repeat_interleave(self.Hq // self.Hkv, 1) for t in (k, v))
+        k, v = (t.float().repeat_interleave(self.Hq // self.Hkv, 1) for t in cached or (k, v))
         score = torch.stack([q[:, h] @ k[:, h].t() for h in range(self.Hq)]) * self.D ** -0.5
         p = torch.softmax(score.masked_fill(torch.ones(L, L, device=x.device, dtype=torch.bool).triu(1), -torch.inf), -1)
         x = x + torch.stack([p[h] @ v[:, h] for h in range(self.Hq)], 1).flatten(1) @ self.o.dense()
@@ -137,7 +138,8 @@ def run(hidden=4096, heads=32, kv_heads=8, head_dim=128, inner=14336, users=16, 
         torch.cuda.synchronize()
         spent += time.perf_counter() - t
     u = users // 2
-    want = layer.reference(tokens[u], rope)[-1]
+    held = qmm.kv4_read(cache, slots_of(u, torch.arange(lens[u] + steps, device=dev))) if cache_bits == 4 else None
+    want = layer.reference(tokens[u], rope, held)[-1]
     error = float((out[u].float() - want).norm() / want.norm())
     return spent / max(1, steps - 1) * 1e6, error
 

@@ -3,7 +3,9 @@ different sizes side by side, sums that cancel.  On an MI355X.
 
 Tolerances count roundings, as in test_kv4_gpu.py.
 """
+import importlib.util
 import math
+import os
 
 import pytest
 import torch
@@ -182,3 +184,16 @@ def test_norms_of_rows_of_any_size(q, size, eps, D, rot, pairs):
     if D % 32 == 0:
         c = q.kv4_cache(8, 2, 16, D)
         assert same(q.kv4_append(xq, xk, v, c, place(70, 8, 16, g), pos, table, pairs, w, u, eps), yq)
+
+
+# ------------------------------------------------------------ run together --
+def test_decoder_layer_example_on_its_cache(q):
+    """The example's last output against the layer in fp32 on what the cache of 4 bits holds: the roundings of its 16-bit
+    form but for those of k and v, some ten of 2^-11 in a row, whose root sum of squares stays below 2^-8."""
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "decoder_layer.py")
+    spec = importlib.util.spec_from_file_location("decoder_layer_4_values", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    for users, prompt, steps, page in ((3, 75, 6, 16), (1, 1, 3, 1), (5, 300, 2, 64)):
+        _, error = example.run(hidden=512, heads=8, kv_heads=2, head_dim=64, inner=1024, users=users, prompt=prompt, steps=steps, page=page, cache_bits=4)
+        assert error < 2.0 ** -8
