@@ -10,7 +10,7 @@ import os
 import pytest
 import torch
 
-from test_kv4_gpu import BF16, DEV, F16, U, Paged, _announce, close, decoded, encoded, gen, heads, norm_bound, place, q, rope_table, same, turned  # noqa: F401
+from test_kv4_gpu import BF16, DEV, F16, U, Paged, _announce, check_stored, close, decoded, encoded, gen, heads, norm_bound, place, q, rope_table, same, turned  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -197,3 +197,76 @@ def test_decoder_layer_example_on_its_cache(q):
     for users, prompt, steps, page in ((3, 75, 6, 16), (1, 1, 3, 1), (5, 300, 2, 64)):
         _, error = example.run(hidden=512, heads=8, kv_heads=2, head_dim=64, inner=1024, users=users, prompt=prompt, steps=steps, page=page, cache_bits=4)
         assert error < 2.0 ** -8
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("D,G", [(128, 64), (128, 32), (64, 64)])
+def test_cache_in_4_bits_beside_one_in_16_of_its_type(q, D, G, dtype):
+    """What the cache reads back as, in a 16-bit cache of the same type at the same shuffled places, gives the same attention.
+
+    Each side rounds its probabilities (4 bits: to fp16, 16 bits: to dtype) and its output, and bf16 rounds the keys and
+    values it is handed; scores then differ by 2^-8 of the sum of |q k| in bf16."""
+    g = gen(D + G)
+    Hq, Hkv, page, L = 8, 2, 16, 300
+    xq, k, v = heads(L, Hq, Hkv, D, dtype, g)
+    w, table = (1 + 0.2 * torch.randn(D, generator=g, device=DEV)).to(dtype), rope_table(L, D)
+    pos, ids = torch.arange(L, device=DEV, dtype=torch.int32), torch.randperm(23, generator=g, device=DEV)
+    at = torch.arange(L, device=DEV)
+    slots = ids[at // page] * page + at % page
+    c = q.kv4_cache(23, Hkv, page, D, G)
+    order = torch.randperm(L, generator=g, device=DEV)              # tokens come in any order
+    y = torch.empty(L, Hq, D, device=DEV, dtype=dtype)
+    y[order] = q.kv4_append(xq[order], k[order], v[order], c, slots[order], pos[order], table, q_norm=w, k_norm=w)
+    held = q.kv4_read(c, slots, dtype)
+    exact = [t.double() for t in q.kv4_read(c, slots)]              # fp16 holds them as they are
+    k16, v16 = (torch.zeros(23, Hkv, page, D, device=DEV, dtype=dtype) for _ in range(2))
+    q.kv_append(None, *held, k16, v16, slots)
+    more = 0.0 if dtype == F16 else U[BF16]
+    pages = ids[:19].to(torch.int32)[None].contiguous()
+    for n in (1, 5, L):
+        args = (pages, torch.tensor([0, n], dtype=torch.int32, device=DEV), torch.tensor([L], dtype=torch.int32, device=DEV), n, L)
+        got, want = q.kv4_attention(y[L - n:], c, *args), q.paged_attention(y[L - n:], k16, v16, *args)
+        # the same in 64 bits, for the sizes that the roundings go by
+        rows = y[L - n:].double().unflatten(1, (Hkv, -1)).transpose(0, 1).transpose(1, 2)                      # [Hkv, g, n, D]
+        seen = torch.arange(L, device=DEV) <= torch.arange(L - n, L, device=DEV)[:, None]
+        x = torch.where(seen, rows @ exact[0].permute(1, 2, 0)[:, None].contiguous() * D ** -0.5, -math.inf)
+        dx = (rows.abs() @ exact[0].abs().permute(1, 2, 0)[:, None].contiguous() * D ** -0.5 * seen).amax(-1, keepdim=True) * (more + (D + 8) * 2.0 ** -24)
+        p = torch.softmax(x, -1)
+        size = (p @ exact[1].abs().transpose(0, 1)[:, None].contiguous()) * (U[F16] + U[dtype] + more + torch.exp(2 * dx) - 1 + (L + 64) * 2.0 ** -23)
+        o = (p @ exact[1].transpose(0, 1)[:, None].contiguous()).abs()
+        bound = (size * (1 + 2.0 ** -6) + 2 * U[dtype] * o + 2.0 ** -24).transpose(1, 2).transpose(0, 1).flatten(1, 2)
+        close(got, want.double(), bound)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("G", [32, 64, 128])
+def test_append_scales_halfway(q, dtype, G):
+    """(hi - lo) / 15 halfway between two scales of 7 bits, to the even one, in numbers that bf16 holds too; a step of the
+    range to either side."""
+    rows = []
+    for n in (129, 131, 133, 253, 255, 187):                       # twice a scale of 7 bits, and one: odd
+        hi, lo = 8 * n, 7 * n                                       # hi + lo = 15 n
+        fits = [(a, 15 * n - a) for a in range(hi, 15 * n) if all(float(torch.tensor(float(x)).to(BF16)) == x for x in (a, 15 * n - a))]
+        assert fits, (n, hi, lo)
+        for a, b in (fits[0], fits[len(fits) // 2], fits[-1]):
+            for e in (-7, 0, 3):
+                rows.append(torch.zeros(G, dtype=torch.float64))
+                rows[-1][:4] = torch.tensor([float(a), -float(b), a / 2.0, -b / 4.0], dtype=torch.float64) * 2.0 ** e
+                for x, y in ((a * (1 + 2.0 ** -7), b), (a, b * (1 + 2.0 ** -7))):      # not halfway any more
+                    rows.append(torch.zeros(G, dtype=torch.float64))
+                    rows[-1][:2] = torch.tensor([x, -y], dtype=torch.float64) * 2.0 ** e
+    x = torch.stack(rows)
+    ties = x[::3]
+    assert torch.equal(ties[:, :2].to(dtype).double(), ties[:, :2]) and torch.equal((ties[:, 0] - ties[:, 1]) / 15 * 2, (ties[:, 0] - ties[:, 1]) * 2 / 15)
+    x = x.to(dtype).to(DEV)[:, None]
+    T = x.shape[0]
+    c = q.kv4_cache(1, 1, T, G, G)
+    before, slots = q.KV4Cache(*(t.clone() for t in c)), torch.arange(T, device=DEV)
+    q.kv4_append(None, x, x, c, slots)
+    check_stored(c, before, x.double(), x.double(), slots, G)
+    for i in range(0, T, 3):                                        # by whole numbers: the even one of n / 2 - 1/2, n / 2 + 1/2
+        n = round(float((x[i].double().max() - x[i].double().min()) / 15 * 2.0 ** 20))
+        top = n >> (n.bit_length() - 8)
+        assert top % 2 == 1 and n == top << (n.bit_length() - 8)
+        even = (top // 2 + (top // 2) % 2) << (n.bit_length() - 7)
+        assert float(c.k_scale[0, 0, i, 0, 0]) == even / 2.0 ** 20, i
