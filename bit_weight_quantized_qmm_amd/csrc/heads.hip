@@ -33,7 +33,7 @@ constexpr float KV4_TOP = 57344.f;
 
 // Rows are read once and written once: neither leaves a trace in the caches (8192 tokens of
 // 64 heads of 128 normed and turned: 57 us with the default policy, 54 so; with k and v into the cache
-// 76 and 72).
+// and read back from it 76 and 72).
 template <typename S, bool VEC>
 __device__ __forceinline__ void load8(const S *p, S (&e)[8])
 {
@@ -225,7 +225,8 @@ __device__ __forceinline__ void turn_rows(const HeadsArgs &a, int block, int gro
 // heads, k and v of each, LN lanes a token's row; range and zero-point go round the G / 8
 // lanes of a group.  A workgroup's 256 / LN tokens stand side by side in a page's head.  Its
 // waves wait for memory (one row a wave: 31 us for 8192 tokens of 2 x 8 heads, k and v of two
-// heads 26; few tokens: see heads_pick), so they run between q's, which is bound by memory: 72 to 78 us for both (cards differ), 54 for q.
+// heads 26; few tokens: see heads_pick), so they run between q's, which is bound by memory: 68 us
+// for both, 54 for q's 64 heads alone (4.6 TB/s; on inputs that the last-level cache holds 64).
 //
 // k is normed, turned and mapped in fp32 first, with a bound of what its roundings may have
 // moved its elements by; where that leaves a scale, a zero-point or a code in doubt
@@ -254,8 +255,9 @@ __device__ __forceinline__ float round_lanes(float x, int span, F f)
 }
 
 // The row's elements after norm and rotation in fp32.  Returns a bound of what its roundings move any of
-// this lane's 8 by: a dozen of 2^-24, and half of the sum of squares' D 2^-24; infinity where that sum
-// leaves fp32's range.
+// this lane's 8 by, 16 of 2^-24 of |x| + |y|; infinity where the sum of squares leaves fp32's range.  They are 12.5 at
+// most: 8 + log2(LN) <= 13 of the sum, as the lanes add it (eight in a row, then a tree: another order needs another
+// bound), a division and eps, halved by the root; root, reciprocal; 2 of the rotation; the product.  (w x is exact.)
 template <int LN, typename S>
 __device__ __forceinline__ float turned8(const HeadsArgs &a, const Row4<S> &r, float (&x)[8])
 {
