@@ -391,7 +391,8 @@ def kv4_attention(q, cache, page_table, cu_q, kv_lens, max_q: int, max_kv: int, 
     """paged_attention over a cache of 4-bit codes.
 
     window > 0: a row sees its last `window` keys and, of those before them, the sequence's first
-    `sinks`.  The other arguments as in paged_attention."""
+    `sinks`.  The other arguments as in paged_attention.  A token with NaN gives NaN to the rows that see it,
+    and to no others."""
     return _binding.kv4_attention(q, cache, page_table, cu_q, kv_lens, max_q, max_kv, scale, window, sinks, out, lse)
 
 

@@ -69,6 +69,9 @@ __device__ __forceinline__ bool row_sees(const Attend4Args &a, int b, const Rang
     return sees_key(a, b, lo, hi) || sees_key(a, b, 0, min(min(a.sinks, lo), hi));
 }
 
+// whether a scale (and its zero-point) has NaN for a scale
+__device__ __forceinline__ bool is_nan(uint32_t sz) { return (sz & 0x7fffu) > 0x7c00u; }
+
 // What turns a product into a base-2 exponent: positive, or NaN as it is given.
 __device__ __forceinline__ float above_zero(float x) { return x < 1e-37f ? 1e-37f : x; }
 
@@ -477,6 +480,11 @@ __global__ __launch_bounds__(64 * rows4_waves(DP)) __attribute__((amdgpu_waves_p
             }
         }
     }
+    // rows of different tokens see different keys: a value of NaN is for those that see it
+    const bool alike = a.by_g(rb * a.rows) == a.by_g(rb * a.rows + nrow - 1);
+    uint32_t spoilt[QT];       // chunk x, place i of 16: bit 16 x + i
+#pragma unroll
+    for (int qt = 0; qt < QT; ++qt) spoilt[qt] = 0;
     // keys that every row of the block sees: [all_lo, all_hi) (and those below the sinks)
     const int all_hi = min(kr.hi, kr.L - kr.n + a.by_g(rb * a.rows) + 1);
     const int all_lo = a.window > 0 ? kr.hi - a.window : 0;
@@ -601,7 +609,7 @@ __global__ __launch_bounds__(64 * rows4_waves(DP)) __attribute__((amdgpu_waves_p
 
         // loads of K n + 1, V n + 1 and K n + 2 stay on their way
         wait_loads<3 * FETCHES>();
-        uint32_t vd[2][VC][VK], vsd[2][4][DEFER ? NS : VC];
+        uint32_t vd[2][VC][VK], vsd[2][4][VC];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             const uint8_t *p = vread + in_ring + t * HALF;
@@ -666,7 +674,24 @@ __global__ __launch_bounds__(64 * rows4_waves(DP)) __attribute__((amdgpu_waves_p
                     // values that no row sees may hold anything: they meet p = 0 as zeros
                     const uint32_t m = (uint32_t)((some << (31 - i)) >> 31);
 #pragma unroll
-                    for (int x = 0; x < (DEFER ? NS : VC); ++x) vsd[t][i][x] &= m;
+                    for (int x = 0; x < VC; ++x) vsd[t][i][x] &= m;
+                }
+                if (!alike) {
+                    bool any = false;
+#pragma unroll
+                    for (int e = 0; e < 4 * VC; ++e) any = any || is_nan(vsd[t][e / VC][e % VC]);
+                    if (__any(any)) {       // such a value counts as 0, and is remembered
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int x = 0; x < VC; ++x) {
+                                const bool nan = is_nan(vsd[t][i][x]);
+                                const uint32_t at = DEFER ? (nan ? 0xffffu : 0u) : (uint32_t)(__ballot(nan) >> (16 * g)) & 0xffffu;
+#pragma unroll
+                                for (int qt = 0; qt < QT; ++qt) spoilt[qt] |= mine[qt] >> i & 1 ? at << (16 * x) : 0u;
+                                vsd[t][i][x] = nan ? 0u : vsd[t][i][x];
+                            }
+                    }
                 }
             }
         }
@@ -813,6 +838,17 @@ __global__ __launch_bounds__(64 * rows4_waves(DP)) __attribute__((amdgpu_waves_p
             }
 #pragma unroll
         for (int qt = 0; qt < QT; ++qt) m[qt] -= lift[qt][0];
+    }
+
+#pragma unroll
+    for (int qt = 0; qt < QT; ++qt) {
+        if (!__any(spoilt[qt] != 0)) continue;
+        spoilt[qt] |= __shfl_xor(spoilt[qt], 16);
+        spoilt[qt] |= __shfl_xor(spoilt[qt], 32);
+#pragma unroll
+        for (int x = 0; x < XT; ++x)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[qt][x][i] = spoilt[qt] >> (16 * (x / VW) + 4 * g + i) & 1 ? NAN : o[qt][x][i];
     }
 
     // the ring is done with: nothing is on its way into LDS any more, from no wave
@@ -977,6 +1013,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DC <= 1
     constexpr int SLOTS = 2 * NW;
     int4_t *places = reinterpret_cast<int4_t *>(att_tiles + 4 * TILE);       // [SLOTS][KB][2]: codes of K low, high, of V; scales likewise
     int4_t *masks = places + 2 * SLOTS * KB;                                 // [SLOTS]: seen low, high, bad low, high
+    int *again = reinterpret_cast<int *>(masks + SLOTS);
     auto key_of = [&](int tile) { return key_at(kr, max(0, min(begin + KB * tile + (lane & (KB - 1)), end - 1))); };
     auto ids_of = [&](int tile) { return table[key_page(a, key_of(tile))]; };
     auto two = [](int64_t x, int64_t y) { return int4_t{(int)(uint32_t)x, (int)(x >> 32), (int)(uint32_t)y, (int)(y >> 32)}; };
@@ -1016,10 +1053,11 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DC <= 1
         vlive = uniform64(mk[0], mk[1]);
         hidden = uniform64(mk[2], mk[3]);
     };
+    uint64_t careful = 0;         // uniform, 0 or 1
     auto store_tile = [&](int buf) {
-        if (~vlive) {     // what no row sees may hold anything: it meets p = 0 as zeros
+        if (~vlive | careful) {     // what no row sees may hold anything: it meets p = 0 as zeros
 #pragma unroll
-            for (int n = 0; n < LN; ++n) vss[n] = (vlive >> (srow + SSTEP * n)) & 1 ? vss[n] : 0;
+            for (int n = 0; n < LN; ++n) vss[n] = (vlive >> (srow + SSTEP * n)) & 1 && !(careful && is_nan(vss[n])) ? vss[n] : 0;
         }
         const bool in = 8 * sp < a.D;
 #pragma unroll
@@ -1047,14 +1085,17 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DC <= 1
         }
     }
 
-    float m = -INFINITY, l = 0.f;
+    float m, l;
     float16v_t o[XT];
+    uint32_t spoilt = 0;          // groups in which this lane's row sees a value of NaN
+    const int tiles = (max(0, end - begin) + KB - 1) / KB;
+    if (tid == 0) *again = 0;
+anew:
+    m = -INFINITY, l = 0.f;
 #pragma unroll
     for (int x = 0; x < XT; ++x)
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[x][e] = 0.f;
-
-    const int tiles = (max(0, end - begin) + KB - 1) / KB;
     look_up(wave, ids_of(wave));
     int pid = ids_of(NW + wave);
     __syncthreads();
@@ -1110,11 +1151,18 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DC <= 1
                     __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
             }
             __builtin_amdgcn_sched_barrier(0);
-            if (v0 + KB > end || key0 + KB > wall_hi || (key0 < wall_lo && key0 + KB > kr.sk) || bad) {
+            if (v0 + KB > end || key0 + KB > wall_hi || (key0 < wall_lo && key0 + KB > kr.sk) || (bad | careful)) {
                 // element e of tile t is key key0 + 4 h + 32 t + e % 4 + 8 (e / 4) (v0 + KB > end with the last places alone: key >= vhi there)
                 const int to = min(vhi, key0 + end - v0) - key0 - 4 * h, from = vlo - key0 - 4 * h, sinks = kr.sk - key0 - 4 * h;
                 auto below = [](int n) { return n >= 64 ? ~uint64_t(0) : (uint64_t(1) << max(n, 0)) - 1; };      // keys before the n-th
                 const uint64_t mine = below(to) & (~below(from) | below(sinks)) & ~(bad >> (4 * h));
+                if (careful) {       // lane l: the scales of key l's values
+                    const int4_t as = places[2 * (tile % SLOTS * KB + (lane & (KB - 1))) + 1];
+                    for (int e = 0; e < a.D >> a.lg_G; ++e) {
+                        const uint64_t nan = __ballot(is_nan(*reinterpret_cast<const uint32_t *>(vsbase + off64(as[2], as[3]) + 4 * e)));
+                        spoilt |= ((KB == 64 ? nan : nan & 0xffffffffu) >> (4 * h) & mine) != 0 ? 1u << e : 0u;
+                    }
+                }
                 const int word[2] = {(int)(uint32_t)mine, (int)(uint32_t)(mine >> 32)};
 #pragma unroll
                 for (int t = 0; t < KT; ++t)
@@ -1164,7 +1212,24 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DC <= 1
         __syncthreads();
     }
 
+    // A value of NaN has reached every row of its block, also those that do not see it: once more, with such values as 0
+    // and with a note of who sees them.
+    if (!careful) {
+        float all = 0.f;
+#pragma unroll
+        for (int x = 0; x < XT; ++x)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) all += o[x][e];
+        if (__any(all != all && l == l) && lane == 0) *again = 1;
+        __syncthreads();
+        if (*again) {
+            careful = 1;
+            goto anew;
+        }
+    }
+
     l += __shfl_xor(l, 32);
+    spoilt |= __shfl_xor(spoilt, 32);
     if (!live) return;
     const bool none = l == 0.f && (a.splits > 1 || !row_sees(a, b, kr, i));
     const float tot = l > 0.f ? l : NAN, inv = 1.f / tot;
@@ -1179,7 +1244,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DC <= 1
             if (d >= a.D) continue;
             float4_t y;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) y[k] = none ? 0.f : o[x][e + k] * inv;
+            for (int k = 0; k < 4; ++k) y[k] = none ? 0.f : spoilt >> (d >> a.lg_G) & 1 ? NAN : o[x][e + k] * inv;
             if (a.splits == 1)
                 *reinterpret_cast<int2v_t *>(out + 2 * d) = int2v_t{pack2(y[0], y[1], tag), pack2(y[2], y[3], tag)};
             else
@@ -1342,7 +1407,7 @@ template <typename S, int DC>
 static hipError_t tiles4_go(const Attend4Args &a, hipStream_t st)
 {
     constexpr int DP = DC == 96 ? 128 : DC, NW = tiles4_waves(DP), KB = tiles4_keys(DP);
-    const size_t lds = (size_t)4 * KB * DP * 2 + 2 * NW * (2 * KB + 1) * 16;   // tiles, places, masks
+    const size_t lds = (size_t)4 * KB * DP * 2 + 2 * NW * (2 * KB + 1) * 16 + 16;   // tiles, places, masks, whether to go again
     const hipError_t e = allow_lds(&attend4_tiles_kernel<S, DC, NW>, lds);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((attend4_tiles_kernel<S, DC, NW>), dim3((unsigned)((int64_t)a.B * a.rblocks * a.Hkv * a.splits)), dim3(64 * NW), lds, st, a);

@@ -527,8 +527,9 @@ typedef struct qmm_kv4_attention_args {
  * rows a key head (of G = 64 and D = 128: 16) and D = G = 64, D = 128 with G 64 or 128,
  * or D = 256 with G 128, it is p s that is rounded so, of the largest in the row and
  * group, and codes and zero-points are summed apart: roundings of fp32 are then those of
- * sum p s (code + z).  Keys that some row of the sequence sees must have finite
- * scales.  Errors: as qmm_paged_attention, and the cache's as in qmm_kv4_append. */
+ * sum p s (code + z).  A key or value whose scale is NaN (of a token that held it) is
+ * NaN to the rows that see it, a value in its group alone; other rows are as
+ * without it.  Errors: as qmm_paged_attention, and the cache's as in qmm_kv4_append. */
 qmm_status qmm_kv4_attention(const qmm_kv4_attention_args *args, qmm_stream stream);
 
 /* Bytes of workspace that qmm_kv4_attention takes for these arguments (from the sizes

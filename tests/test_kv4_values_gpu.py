@@ -163,6 +163,51 @@ def test_scores_are_sums_of_fp32(q, D, G, g, kind, dtype):
     assert math.sqrt(square) < 2.0 ** -21
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (40, 7)])
+@pytest.mark.parametrize("D,G", FED + [(128, 32), (192, 64), (96, 32), (64, 32)])
+def test_values_of_nan_reach_the_rows_that_see_them(q, D, G, window, sinks, dtype):
+    """As the formula has it: a scale of NaN at a value makes its group NaN for the rows that see its key, and nothing else: the
+    other outputs are those of a value of zeros there.  Up to 32 rows a key head to the bit.  Beyond, the call masks more in its
+    second look, which moves the running maxima: fp32 roundings of exponents up to 32 (2^-19 each) and of sums, so
+    that each side's probabilities, and its outputs, may round by half a step the other way."""
+    for seqs, Hq, Hkv, page in (([(1, 90), (5, 200), (2, 33)], 4, 2, 16), ([(3, 150), (1, 20)], 8, 1, 3), ([(7, 64), (2, 2)], 2, 2, 1),
+                                ([(70, 300), (1, 120), (33, 33)], 4, 2, 16), ([(300, 420)], 2, 1, 7), ([(4, 6000), (1, 40)], 4, 2, 16), ([(20, 6000)], 4, 1, 16)):
+        c = Paged(q, seqs, Hq, Hkv, D, G, page, dtype, window=window, sinks=sinks, seed=D + G + page)
+        g, t = gen(page), 0
+        marks = []                                                  # (sequence, key, head, group)
+        for b, (n, L) in enumerate(seqs):
+            for j in {L - 1, L - 2, L - n, L - n // 2 - 1, 0, 5, L // 2, L - n - 30}:
+                if 0 <= j < L and (not window or j < sinks or j > L - n - window):
+                    marks.append((b, j, int(torch.randint(0, Hkv, (), generator=g, device=DEV)), int(torch.randint(0, D // G, (), generator=g, device=DEV))))
+        for b, j, h, e in marks:
+            c.cache.v_scale[c.table[b, j // page].long(), h, j % page, e] = 0
+        want, lse = c.run(q)
+        for b, j, h, e in marks:
+            c.cache.v_scale[c.table[b, j // page].long(), h, j % page, e, 0] = math.nan
+        got, lse2 = c.run(q)
+        want = want.clone().unflatten(1, (Hkv, -1)).unflatten(3, (-1, G))
+        exact = max(n for n, _ in seqs) * Hq // Hkv <= 32
+        assert torch.isfinite(want).all()
+        if exact:
+            assert same(lse, lse2)
+        close(lse2, lse.double(), 2.0 ** -18 + 2.0 ** -22 * lse.double().abs() + (max(L for _, L in seqs) + 64) * 2.0 ** -23)
+        for b, (n, L) in enumerate(seqs):
+            pos = torch.arange(L - n, L, device=DEV)
+            for b2, j, h, e in marks:
+                if b2 == b:
+                    sees = (pos >= j) & ((pos - window < j) | (j < sinks) if window else pos >= j)
+                    want[t:t + n, h, :, e][sees] = math.nan
+            t += n
+        want = want.flatten(3).flatten(1, 2)
+        assert torch.equal(got.isnan(), want.isnan())
+        got, want = got.nan_to_num(5.0), want.nan_to_num(5.0)
+        if exact:
+            assert same(got, want)
+        most = max(float(v.abs().max()) for v in c.v)
+        close(got, want.double(), (2 * U[F16] + 2.0 ** -17 + (max(L for _, L in seqs) + 64) * 2.0 ** -23) * most + 2 * U[dtype] * want.double().abs() + 2.0 ** -24)
+
+
 # ------------------------------------------------------------------- norms --
 @pytest.mark.parametrize("pairs", [False, True], ids=["halves", "pairs"])
 @pytest.mark.parametrize("D,rot", [(128, 128), (80, 48), (256, 0)])
