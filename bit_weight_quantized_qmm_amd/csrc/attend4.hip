@@ -206,9 +206,11 @@ __device__ __forceinline__ int4_t places4(uint32_t w)
 // up the l-th half of the next 32 blocks, and its place goes to scalar registers
 // when its turn comes.  Other page sizes: a lane's key by its own page, two blocks a lookup; where
 // a page holds a cache line or less of a head (SHARED), a sequence's heads run on one L2, whose lines they share.
-// Measured (us): 4 sequences of up to 131071 keys, 8 key heads of 128 for 64, G 128: 96 (5.2
-// TB/s; the loads alone 85; a plain streaming read reaches 7.1); 64 of up to 8192, 32 heads: G 128 65 (4.4; the loads alone
-// 57), G 64 74 (57), G 32 77 (63); one of 513 keys 9.5 (7.4).
+// A value of NaN counts as 0 where rows of the block see different keys, and makes its group NaN for the rows that
+// see it at the end; where all see it the products do that.
+// Measured (us): 4 sequences of up to 131071 keys, 8 key heads of 128 for 64, G 128: 95 to 98 (5.2
+// TB/s; the loads alone 85; a plain streaming read reaches 7.1); 64 of up to 8192, 32 heads: G 128 64 (4.4; the loads alone
+// 57), G 64 70 to 76 (57; cards differ), G 32 76 (63); one of 513 keys 9.5 (7.4).
 // ---------------------------------------------------------------------------
 enum { HALVES, ANY, SHARED };         // PAGES
 __host__ __device__ constexpr int rows4_occupancy(int DP, int GM, int PAGES, int QT)
@@ -919,10 +921,12 @@ __global__ __launch_bounds__(64 * rows4_waves(DP)) __attribute__((amdgpu_waves_p
 // Keys stand in LDS in codes' order within each 8 elements (q's rows do too), values in
 // their own.
 // The matrix instructions and the softmax between them bound it, which share a SIMD's issue: 2 prompts of 4096
-// tokens, 32 heads of 128: 326 us, 842 TFLOP/s of a large product's 1216, matrix instructions in 39 % of the
+// tokens, 32 heads of 128: 321 to 338 us (cards differ), 814 to 857 TFLOP/s of a large product's 1216, matrix instructions in 39 % of the
 // cycles and vector ones in 54 %.  Taking the codes out costs what reading rows of 16 bits does (those: 335
-// us).  Masks as a bit a key (compared key by key: 337; 16 chunks of up to 256 tokens 37.6, now 34.0).  D = 256 has one
-// wave a SIMD (2 chunks of 300 on up to 8192 keys, 16 heads: 230 us, 280 TFLOP/s).
+// us).  Masks as a bit a key (compared key by key 337 on the card of 326; 16 chunks of up to 256 tokens 37.6, now 34.3).  D = 256
+// has one wave a SIMD (2 chunks of 300 on up to 8192 keys, 16 heads: 234 us, 275 TFLOP/s).
+// Values of NaN: rows that do not see them get 0 times NaN too, so a workgroup whose outputs hold NaN goes again, with
+// such values as 0 and a look at each tile's scales for who sees them.  (Looking in the first pass would cost every tile.)
 // ---------------------------------------------------------------------------
 __host__ __device__ constexpr int tiles4_keys(int D) { return D <= 128 ? 64 : 32; }
 __host__ __device__ constexpr int tiles4_waves(int D) { return D <= 128 ? 8 : 4; }
@@ -1435,8 +1439,9 @@ static hipError_t rows4_pick(const Attend4Args &a, hipStream_t st)
     return rows4_go<S, DP, GM, PAGES, 1>(a, st);
 }
 // Groups that leave the codes as they are where they pay: of 64 in rows of 64 and 128, of 128 in rows of 128
-// and 256 (64 users of up to 8192 keys, us, so and as (c - z) s: D 64, G 64: 52 and 59; D 128, G 128: 65 and 75; D 128, G 64: 76 and
-// 80, pages of 100 tokens 78 and 85).  Two tiles of rows with groups of 64 in rows of 128 have not the registers for it (105 and 102).
+// and 256 (64 users of up to 8192 keys, us, so and as (c - z) s: D 64, G 64: 49 and 57; D 128, G 128: 64 and 73, two tiles of rows
+// 98 and 104; D 128, G 64: 76 and 80, pages of 100 tokens 79 and 83; D 256, G 128, up to 4096 keys: 83 and 92).  Two tiles of rows
+// with groups of 64 in rows of 128 have not the registers for it (105 and 102).
 template <typename S, int DP, int PAGES>
 static hipError_t rows4_by_group(const Attend4Args &a, hipStream_t st)
 {
