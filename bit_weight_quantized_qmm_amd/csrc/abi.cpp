@@ -428,7 +428,7 @@ qmm_status qmm_qk_norm(const qmm_qk_norm_args *p, qmm_stream stream)
     a.q_ts = p->q_stride[0], a.q_hs = p->q_stride[1], a.k_ts = p->k_stride[0], a.k_hs = p->k_stride[1];
     a.qo_ts = p->q_out_stride[0], a.qo_hs = p->q_out_stride[1], a.ko_ts = p->k_out_stride[0], a.ko_hs = p->k_out_stride[1];
     a.T = (int)p->T, a.Hq = (int)p->Hq, a.Hk = (int)p->Hkv, a.D = (int)p->D, a.rot = (int)p->rot, a.table_rows = (int)p->table_rows;
-    a.eps = (float)p->eps, a.pairs = p->pairs != 0;
+    a.eps = p->eps, a.pairs = p->pairs != 0;
     const bool vec = even_rows({{p->Hq ? p->q : nullptr, p->q_stride}, {p->Hkv ? p->k : nullptr, p->k_stride}, {p->Hq ? p->q_out : nullptr, p->q_out_stride},
                                 {p->Hkv ? p->k_out : nullptr, p->k_out_stride}});
     return hip_status(qmm::launch_heads(a, p->dtype == QMM_BF16, vec, false, (hipStream_t)stream), fn);
@@ -457,7 +457,7 @@ qmm_status qmm_kv4_append(const qmm_kv4_append_args *p, qmm_stream stream)
     a.kc_ps = c.k_stride[0], a.kc_hs = c.k_stride[1], a.kc_ts = c.k_stride[2], a.vc_ps = c.v_stride[0], a.vc_hs = c.v_stride[1], a.vc_ts = c.v_stride[2];
     a.ks_ps = c.k_scale_stride[0], a.ks_hs = c.k_scale_stride[1], a.vs_ps = c.v_scale_stride[0], a.vs_hs = c.v_scale_stride[1];
     a.T = (int)p->T, a.Hq = (int)p->Hq, a.Hk = 0, a.Hkv = (int)c.Hkv, a.D = (int)c.D, a.G = (int)c.G, a.rot = (int)p->rot;
-    a.page = (int)c.page, a.pages = (int)c.pages, a.table_rows = (int)p->table_rows, a.eps = (float)p->eps, a.pairs = p->pairs != 0;
+    a.page = (int)c.page, a.pages = (int)c.pages, a.table_rows = (int)p->table_rows, a.eps = p->eps, a.pairs = p->pairs != 0;
     const bool vec = even_rows({{p->k, p->k_stride}, {p->v, p->v_stride}, {p->Hq ? p->q : nullptr, p->q_stride}, {p->Hq ? p->out : nullptr, p->out_stride}});
     return hip_status(qmm::launch_heads(a, p->dtype == QMM_BF16, vec, true, (hipStream_t)stream), fn);
 }

@@ -105,7 +105,7 @@ __device__ __forceinline__ double quotient(double x, double s, double inv)
 // once.  As in append.hip a lane owns two vectors of 8 elements that turn
 // together (past rot two that stay), of HP heads of one token, so that cos and
 // sin are read once for them; U lanes own a row, and the sum of its squares goes
-// round them (in fp64 where a row of bf16 has squares beyond fp32).  8192 tokens of 64 + 8
+// round them (of smaller or larger numbers where it leaves fp32).  8192 tokens of 64 + 8
 // heads of 128, bf16: 59 us, 5.2 TB/s (a large copy the same); 1 token 4.2, the call.
 // ---------------------------------------------------------------------------
 template <typename S, bool PAIRS, bool VEC, int U, int HP>
@@ -162,24 +162,28 @@ __device__ __forceinline__ void turn_rows(const HeadsArgs &a, int block, int gro
             for (int e = 0; e < 8; ++e) sum += x[0][e] * x[0][e] + x[1][e] * x[1][e];
 #pragma unroll
             for (int m = 1; m < U; m <<= 1) sum += __shfl_xor(sum, m);
-            const float mean = sum / (float)a.D + a.eps;
-            float r = 1.f / sqrtf(mean);
-            if constexpr (__is_same(S, bf16_t)) {
-                if (__any(!(mean > 0x1p-100f && mean < 0x1p112f))) {      // squares outside fp32's range, or rows of zeros
-                    double far = 0.0;
+            float mean = sum / (float)a.D + (float)a.eps;
+            if (__any(!(mean > 0x1p-100f && mean < 0x1p112f))) {
+                // squares (or eps) outside fp32's range: the same of x 2^-up and eps 4^-up, the larger about 1
+                float top = 0.f;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) far += (double)x[0][e] * (double)x[0][e] + (double)x[1][e] * (double)x[1][e];
+                for (int e = 0; e < 8; ++e) top = fmaxf(top, fmaxf(fabsf(x[0][e]), fabsf(x[1][e])));
 #pragma unroll
-                    for (int m = 1; m < U; m <<= 1) far += __shfl_xor(far, m);
-                    far = 1.0 / sqrt(far / (double)a.D + (double)a.eps);
+                for (int m = 1; m < U; m <<= 1) top = fmaxf(top, __shfl_xor(top, m));
+                const int half = a.eps > 0.0 ? (__builtin_amdgcn_frexp_exp(a.eps) + 1) >> 1 : -1000;
+                const int up = top > 0.f ? max(__builtin_amdgcn_frexp_expf(top), half) : half;
+                sum = 0.f;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        x[0][e] = (float)((double)x[0][e] * far);
-                        x[1][e] = (float)((double)x[1][e] * far);
-                    }
-                    r = 1.f;
+                for (int e = 0; e < 8; ++e) {
+                    x[0][e] = ldexpf(x[0][e], -up);
+                    x[1][e] = ldexpf(x[1][e], -up);
+                    sum += x[0][e] * x[0][e] + x[1][e] * x[1][e];
                 }
+#pragma unroll
+                for (int m = 1; m < U; m <<= 1) sum += __shfl_xor(sum, m);
+                mean = sum / (float)a.D + (float)ldexp(a.eps, -2 * up);
             }
+            const float r = 1.f / sqrtf(mean);
             if (live) {
                 S wa[8], wb[8];
                 load_weights(w + first, wa);
@@ -255,9 +259,9 @@ __device__ __forceinline__ float round_lanes(float x, int span, F f)
 }
 
 // The row's elements after norm and rotation in fp32.  Returns a bound of what its roundings move any of
-// this lane's 8 by, 16 of 2^-24 of |x| + |y|; infinity where the sum of squares leaves fp32's range.  They are 12.5 at
+// this lane's 8 by, 16 of 2^-24 of |x| + |y|; infinity where the sum of squares leaves fp32's range.  They are 12.75 at
 // most: 8 + log2(LN) <= 13 of the sum, as the lanes add it (eight in a row, then a tree: another order needs another
-// bound), a division and eps, halved by the root; root, reciprocal; 2 of the rotation; the product.  (w x is exact.)
+// bound), a division, eps and its rounding, halved by the root; root, reciprocal; 2 of the rotation; the product.  (w x is exact.)
 template <int LN, typename S>
 __device__ __forceinline__ float turned8(const HeadsArgs &a, const Row4<S> &r, float (&x)[8])
 {
@@ -270,7 +274,7 @@ __device__ __forceinline__ float turned8(const HeadsArgs &a, const Row4<S> &r, f
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum = fmaf(x[i], x[i], sum);
         sum = round_lanes(sum, LN, [](float p, float q) { return p + q; });
-        const float mean = sum / (float)a.D + a.eps;
+        const float mean = sum / (float)a.D + (float)a.eps;
         in_range = mean > 0x1p-100f && mean < 0x1p112f;
         root = 1.f / sqrtf(mean);
 #pragma unroll
@@ -315,7 +319,7 @@ __device__ __forceinline__ void turned8(const HeadsArgs &a, const Row4<S> &r, do
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum += (double)to_f32(r.own[i]) * (double)to_f32(r.own[i]);
         for (int m = 1; m < LN; m <<= 1) sum += __shfl_xor(sum, m);
-        root = 1.0 / sqrt(sum / (double)a.D + (double)a.eps);
+        root = 1.0 / sqrt(sum / (double)a.D + a.eps);
     }
     auto scaled = [&](S v, S w) { return r.norm ? (double)to_f32(v) * (double)to_f32(w) * root : (double)to_f32(v); };
 #pragma unroll

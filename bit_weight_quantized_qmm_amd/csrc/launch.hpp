@@ -115,7 +115,7 @@ struct HeadsArgs {
     int T, Hq, Hk, Hkv, D, G, rot, page, pages, table_rows;   // Hk: heads of k that go to k_out
     int put_blocks;                       // workgroups that store k and v; one in by_period.d is one (set by the launcher)
     Divisor by_period, by_page, by_G;
-    float eps;
+    double eps;
     bool pairs;
 };
 

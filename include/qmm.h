@@ -428,8 +428,8 @@ typedef struct qmm_qk_norm_args {
  * every token and head
  *     y = x / sqrt(mean(x^2) + eps) * weight,
  * then each pair (a, b) of y's first rot elements becomes (a cos - b sin, b cos +
- * a sin).  fp32 arithmetic (the sum of squares too, and in fp64 where that leaves
- * fp32's range), rounded once.  What it writes can go to qmm_kv_append (without a
+ * a sin).  fp32 arithmetic (the sum of squares too, by a power of two where that
+ * leaves fp32's range), rounded once.  What it writes can go to qmm_kv_append (without a
  * table) and qmm_paged_attention.
  *   args   HOST struct, read during the call only
  * rot may be 0 (positions and rope NULL).  T = 0 does nothing.

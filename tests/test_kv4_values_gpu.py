@@ -231,6 +231,43 @@ def test_norms_of_rows_of_any_size(q, size, eps, D, rot, pairs):
         assert same(q.kv4_append(xq, xk, v, c, place(70, 8, 16, g), pos, table, pairs, w, u, eps), yq)
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("by", [-0.25, 0.0, 0.25])
+def test_append_takes_eps_as_it_is(q, dtype, by):
+    """Keys whose quotients are ties if eps is rounded to fp32, and 2^-28 beside them by the formula."""
+    D = 128
+    k = ((torch.arange(D, device=DEV) % 31) / 2 * 2.0 ** -12).to(dtype).expand(5, 3, D).contiguous()
+    k[1] *= -1
+    mean = float(k[0, 0].double().square().mean())
+    eps = 2.0 ** -16 - mean                                          # a number of fp32; the root is then 2^-8
+    assert float(torch.tensor(eps, dtype=torch.float32)) == eps
+    eps += by * 2.0 ** (math.frexp(eps)[1] - 24)                     # a quarter of its step beside it
+    w, slots = torch.ones(D, device=DEV).to(dtype), torch.arange(5, device=DEV)
+    c = q.kv4_cache(1, 3, 16, D)
+    before = q.KV4Cache(*(t.clone() for t in c))
+    v = torch.zeros_like(k)
+    q.kv4_append(None, k, v, c, slots, k_norm=w, eps=eps)
+    want, _, _ = encoded(turned(k, w, eps, None, None, False)[0], D)
+    ties, _, _ = encoded(k.double(), D)
+    assert by == 0 or not torch.equal(want, ties)
+    check_stored(c, before, turned(k, w, eps, None, None, False)[0], v.double(), slots, D)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("eps", [1e-50, 1e-310])
+def test_norms_with_eps_below_fp32(q, dtype, eps):
+    """Rows of zeros stay zeros under any eps, however small."""
+    x = torch.randn(4, 2, 64, generator=gen(1), device=DEV).to(dtype)
+    x[2] = 0
+    w = torch.ones(64, device=DEV).to(dtype)
+    c = q.kv4_cache(1, 2, 16, 64)
+    before = q.KV4Cache(*(t.clone() for t in c))
+    y = q.kv4_append(x, x, x, c, torch.arange(4, device=DEV), q_norm=w, k_norm=w, eps=eps)
+    want, most = turned(x, w, eps, None, None, False)
+    close(y, want, norm_bound(want, most, 64, dtype))
+    check_stored(c, before, want, x.double(), torch.arange(4, device=DEV), 64)
+
+
 # ------------------------------------------------------------ run together --
 def test_decoder_layer_example_on_its_cache(q):
     """The example's last output against the layer in fp32 on what the cache of 4 bits holds: the roundings of its 16-bit
